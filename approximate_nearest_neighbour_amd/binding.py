@@ -73,7 +73,10 @@ EXPORTS = ("ivfpq_validate_index_file", "ivfpq_validate_host_index", "ivfpq_load
            "ivfpq_profile_begin",
            "ivfpq_profile_end", "ivfpq_flat_load_bf16", "ivfpq_flat_free",
            "ivfpq_flat_search_bf16_ex", "ivfpq_flat_search_bf16", "ivfpq_flat_profile_begin",
-           "ivfpq_flat_profile_end", "ivfpq_stream_read", "ivfpq_last_error",
+           "ivfpq_flat_profile_end", "ivfpq_mx4_quantize_ex", "ivfpq_mx4_dequantize_ex",
+           "ivfpq_mx4_product_ex", "ivfpq_mx4_list_product_ex", "ivfpq_route_sort_bytes",
+           "ivfpq_route_sort_ex", "ivfpq_route_gather_ex", "ivfpq_route_combine_ex",
+           "ivfpq_route_combine_grad_ex", "ivfpq_stream_read", "ivfpq_last_error",
            "ivfpq_status_string")
 
 _lib = None
@@ -114,6 +117,16 @@ def lib():
             "ivfpq_flat_search_bf16": ([P, P, i64, i32, P, P], st),
             "ivfpq_flat_profile_begin": ([P, i32], st),
             "ivfpq_flat_profile_end": ([P, P], st),
+            "ivfpq_mx4_quantize_ex": ([P, i32, i64, i32, i64, P, P, P], st),
+            "ivfpq_mx4_dequantize_ex": ([P, P, i64, i32, i32, P, P], st),
+            "ivfpq_mx4_product_ex": ([P, P, i64, P, P, i64, i32, i32, P, P], st),
+            "ivfpq_mx4_list_product_ex": ([P, P, i64, P, P, i32, i64, i32, P, P, i32, i64, i32, P,
+                                           P], st),
+            "ivfpq_route_sort_bytes": ([i64, i32, i32], ctypes.c_size_t),
+            "ivfpq_route_sort_ex": ([P, i64, i32, i32, P, ctypes.c_size_t, P, P, P, P], st),
+            "ivfpq_route_gather_ex": ([P, i32, i64, i32, P, P, i32, P, P], st),
+            "ivfpq_route_combine_ex": ([P, i32, i64, i32, P, P, i32, P, P], st),
+            "ivfpq_route_combine_grad_ex": ([P, P, i32, i64, i32, P, P, P, i32, P, P, P], st),
             "ivfpq_stream_read": ([P, ctypes.c_size_t, P, i32, P], st),
             "ivfpq_last_error": ([], ctypes.c_char_p),
             "ivfpq_status_string": ([i32], ctypes.c_char_p),
@@ -406,6 +419,217 @@ def ivfpq_profile_end(index: Index) -> dict:
     t = Timings()
     _check(lib().ivfpq_profile_end(index.handle, ctypes.byref(t)))
     return {f: getattr(t, f) for f, _ in Timings._fields_ if f != "reserved"}
+
+
+# ---------------------------------------------------------------------------
+# 4-bit rows, their products, and vectors sorted by list
+# ---------------------------------------------------------------------------
+
+TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _row_type(dtype) -> int:
+    if dtype not in TYPES:
+        raise ValueError("expected float32, bfloat16 or float16")
+    return TYPES[dtype]
+
+
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    _row_type(t.dtype)
+    _dev(t, t.dtype)
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError("expected rows [n, d] with d >= 1")
+    return t
+
+
+def _ptr(t) -> ctypes.c_void_p:
+    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+
+
+def _out(out, shape, dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"expected an output of shape {tuple(shape)}")
+    return _dev(out, dtype)
+
+
+def _mx4(pair, dims: int):
+    codes, scales = pair
+    _dev(codes, torch.uint8)
+    _dev(scales, torch.uint8)
+    if codes.dim() != dims or codes.shape[:-1] != scales.shape[:-1] or scales.dim() != dims or \
+            codes.shape[-1] != 16 * scales.shape[-1] or scales.shape[-1] < 1:
+        raise ValueError("expected 4-bit rows: codes [..., n, 16 kb] and scales [..., n, kb]")
+    return codes, scales
+
+
+def ivfpq_mx4_quantize_ex(x: torch.Tensor, out=None, stream=None):
+    """Rows [n, d] (float32, bfloat16 or float16; a view with contiguous rows
+    will do) to microscaled 4-bit rows: (codes [n, 16 kb] uint8, scales [n, kb]
+    uint8), kb = ceil(d / 32)."""
+    kind = _row_type(x.dtype)
+    if not x.is_cuda or x.dim() != 2 or x.shape[1] < 1 or \
+            (x.shape[1] > 1 and x.stride(1) != 1) or x.stride(0) < 0:
+        raise ValueError("expected device rows [n, d], d >= 1, each row contiguous")
+    n, d = x.shape
+    kb = (d + 31) // 32
+    codes, scales = (None, None) if out is None else out
+    codes = _out(codes, (n, 16 * kb), torch.uint8, x.device)
+    scales = _out(scales, (n, kb), torch.uint8, x.device)
+    _check(lib().ivfpq_mx4_quantize_ex(_ptr(x), kind, n, d, x.stride(0), _ptr(codes),
+                                       _ptr(scales), _stream_ptr(stream)))
+    return codes, scales
+
+
+def ivfpq_mx4_dequantize_ex(codes: torch.Tensor, scales: torch.Tensor, d: int,
+                            dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
+    """The values [n, d] that 4-bit rows stand for."""
+    kind = _row_type(dtype)
+    codes, scales = _mx4((codes, scales), 2)
+    if d < 1 or (d + 31) // 32 != scales.shape[1]:
+        raise ValueError("d does not fit the rows' blocks")
+    out = _out(out, (codes.shape[0], d), dtype, codes.device)
+    _check(lib().ivfpq_mx4_dequantize_ex(_ptr(codes), _ptr(scales), codes.shape[0], d, kind,
+                                         _ptr(out), _stream_ptr(stream)))
+    return out
+
+
+def ivfpq_mx4_product_ex(a, b, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
+    """A B^T of 4-bit rows a = (codes, scales) of [m, d] and b of [n, d]:
+    [m, n] of dtype, summed in float32."""
+    kind = _row_type(dtype)
+    (ac, as_), (bc, bs) = _mx4(a, 2), _mx4(b, 2)
+    if as_.shape[1] != bs.shape[1]:
+        raise ValueError("the operands' rows have different lengths")
+    m, n = ac.shape[0], bc.shape[0]
+    out = _out(out, (m, n), dtype, ac.device)
+    _check(lib().ivfpq_mx4_product_ex(_ptr(ac), _ptr(as_), m, _ptr(bc), _ptr(bs), n,
+                                      32 * as_.shape[1], kind, _ptr(out), _stream_ptr(stream)))
+    return out
+
+
+def ivfpq_mx4_list_product_ex(a, b, offsets: torch.Tensor, order: torch.Tensor = None, k: int = 1,
+                              dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
+    """Rows sorted by list times their list's matrix: b = (codes [nlist, n,
+    16 kb], scales [nlist, n, kb]), offsets [nlist + 1] int32.  With order
+    ([rows] int32, of ivfpq_route_sort_ex) output row p takes row order[p] // k
+    of a, without it row p.  Returns [rows, n] of dtype, zero past
+    offsets[nlist]."""
+    kind = _row_type(dtype)
+    (ac, as_), (bc, bs) = _mx4(a, 2), _mx4(b, 3)
+    offsets = _dev(offsets, torch.int32)
+    nlist, n = bc.shape[:2]
+    if as_.shape[1] != bs.shape[2]:
+        raise ValueError("the operands' rows have different lengths")
+    if offsets.shape != (nlist + 1,):
+        raise ValueError("expected offsets [nlist + 1]")
+    if order is not None and _dev(order, torch.int32).dim() != 1:
+        raise ValueError("expected order [rows]")
+    rows = ac.shape[0] if order is None else order.shape[0]
+    out = _out(out, (rows, n), dtype, ac.device)
+    _check(lib().ivfpq_mx4_list_product_ex(_ptr(ac), _ptr(as_), ac.shape[0], _ptr(bc), _ptr(bs),
+                                           nlist, n, 32 * as_.shape[1], _ptr(offsets),
+                                           _ptr(order), k, rows, kind, _ptr(out),
+                                           _stream_ptr(stream)))
+    return out
+
+
+def ivfpq_route_sort_bytes(nvec: int, k: int, nlist: int) -> int:
+    return lib().ivfpq_route_sort_bytes(nvec, k, nlist)
+
+
+def ivfpq_route_sort_ex(lists: torch.Tensor, nlist: int, out=None, workspace=None, stream=None):
+    """(vector, list) pairs sorted by list, stable: lists [nvec, k] int32 (outside
+    [0, nlist): masked) -> (offsets [nlist + 1], order [nvec k], pos [nvec, k]),
+    all int32.  workspace: uint8 device tensor of ivfpq_route_sort_bytes."""
+    lists = _dev(lists, torch.int32)
+    if lists.dim() != 2 or lists.shape[1] < 1:
+        raise ValueError("expected lists [nvec, k], k >= 1")
+    nvec, k = lists.shape
+    offsets, order, pos = (None, None, None) if out is None else out
+    if nlist < 1:
+        raise ValueError("nlist must be at least 1")
+    offsets = _out(offsets, (nlist + 1,), torch.int32, lists.device)
+    order = _out(order, (nvec * k,), torch.int32, lists.device)
+    pos = _out(pos, (nvec, k), torch.int32, lists.device)
+    if workspace is None:
+        workspace = torch.empty(max(16, ivfpq_route_sort_bytes(nvec, k, nlist)),
+                                dtype=torch.uint8, device=lists.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    _dev(workspace, torch.uint8)
+    _check(lib().ivfpq_route_sort_ex(_ptr(lists), nvec, k, nlist, _ptr(workspace),
+                                     workspace.numel(), _ptr(offsets), _ptr(order), _ptr(pos),
+                                     _stream_ptr(stream)))
+    return offsets, order, pos
+
+
+def _slots(t: torch.Tensor, dims: int, what: str) -> torch.Tensor:
+    if _dev(t, torch.int32).dim() != dims:
+        raise ValueError(f"expected {what}")
+    return t
+
+
+def _slot_weights(weights, nvec: int, k: int):
+    if weights is not None and _dev(weights, torch.float32).shape != (nvec, k):
+        raise ValueError("expected weights [nvec, k]")
+    return weights
+
+
+def ivfpq_route_gather_ex(x: torch.Tensor, order: torch.Tensor, k: int,
+                          weights: torch.Tensor = None, out=None, stream=None) -> torch.Tensor:
+    """Row p = x[order[p] // k] (times weights[order[p]]), zero where order is -1:
+    [nvec k, d] from x [nvec, d].  Its gradient with respect to x is
+    ivfpq_route_combine_ex of the rows' gradient."""
+    x = _rows(x)
+    nvec, d = x.shape
+    if k < 1 or _slots(order, 1, "order [nvec k]").shape[0] != nvec * k:
+        raise ValueError("expected order [nvec k], k >= 1")
+    weights = _slot_weights(weights, nvec, k)
+    out = _out(out, (nvec * k, d), x.dtype, x.device)
+    _check(lib().ivfpq_route_gather_ex(_ptr(x), _row_type(x.dtype), nvec, d, _ptr(order),
+                                       _ptr(weights), k, _ptr(out), _stream_ptr(stream)))
+    return out
+
+
+def ivfpq_route_combine_ex(rows: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor = None,
+                           out=None, stream=None) -> torch.Tensor:
+    """y[t] = sum_j weights[t, j] rows[pos[t, j]] (weights 1 without them), masked
+    slots (pos -1) skipped: [nvec, d] from rows [nvec k, d]."""
+    rows = _rows(rows)
+    nvec, k = _slots(pos, 2, "pos [nvec, k]").shape
+    if k < 1 or rows.shape[0] != nvec * k:
+        raise ValueError("expected rows [nvec k, d] and pos [nvec, k]")
+    weights = _slot_weights(weights, nvec, k)
+    out = _out(out, (nvec, rows.shape[1]), rows.dtype, rows.device)
+    _check(lib().ivfpq_route_combine_ex(_ptr(rows), _row_type(rows.dtype), nvec, rows.shape[1],
+                                        _ptr(pos), _ptr(weights), k, _ptr(out),
+                                        _stream_ptr(stream)))
+    return out
+
+
+def ivfpq_route_combine_grad_ex(grad: torch.Tensor, rows: torch.Tensor, order: torch.Tensor,
+                                pos: torch.Tensor, weights: torch.Tensor, out=None, stream=None):
+    """Gradients of ivfpq_route_combine_ex(rows, pos, weights) for the output
+    gradient grad [nvec, d]: (of rows [nvec k, d], of weights [nvec, k] float32)."""
+    rows, grad = _rows(rows), _rows(grad)
+    nvec, k = _slots(pos, 2, "pos [nvec, k]").shape
+    d = rows.shape[1]
+    if k < 1 or rows.shape[0] != nvec * k or grad.shape != (nvec, d) or grad.dtype != rows.dtype:
+        raise ValueError("expected grad [nvec, d], rows [nvec k, d] of its type and pos [nvec, k]")
+    if _slots(order, 1, "order [nvec k]").shape[0] != nvec * k:
+        raise ValueError("expected order [nvec k]")
+    if weights is None:
+        raise ValueError("expected weights [nvec, k]")
+    weights = _slot_weights(weights, nvec, k)
+    d_rows, d_weights = (None, None) if out is None else out
+    d_rows = _out(d_rows, (nvec * k, d), rows.dtype, rows.device)
+    d_weights = _out(d_weights, (nvec, k), torch.float32, rows.device)
+    _check(lib().ivfpq_route_combine_grad_ex(_ptr(grad), _ptr(rows), _row_type(rows.dtype), nvec,
+                                             d, _ptr(order), _ptr(pos), _ptr(weights), k,
+                                             _ptr(d_rows), _ptr(d_weights), _stream_ptr(stream)))
+    return d_rows, d_weights
 
 
 # ---------------------------------------------------------------------------

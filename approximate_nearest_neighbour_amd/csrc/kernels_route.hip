@@ -1,0 +1,444 @@
+// Vectors sorted by list and back: a stable sort of (vector, list) pairs by
+// list, rows gathered in that order, and rows in that order summed back to
+// their vectors with weights; and the gradients of both.
+//
+// Slot u = t k + j is pair j of vector t.  The sort gives every kept slot a
+// position p; order[p] is the slot at p (-1 past the kept ones) and pos[u] the
+// position of slot u (-1 for a slot without a list).
+#include "common.hpp"
+#include "internal.hpp"
+#include "rows.hpp"
+
+namespace ivfpq {
+
+// ---------------------------------------------------------------------------
+// stable sort by list
+// ---------------------------------------------------------------------------
+
+constexpr int kSortWaves = 4;
+constexpr int kSortChunk = 2048; // slots of one workgroup
+constexpr int kSortBits = 11;    // bits of one pass
+constexpr int kSortBins = 1 << kSortBits;
+
+// The sort key of a slot: its list, or nlist when it has none.
+__device__ __forceinline__ uint32_t list_key(const int32_t *lists, uint32_t u, uint32_t nlist)
+{
+    const uint32_t l = (uint32_t)lists[u];
+    return l < nlist ? l : nlist;
+}
+
+struct SortPass {
+    const int32_t *lists;   // first pass: the lists themselves
+    const uint32_t *key_in; // later passes: keys and slots of the pass before
+    const uint32_t *slot_in;
+    uint32_t n, nlist, shift, bins, blocks;
+    uint32_t *hist;  // [bins][blocks], then the exclusive sums along a bin
+    uint32_t *total; // [bins]
+    uint32_t *key_out, *slot_out; // nullptr in the last pass of a single-pass sort
+    int32_t *offsets, *order, *pos; // of the last pass (offsets: single-pass sort only)
+
+    __device__ __forceinline__ uint32_t key(uint32_t i) const
+    {
+        return key_in ? key_in[i] : list_key(lists, i, nlist);
+    }
+    __device__ __forceinline__ uint32_t bin(uint32_t k) const
+    {
+        return (k >> shift) & (kSortBins - 1);
+    }
+};
+
+// Counts of one workgroup's chunk by bin.
+__global__ __launch_bounds__(64 * kSortWaves) void route_count_kernel(SortPass s)
+{
+    __shared__ uint32_t count[kSortBins];
+    for (uint32_t b = threadIdx.x; b < s.bins; b += blockDim.x)
+        count[b] = 0;
+    __syncthreads();
+    const uint32_t first = blockIdx.x * (uint32_t)kSortChunk;
+    const uint32_t end = min(first + (uint32_t)kSortChunk, s.n);
+    for (uint32_t i = first + threadIdx.x; i < end; i += blockDim.x)
+        atomicAdd(&count[s.bin(s.key(i))], 1u);
+    __syncthreads();
+    for (uint32_t b = threadIdx.x; b < s.bins; b += blockDim.x)
+        s.hist[(size_t)b * s.blocks + blockIdx.x] = count[b];
+}
+
+// Exclusive sums of a bin's counts along the workgroups, one wave a bin.
+__global__ __launch_bounds__(256) void route_scan_kernel(SortPass s)
+{
+    const uint32_t b = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (b >= s.bins)
+        return;
+    const int lane = lane_id();
+    uint32_t *h = s.hist + (size_t)b * s.blocks;
+    uint32_t base = 0;
+    for (uint32_t i0 = 0; i0 < s.blocks; i0 += 64) {
+        const uint32_t v = i0 + lane < s.blocks ? h[i0 + lane] : 0;
+        const uint32_t upto = wave_inclusive_sum(v);
+        if (i0 + lane < s.blocks)
+            h[i0 + lane] = base + upto - v;
+        base += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+    }
+    if (lane == 0)
+        s.total[b] = base;
+}
+
+// Every slot to its place: start of its bin, plus the bin's slots of earlier
+// workgroups, of earlier waves of this one (each wave has a contiguous part of
+// the chunk) and of earlier lanes.
+__global__ __launch_bounds__(64 * kSortWaves) void route_scatter_kernel(SortPass s)
+{
+    __shared__ uint32_t at[kSortWaves][kSortBins];
+    __shared__ uint32_t sums[kSortWaves];
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    for (uint32_t b = threadIdx.x; b < s.bins; b += blockDim.x)
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w)
+            at[w][b] = 0;
+    __syncthreads();
+    constexpr uint32_t kPart = kSortChunk / kSortWaves;
+    const uint32_t first = min(blockIdx.x * (uint32_t)kSortChunk + wave * kPart, s.n);
+    const uint32_t end = min(first + kPart, s.n);
+    for (uint32_t i = first + lane; i < end; i += 64)
+        atomicAdd(&at[wave][s.bin(s.key(i))], 1u);
+    __syncthreads();
+    // bins in order, 256 at a time: exclusive sums of the totals
+    uint32_t base = 0;
+    for (uint32_t b0 = 0; b0 < s.bins; b0 += 64 * kSortWaves) {
+        const uint32_t b = b0 + threadIdx.x;
+        const uint32_t v = b < s.bins ? s.total[b] : 0;
+        const uint32_t upto = wave_inclusive_sum(v);
+        if (lane == 63)
+            sums[wave] = upto;
+        __syncthreads();
+        uint32_t start = base + upto - v;
+        uint32_t all = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+            start += w < wave ? sums[w] : 0;
+            all += sums[w];
+        }
+        base += all;
+        if (b < s.bins) {
+            if (s.offsets && blockIdx.x == 0)
+                s.offsets[b] = (int32_t)start;
+            start += s.hist[(size_t)b * s.blocks + blockIdx.x];
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) {
+                const uint32_t c = at[w][b];
+                at[w][b] = start;
+                start += c;
+            }
+        }
+        __syncthreads();
+    }
+    int bits = 0;
+    while ((1u << bits) < s.bins)
+        ++bits;
+    for (uint32_t i0 = first; i0 < end; i0 += 64) {
+        const uint32_t i = i0 + lane;
+        const bool live = i < end;
+        const uint32_t key = live ? s.key(i) : 0;
+        const uint32_t bin = s.bin(key);
+        uint64_t same = __ballot(live);
+        for (int q = 0; q < bits; ++q) {
+            const uint64_t m = __ballot((bin >> q) & 1);
+            same &= (bin >> q) & 1 ? m : ~m;
+        }
+        if (live) {
+            const uint32_t before = (uint32_t)__popcll(same & ((1ull << lane) - 1));
+            const uint32_t p = at[wave][bin] + before;
+            const uint32_t u = s.slot_in ? s.slot_in[i] : i;
+            if (s.slot_out)
+                s.slot_out[p] = u;
+            if (s.key_out)
+                s.key_out[p] = key;
+            if (s.order) {
+                s.order[p] = key < s.nlist ? (int32_t)u : -1;
+                s.pos[u] = key < s.nlist ? (int32_t)p : -1;
+            }
+            if ((same >> lane) == 1) // the bin's last lane moves its cursor on
+                at[wave][bin] = p + 1;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); // the cursors, for the next 64
+    }
+}
+
+// List starts of a sort of more than one pass: offsets[l] = keys below l.
+__global__ __launch_bounds__(256) void route_bounds_kernel(const uint32_t *__restrict__ keys,
+                                                           uint32_t n, uint32_t nlist,
+                                                           int32_t *__restrict__ offsets)
+{
+    const uint32_t l = blockIdx.x * 256u + threadIdx.x;
+    if (l > nlist)
+        return;
+    uint32_t lo = 0, hi = n;
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (keys[mid] < l)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    offsets[l] = (int32_t)lo;
+}
+
+static uint32_t sort_blocks(int64_t n)
+{
+    return (uint32_t)((n + kSortChunk - 1) / kSortChunk);
+}
+
+size_t route_sort_bytes(int64_t n, int nlist)
+{
+    const size_t blocks = sort_blocks(n);
+    const size_t bins = nlist < kSortBins ? (size_t)nlist + 1 : (size_t)kSortBins;
+    size_t b = (bins * blocks + bins) * 4;
+    if (nlist >= kSortBins)
+        b += (size_t)n * 4 * 3; // keys and slots after the first pass, keys after the second
+    return b;
+}
+
+hipError_t launch_route_sort(const int32_t *lists, int64_t n, int nlist, void *ws, int32_t *offsets,
+                             int32_t *order, int32_t *pos, hipStream_t stream)
+{
+    SortPass s{};
+    s.lists = lists;
+    s.n = (uint32_t)n;
+    s.nlist = (uint32_t)nlist;
+    s.blocks = sort_blocks(n);
+    const bool two = nlist >= kSortBins;
+    s.bins = two ? kSortBins : (uint32_t)nlist + 1;
+    s.hist = static_cast<uint32_t *>(ws);
+    s.total = s.hist + (size_t)s.bins * s.blocks;
+    uint32_t *keys = s.total + s.bins, *slots = keys + n, *sorted = slots + n;
+    if (n == 0) { // every list is empty
+        hipLaunchKernelGGL(route_bounds_kernel, dim3((unsigned)nlist / 256 + 1), dim3(256), 0,
+                           stream, nullptr, 0u, (uint32_t)nlist, offsets);
+        return hipGetLastError();
+    }
+    for (int pass = 0; pass < (two ? 2 : 1); ++pass) {
+        if (pass == 1) {
+            s.shift = kSortBits;
+            s.bins = ((uint32_t)nlist >> kSortBits) + 1;
+            s.key_in = keys;
+            s.slot_in = slots;
+        }
+        const bool last = pass == (two ? 1 : 0);
+        s.key_out = !two ? nullptr : last ? sorted : keys;
+        s.slot_out = last ? nullptr : slots;
+        s.order = last ? order : nullptr;
+        s.pos = last ? pos : nullptr;
+        s.offsets = two ? nullptr : offsets;
+        hipLaunchKernelGGL(route_count_kernel, dim3(s.blocks), dim3(64 * kSortWaves), 0, stream, s);
+        hipLaunchKernelGGL(route_scan_kernel, dim3((s.bins + 3) / 4), dim3(256), 0, stream, s);
+        hipLaunchKernelGGL(route_scatter_kernel, dim3(s.blocks), dim3(64 * kSortWaves), 0, stream,
+                           s);
+    }
+    if (two)
+        hipLaunchKernelGGL(route_bounds_kernel, dim3((unsigned)nlist / 256 + 1), dim3(256), 0,
+                           stream, sorted, (uint32_t)n, (uint32_t)nlist, offsets);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// rows there and back
+// ---------------------------------------------------------------------------
+
+// Lanes that share a row: enough for one 16-byte piece each, at most a wave.
+template <typename T>
+static int row_lanes(int d)
+{
+    const int pieces = (d + Piece<T>::N - 1) / Piece<T>::N;
+    int l = 1;
+    while (l < pieces && l < 64)
+        l *= 2;
+    return l;
+}
+
+// rows[p] = w x[t] of the slot at p, zero where no slot is.
+template <typename T>
+__global__ __launch_bounds__(256) void route_gather_kernel(const T *__restrict__ x, int64_t n,
+                                                           int d, int lanes, FastDiv k,
+                                                           const int32_t *__restrict__ order,
+                                                           const float *__restrict__ weights,
+                                                           T *__restrict__ rows)
+{
+    constexpr int N = Piece<T>::N;
+    const int64_t p = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+    if (p >= n)
+        return;
+    const uint32_t u = (uint32_t)order[p];
+    const bool kept = u < (uint64_t)n;
+    const T *src = x + (kept ? (int64_t)k.div(u) : 0) * d;
+    const float w = kept && weights ? weights[u] : 1.f;
+    for (int c = (threadIdx.x & (lanes - 1)) * N; c < d; c += lanes * N) {
+        Piece<T> v;
+        if (kept)
+            v.load(src + c, d - c);
+        else
+            v.zero();
+        if (weights) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v.v[i] *= w;
+        }
+        v.store(rows + p * d + c, d - c);
+    }
+}
+
+// y[t] = sum over j of w[t][j] rows[pos[t][j]], j ascending in float32,
+// rounded once; slots without a position are skipped.
+template <typename T>
+__global__ __launch_bounds__(256) void route_combine_kernel(const T *__restrict__ rows,
+                                                            int64_t nvec, int d, int lanes, int k,
+                                                            const int32_t *__restrict__ pos,
+                                                            const float *__restrict__ weights,
+                                                            T *__restrict__ out)
+{
+    constexpr int N = Piece<T>::N;
+    const int64_t t = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+    if (t >= nvec)
+        return;
+    const int64_t n = nvec * k;
+    for (int c = (threadIdx.x & (lanes - 1)) * N; c < d; c += lanes * N) {
+        Piece<T> sum;
+        sum.zero();
+        for (int j = 0; j < k; ++j) {
+            const int64_t p = pos[t * k + j];
+            if (p < 0 || p >= n)
+                continue;
+            const float w = weights ? weights[t * k + j] : 1.f;
+            Piece<T> v;
+            v.load(rows + p * d + c, d - c);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                sum.v[i] = fmaf(w, v.v[i], sum.v[i]);
+        }
+        sum.store(out + t * d + c, d - c);
+    }
+}
+
+// Gradient of the weighted sum, a group of lanes a slot: d_rows[p] = w dy[t]
+// and d_weights[slot] = <dy[t], rows[p]>.  The same group also clears row
+// number slot when no slot sits there.
+template <typename T>
+__global__ __launch_bounds__(256) void route_combine_grad_kernel(
+    const T *__restrict__ grad, const T *__restrict__ rows, int64_t n, int d, int lanes, FastDiv k,
+    const int32_t *__restrict__ order, const int32_t *__restrict__ pos,
+    const float *__restrict__ weights, T *__restrict__ d_rows, float *__restrict__ d_weights)
+{
+    constexpr int N = Piece<T>::N;
+    const int64_t u = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+    const int sub = threadIdx.x & (lanes - 1);
+    const int64_t p = u < n ? pos[u] : -1;
+    const bool kept = p >= 0 && p < n;
+    const bool clear = u < n && (uint32_t)order[u] >= (uint64_t)n;
+    const T *dy = grad + (u < n ? (int64_t)k.div((uint32_t)u) : 0) * d;
+    const float w = kept ? weights[u] : 0.f;
+    float dot = 0.f;
+    for (int c = sub * N; c < d; c += lanes * N) {
+        if (kept) {
+            Piece<T> g, r;
+            g.load(dy + c, d - c);
+            r.load(rows + p * d + c, d - c);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                dot = fmaf(g.v[i], r.v[i], dot);
+                g.v[i] *= w;
+            }
+            g.store(d_rows + p * d + c, d - c);
+        }
+        if (clear) {
+            Piece<T> z;
+            z.zero();
+            z.store(d_rows + u * d + c, d - c);
+        }
+    }
+    for (int s = 1; s < lanes; s <<= 1)
+        dot += __uint_as_float((uint32_t)__builtin_amdgcn_ds_bpermute(
+            (lane_id() ^ s) << 2, (int)__float_as_uint(dot)));
+    if (sub == 0 && u < n)
+        d_weights[u] = dot;
+}
+
+static dim3 row_grid(int64_t rows, int lanes)
+{
+    const int64_t per = 256 / lanes;
+    return dim3((unsigned)((rows + per - 1) / per));
+}
+
+template <typename T>
+static hipError_t gather_as(const void *x, int64_t nvec, int d, const int32_t *order,
+                            const float *weights, int k, void *rows, hipStream_t stream)
+{
+    const int lanes = row_lanes<T>(d);
+    hipLaunchKernelGGL(route_gather_kernel<T>, row_grid(nvec * k, lanes), dim3(256), 0, stream,
+                       static_cast<const T *>(x), nvec * k, d, lanes, FastDiv((uint32_t)k), order,
+                       weights, static_cast<T *>(rows));
+    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t combine_as(const void *rows, int64_t nvec, int d, const int32_t *pos,
+                             const float *weights, int k, void *out, hipStream_t stream)
+{
+    const int lanes = row_lanes<T>(d);
+    hipLaunchKernelGGL(route_combine_kernel<T>, row_grid(nvec, lanes), dim3(256), 0, stream,
+                       static_cast<const T *>(rows), nvec, d, lanes, k, pos, weights,
+                       static_cast<T *>(out));
+    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t combine_grad_as(const void *grad, const void *rows, int64_t nvec, int d,
+                                  const int32_t *order, const int32_t *pos, const float *weights,
+                                  int k, void *d_rows, float *d_weights, hipStream_t stream)
+{
+    const int lanes = row_lanes<T>(d);
+    hipLaunchKernelGGL(route_combine_grad_kernel<T>, row_grid(nvec * k, lanes), dim3(256), 0,
+                       stream, static_cast<const T *>(grad), static_cast<const T *>(rows),
+                       nvec * k, d, lanes, FastDiv((uint32_t)k), order, pos, weights,
+                       static_cast<T *>(d_rows), d_weights);
+    return hipGetLastError();
+}
+
+hipError_t launch_route_gather(const void *x, int type, int64_t nvec, int d, const int32_t *order,
+                               const float *weights, int k, void *rows, hipStream_t stream)
+{
+    switch (type) {
+    case kF32: return gather_as<float>(x, nvec, d, order, weights, k, rows, stream);
+    case kBF16: return gather_as<__bf16>(x, nvec, d, order, weights, k, rows, stream);
+    default: return gather_as<_Float16>(x, nvec, d, order, weights, k, rows, stream);
+    }
+}
+
+hipError_t launch_route_combine(const void *rows, int type, int64_t nvec, int d, const int32_t *pos,
+                                const float *weights, int k, void *out, hipStream_t stream)
+{
+    switch (type) {
+    case kF32: return combine_as<float>(rows, nvec, d, pos, weights, k, out, stream);
+    case kBF16: return combine_as<__bf16>(rows, nvec, d, pos, weights, k, out, stream);
+    default: return combine_as<_Float16>(rows, nvec, d, pos, weights, k, out, stream);
+    }
+}
+
+hipError_t launch_route_combine_grad(const void *grad, const void *rows, int type, int64_t nvec,
+                                     int d, const int32_t *order, const int32_t *pos,
+                                     const float *weights, int k, void *d_rows, float *d_weights,
+                                     hipStream_t stream)
+{
+    switch (type) {
+    case kF32:
+        return combine_grad_as<float>(grad, rows, nvec, d, order, pos, weights, k, d_rows,
+                                      d_weights, stream);
+    case kBF16:
+        return combine_grad_as<__bf16>(grad, rows, nvec, d, order, pos, weights, k, d_rows,
+                                       d_weights, stream);
+    default:
+        return combine_grad_as<_Float16>(grad, rows, nvec, d, order, pos, weights, k, d_rows,
+                                         d_weights, stream);
+    }
+}
+
+} // namespace ivfpq

@@ -403,6 +403,115 @@ ivfpq_status ivfpq_flat_search_bf16(const ivfpq_flat *f, const uint16_t *queries
 ivfpq_status ivfpq_flat_profile_begin(ivfpq_flat *f, int max_calls);
 ivfpq_status ivfpq_flat_profile_end(ivfpq_flat *f, ivfpq_flat_timings *out);
 
+/* ---- 4-bit rows and their products --------------------------------------
+ *
+ * Rows of d values in microscaled 4-bit floats (the OCP Microscaling
+ * specification's MXFP4): kb = ceil(d / 32) blocks of 32 values, the last one
+ * padded with zeros; a block is 16 bytes of e2m1 codes (value i in byte i / 2,
+ * the even one in the low nibble; magnitudes 0 .5 1 1.5 2 3 4 6, bit 3 the
+ * sign) and one exponent byte s, and stands for code * 2^(s - 127).  A matrix
+ * of such rows is two arrays: codes [rows][16 kb], 16-byte aligned, and scales
+ * [rows][kb].  s = 255 makes the whole block NaN; unlike the searches, these
+ * calls take infinities and NaN, as described at each. */
+typedef enum { IVFPQ_F32 = 0, IVFPQ_BF16 = 1, IVFPQ_F16 = 2 } ivfpq_type;
+
+/* Rows to 4 bits (device buffers, asynchronous on `stream`): rows_dev holds
+ * `rows` rows of d values of `type`, `stride` values from one row's start to
+ * the next's.  A block's exponent byte is max(0, e - 2), e the float32
+ * exponent field of its largest magnitude; its values are rounded to the
+ * nearest code, halves to even, magnitudes above 6 to 6.  A block that holds
+ * an infinity or a NaN gets s = 255 and zero codes.  rows = 0 is a no-op.
+ * Errors: IVFPQ_E_INVALID_ARG (rows outside [0, 2^31), d outside [1, 2^20],
+ * stride < 0, a bad type, a NULL or misaligned pointer), IVFPQ_E_DEVICE. */
+ivfpq_status ivfpq_mx4_quantize_ex(const void *rows_dev, int type, int64_t rows, int d,
+                                   int64_t stride, uint8_t *codes_dev, uint8_t *scales_dev,
+                                   void *stream);
+
+/* 4-bit rows back to values: out_dev [rows][d] of `type`, rounded to it once
+ * (float32 and bfloat16 hold every value exactly).  Errors as above. */
+ivfpq_status ivfpq_mx4_dequantize_ex(const uint8_t *codes_dev, const uint8_t *scales_dev,
+                                     int64_t rows, int d, int type, void *out_dev, void *stream);
+
+/* out_dev [m][n] = A B^T of A [m][d] and B [n][d], both in 4-bit rows: the
+ * scores of m queries against n database rows, or m activations times a weight
+ * matrix of n rows.  Products on the matrix cores, summed in float32, rounded
+ * once to `type`.  A result with a NaN block on either side is NaN.  m = 0 or
+ * n = 0 is a no-op.  Errors: IVFPQ_E_INVALID_ARG (m or n outside [0, 2^31),
+ * m n >= 2^39, d outside [1, 2^20], a bad type, a NULL or misaligned
+ * pointer), IVFPQ_E_DEVICE. */
+ivfpq_status ivfpq_mx4_product_ex(const uint8_t *a_codes_dev, const uint8_t *a_scales_dev,
+                                  int64_t m, const uint8_t *b_codes_dev,
+                                  const uint8_t *b_scales_dev, int64_t n, int d, int type,
+                                  void *out_dev, void *stream);
+
+/* Rows sorted by list, each times its list's own matrix: B holds nlist
+ * matrices of n rows ([nlist][n] rows), offsets_dev [nlist + 1] int32 the
+ * lists' first rows (ascending, as ivfpq_route_sort_ex writes them; read on
+ * the device).  Output row p of list e (offsets[e] <= p < offsets[e + 1]) is
+ * row order[p] / k of A times matrix e, or row p of A when order_dev is NULL
+ * (then arows >= rows).  Rows from offsets[nlist] to `rows` are zero.  out_dev
+ * [rows][n] of `type`.  An entry of order outside A reads row 0.  Errors as
+ * above, and IVFPQ_E_INVALID_ARG for nlist outside [1, 2^16], k < 1 or
+ * rows n >= 2^38. */
+ivfpq_status ivfpq_mx4_list_product_ex(const uint8_t *a_codes_dev, const uint8_t *a_scales_dev,
+                                       int64_t arows, const uint8_t *b_codes_dev,
+                                       const uint8_t *b_scales_dev, int nlist, int64_t n, int d,
+                                       const int32_t *offsets_dev, const int32_t *order_dev, int k,
+                                       int64_t rows, int type, void *out_dev, void *stream);
+
+/* ---- vectors sorted by list, and back ------------------------------------
+ *
+ * nvec vectors with k lists each (the probes of ivfpq_coarse_ex, or a router's
+ * choices): slot u = t k + j is list j of vector t, n = nvec k < 2^31 slots.
+ * All calls are asynchronous on `stream`, allocate nothing and may be captured
+ * in a graph.  Rows are row-major and contiguous. */
+
+/* Bytes of device workspace for ivfpq_route_sort_ex; 0 for arguments that it
+ * rejects. */
+size_t ivfpq_route_sort_bytes(int64_t nvec, int k, int nlist);
+
+/* Stable sort of the slots by list: offsets_dev [nlist + 1] receives each
+ * list's first position (offsets[nlist]: kept slots), order_dev [n] the slot at
+ * each position, in ascending slot number inside a list (-1 from
+ * offsets[nlist] on), pos_dev [nvec][k] the position of each slot, -1 for a
+ * slot whose list is outside [0, nlist) (a masked one).  The result does not
+ * depend on the run.  Errors: IVFPQ_E_INVALID_ARG (k < 1, n >= 2^31, nlist
+ * outside [1, 2^22), a NULL pointer, a workspace below
+ * ivfpq_route_sort_bytes or not 16-byte aligned), IVFPQ_E_DEVICE. */
+ivfpq_status ivfpq_route_sort_ex(const int32_t *lists_dev, int64_t nvec, int k, int nlist,
+                                 void *workspace_dev, size_t workspace_bytes, int32_t *offsets_dev,
+                                 int32_t *order_dev, int32_t *pos_dev, void *stream);
+
+/* rows_dev [n][d]: row p is vector order[p] / k, times weights[order[p]]
+ * (float32 [nvec][k], rounded once) when weights_dev is not NULL; a row whose
+ * order is outside [0, n) is zero.  Its gradient is ivfpq_route_combine_ex of
+ * the rows' gradient (with the same weights).  Errors: IVFPQ_E_INVALID_ARG
+ * (a bad type, d outside [1, 2^20], k < 1, n >= 2^31, a NULL or misaligned
+ * pointer), IVFPQ_E_DEVICE. */
+ivfpq_status ivfpq_route_gather_ex(const void *vectors_dev, int type, int64_t nvec, int d,
+                                   const int32_t *order_dev, const float *weights_dev, int k,
+                                   void *rows_dev, void *stream);
+
+/* out_dev [nvec][d]: the sum over j of weights[t][j] (1 when weights_dev is
+ * NULL) times row pos[t][j] of rows_dev [n][d], j ascending in float32, rounded
+ * once; slots whose position is outside [0, n) are skipped and their rows never
+ * read.  A vector without kept slots gets zeros.  Errors as above. */
+ivfpq_status ivfpq_route_combine_ex(const void *rows_dev, int type, int64_t nvec, int d,
+                                    const int32_t *pos_dev, const float *weights_dev, int k,
+                                    void *out_dev, void *stream);
+
+/* Gradient of ivfpq_route_combine_ex with weights: grad_dev [nvec][d] is the
+ * gradient of its output; grad_rows_dev [n][d] receives weights[u] times
+ * grad[u / k] at the position of slot u (zero past the kept slots) and
+ * grad_weights_dev [nvec][k] float32 the products <grad[t], rows[pos[t][j]]>
+ * (0 for a slot without a position), summed in float32.  order_dev and pos_dev
+ * are those of one ivfpq_route_sort_ex.  Errors as above. */
+ivfpq_status ivfpq_route_combine_grad_ex(const void *grad_dev, const void *rows_dev, int type,
+                                         int64_t nvec, int d, const int32_t *order_dev,
+                                         const int32_t *pos_dev, const float *weights_dev, int k,
+                                         void *grad_rows_dev, float *grad_weights_dev,
+                                         void *stream);
+
 /* ---- measurement support ---------------------------------------------- */
 
 /* Reference streaming read for the bandwidth roofline (not part of the search
