@@ -279,9 +279,350 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_direct_kernel(Mx4Product p)
             out[i] = (T)acc[i];
 }
 
+// Large tiles.
+//
+// A workgroup of four waves forms a (32 WM) x (32 WN) tile, each wave a
+// quarter of it: WM x WN sums of 16 x 16 in accumulator registers.  A row's
+// blocks come eight at a time (a chunk, 128 bytes of codes), both operands'
+// rows copied from memory into LDS without passing through registers; while
+// the matrix cores work on one chunk the next one arrives in the other half
+// of the LDS.  Inside a chunk the operands of the second half are read from
+// LDS while the first half is multiplied, and those of the next chunk's first
+// half while the second is.
+//
+// Code rows lie in LDS 128 bytes apart, their eight 16-byte blocks permuted by
+// an exclusive or with three bits of the row, so that eight lanes that read
+// the same block of eight rows touch all banks once.  Exponent bytes lie as
+// the lanes want them: the bytes of all of a lane's operands side by side, so
+// that one read brings them and the instruction's byte selector picks.
+//
+// Results of a lane are consecutive columns: four for each sum, or eight over
+// two sums for 16-bit outputs, whose B rows are dealt to the sums accordingly
+// (pair_row); every store is then 16 bytes, 64 side by side.
+
+__device__ const uint32_t kZeroBlock[4] = {0, 0, 0, 0};
+
+__device__ __forceinline__ void copy16_to_lds(const uint8_t *src, uint8_t *lds)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                     (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+}
+
+// The product with the exponent bytes' selectors as run-time values that are
+// constants after unrolling.
+__device__ __forceinline__ f32x4 mfma_mx4_sel(i32x4 a, uint32_t sa, int sel_a, i32x4 b, uint32_t sb,
+                                              int sel_b, f32x4 c)
+{
+#define MX4_CASE(A, B)                                                                             \
+    case A * 4 + B:                                                                                \
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(low_half(a), low_half(b), c, 4, 4, \
+                                                                A, (int)sa, B, (int)sb);
+    switch (sel_a * 4 + sel_b) {
+        MX4_CASE(0, 0) MX4_CASE(0, 1) MX4_CASE(0, 2) MX4_CASE(0, 3)
+        MX4_CASE(1, 0) MX4_CASE(1, 1) MX4_CASE(1, 2) MX4_CASE(1, 3)
+        MX4_CASE(2, 0) MX4_CASE(2, 1) MX4_CASE(2, 2) MX4_CASE(2, 3)
+        MX4_CASE(3, 0) MX4_CASE(3, 1) MX4_CASE(3, 2) MX4_CASE(3, 3)
+    }
+#undef MX4_CASE
+    return c;
+}
+
+// Row of a wave's 16 W that operand row r of sum f holds, and back.  PAIR:
+// rows 32 h + 8 q + 4 o + i for f = 2 h + o, r = 4 q + i.
+template <bool PAIR>
+__device__ __forceinline__ int pair_row(int f, int r)
+{
+    return PAIR ? (f >> 1) * 32 + (r >> 2) * 8 + (f & 1) * 4 + (r & 3) : f * 16 + r;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void pair_row_back(int n, int &f, int &r)
+{
+    f = PAIR ? (n >> 5) * 2 + ((n >> 2) & 1) : n >> 4;
+    r = PAIR ? ((n >> 3) & 3) * 4 + (n & 3) : n & 15;
+}
+
+// The three bits of a row that permute its blocks: different for lanes 0..7
+// (and 8..15) of an operand read.
+template <bool PAIR>
+__device__ __forceinline__ int block_swizzle(int row)
+{
+    return PAIR ? (row & 3) | ((row >> 1) & 4) : row & 7;
+}
+
+// Eight exponent bytes from byte c0 of a row's kb, zero past its end.
+__device__ __forceinline__ uint64_t scale_bytes(const uint8_t *row, int c0, int kb)
+{
+    typedef uint64_t U __attribute__((aligned(1)));
+    if (c0 + 8 <= kb)
+        return *reinterpret_cast<const U *>(row + c0);
+    uint64_t v = 0;
+    for (int i = 0; c0 + i < kb; ++i)
+        v |= (uint64_t)row[c0 + i] << (8 * i);
+    return v;
+}
+
+// W exponent byte pairs of a lane, two a register.
+template <int W>
+struct ScaleRegs {
+    uint32_t v[(W + 1) / 2];
+    __device__ __forceinline__ void read(const uint16_t *p)
+    {
+        if constexpr (W == 8) {
+            const u32x4 t = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = t[i];
+        } else if constexpr (W == 4) {
+            const u32x2 t = *reinterpret_cast<const u32x2 *>(p);
+            v[0] = t[0];
+            v[1] = t[1];
+        } else if constexpr (W == 2) {
+            v[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            v[0] = *p;
+        }
+    }
+};
+
+// Tile numbers: the workgroups of one XCD (every eighth) take a contiguous
+// range of tiles, and that range runs through groups of kGroup tiles along m
+// by all tiles along n, so that tiles in flight together share operands in
+// the XCD's cache.
+constexpr uint32_t kGroup = 8;
+
+__device__ __forceinline__ void tile_of_block(uint32_t mt, uint32_t nt, uint32_t &m, uint32_t &n)
+{
+    const uint32_t all = gridDim.x, x = blockIdx.x & 7, i = blockIdx.x >> 3;
+    const uint32_t per = all >> 3, extra = all & 7;
+    const uint32_t id = x * per + min(x, extra) + i;
+    const uint32_t group = id / (kGroup * nt);
+    const uint32_t first = group * kGroup;
+    const uint32_t rows = min(kGroup, mt - first);
+    const uint32_t in = id - group * kGroup * nt;
+    m = first + in % rows;
+    n = in / rows;
+}
+
+template <typename T, bool LIST, int WM, int WN>
+__global__ __launch_bounds__(256) void mx4_tile_kernel(Mx4Product p, uint32_t mtiles,
+                                                       uint32_t ntiles)
+{
+    constexpr bool PAIR = sizeof(T) == 2;
+    constexpr int TM = 32 * WM, TN = 32 * WN;
+    __shared__ __align__(16) uint8_t code[2][(TM + TN) * 128];
+    __shared__ __align__(16) uint16_t scale[2][(TM + TN) * 4];
+
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    uint32_t mt, nt;
+    tile_of_block(mtiles, ntiles, mt, nt);
+    const int n0 = (int)nt * TN;
+    ListTile tile{0, (int64_t)mt * TM, min((int64_t)mt * TM + TM, p.m)};
+    if constexpr (LIST)
+        tile = find_tile<TM>(p.offsets, p.nlist, p.m, mt);
+    if (tile.p0 >= tile.p1)
+        return;
+    const int wm = wave & 1, wn = wave >> 1;
+    const int r = lane & 15, g = lane >> 4;
+    T *out = static_cast<T *>(p.out);
+
+    f32x4 acc[WM][WN];
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if (!LIST || tile.e < p.nlist) {
+        // rows past the tile's end repeat its last row; their results are not stored
+        auto a_row = [&](int row) -> int64_t {
+            int64_t q = min(tile.p0 + row, tile.p1 - 1);
+            if constexpr (LIST) {
+                if (p.order) {
+                    const int32_t slot = p.order[q];
+                    q = slot >= 0 ? slot / p.k : -1;
+                }
+                q = q >= 0 && q < p.arows ? q : 0;
+            }
+            return q;
+        };
+        auto b_row = [&](int row) -> int64_t {
+            return (LIST ? (int64_t)tile.e * p.n : 0) + min(n0 + row, p.n - 1);
+        };
+        // copies: instruction j of a wave brings rows 8 (4 j + wave) .. + 7, a lane one block
+        const int sub = lane >> 3;
+        const int ablk = (lane & 7) ^ sub;
+        const int bblk = (lane & 7) ^ block_swizzle<PAIR>(wave * 8 + sub);
+        const uint8_t *src[WM + WN];
+#pragma unroll
+        for (int j = 0; j < WM; ++j)
+            src[j] = p.a + (a_row((j * 4 + wave) * 8 + sub) * p.kb + ablk) * 16;
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+            src[WM + j] = p.b + (b_row((j * 4 + wave) * 8 + sub) * p.kb + bblk) * 16;
+        // exponent bytes: a thread per row of either operand
+        const uint8_t *asrc = p.as + a_row(min((int)threadIdx.x, TM - 1)) * p.kb;
+        const uint8_t *bsrc = p.bs + b_row(min((int)threadIdx.x, TN - 1)) * p.kb;
+        int bf, br;
+        pair_row_back<PAIR>((int)threadIdx.x % (16 * WN), bf, br);
+        const int aput = (int)threadIdx.x / (16 * WM) * 64 * WM + ((int)threadIdx.x & 15) * WM +
+                         (int)threadIdx.x % (16 * WM) / 16;
+        const int bput = TM * 4 + (int)threadIdx.x / (16 * WN) * 64 * WN + br * WN + bf;
+
+        const int chunks = (p.kb + 7) >> 3;
+        uint64_t asc = 0, bsc = 0;
+        auto fetch = [&](int c) {
+            uint8_t *to = code[c & 1] + wave * 1024;
+            const int left = p.kb - c * 8;
+            const uint8_t *zero = reinterpret_cast<const uint8_t *>(kZeroBlock);
+#pragma unroll
+            for (int j = 0; j < WM + WN; ++j) {
+                const uint8_t *from = src[j];
+                if (left < 8) // blocks past the row's end are zero
+                    from = (j < WM ? ablk : bblk) < left ? from : zero;
+                copy16_to_lds(from, to + (j < WM ? j * 4096 : TM * 128 + (j - WM) * 4096));
+                src[j] += 128;
+            }
+            asc = scale_bytes(asrc, c * 8, p.kb);
+            bsc = scale_bytes(bsrc, c * 8, p.kb);
+        };
+        auto put_scales = [&](int c) {
+            uint16_t *to = scale[c & 1];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (TM == 256 || (int)threadIdx.x < TM)
+                    to[aput + q * 16 * WM] =
+                        (uint16_t)((asc >> (8 * q) & 255) | (asc >> (24 + 8 * q) & 0xFF00));
+                if (TN == 256 || (int)threadIdx.x < TN)
+                    to[bput + q * 16 * WN] =
+                        (uint16_t)((bsc >> (8 * q) & 255) | (bsc >> (24 + 8 * q) & 0xFF00));
+            }
+        };
+        // operand reads: half h of a chunk is blocks 4 h .. 4 h + 3, one a lane group
+        int aoff[2], boff[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            aoff[h] = wm * WM * 2048 + r * 128 + (((4 * h + g) ^ (r & 7)) * 16);
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const int row = pair_row<PAIR>(o, r);
+                boff[h][o] = TM * 128 + wn * WN * 2048 + row * 128 +
+                             (((4 * h + g) ^ block_swizzle<PAIR>(row)) * 16);
+            }
+        }
+        struct Operands {
+            i32x4 a[WM], b[WN];
+        };
+        auto read_a = [&](const uint8_t *from, int h, int i) {
+            return *reinterpret_cast<const i32x4 *>(from + aoff[h] + i * 2048);
+        };
+        auto read_b = [&](const uint8_t *from, int h, int j) {
+            return *reinterpret_cast<const i32x4 *>(
+                from + boff[h][j & 1] + (PAIR ? (j >> 1) * 4096 : (j & ~1) * 2048));
+        };
+        ScaleRegs<WM> sa;
+        ScaleRegs<WN> sb;
+        const int sa_at = wm * 64 * WM + (g * 16 + r) * WM;
+        const int sb_at = TM * 4 + wn * 64 * WN + (g * 16 + r) * WN;
+
+        fetch(0);
+        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        put_scales(0);
+        lds_barrier();
+        if (chunks > 1)
+            fetch(1);
+        Operands x, y;
+#pragma unroll
+        for (int i = 0; i < WM; ++i)
+            x.a[i] = read_a(code[0], 0, i);
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+            x.b[j] = read_b(code[0], 0, j);
+        sa.read(scale[0] + sa_at);
+        sb.read(scale[0] + sb_at);
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const uint8_t *now = code[c & 1], *next = code[(c + 1) & 1];
+#pragma unroll
+            for (int i = 0; i < WM; ++i)
+                y.a[i] = read_a(now, 1, i);
+#pragma unroll
+            for (int j = 0; j < WN; ++j)
+                y.b[j] = read_b(now, 1, j);
+#pragma unroll
+            for (int i = 0; i < WM; ++i)
+#pragma unroll
+                for (int j = 0; j < WN; ++j)
+                    acc[i][j] = mfma_mx4_sel(x.b[j], sb.v[j / 2], (j & 1) * 2, x.a[i], sa.v[i / 2],
+                                             (i & 1) * 2, acc[i][j]);
+            if (c + 1 < chunks) {
+                __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                put_scales(c + 1);
+            }
+            lds_barrier(); // everyone has read this chunk and brought the next one
+            if (c + 2 < chunks)
+                fetch(c + 2);
+            ScaleRegs<WM> ta;
+            ScaleRegs<WN> tb;
+            ta.read(scale[(c + 1) & 1] + sa_at);
+            tb.read(scale[(c + 1) & 1] + sb_at);
+#pragma unroll
+            for (int i = 0; i < WM; ++i)
+                x.a[i] = read_a(next, 0, i);
+#pragma unroll
+            for (int j = 0; j < WN; ++j)
+                x.b[j] = read_b(next, 0, j);
+#pragma unroll
+            for (int i = 0; i < WM; ++i)
+#pragma unroll
+                for (int j = 0; j < WN; ++j)
+                    acc[i][j] = mfma_mx4_sel(y.b[j], sb.v[j / 2], (j & 1) * 2 + 1, y.a[i],
+                                             sa.v[i / 2], (i & 1) * 2 + 1, acc[i][j]);
+            sa = ta;
+            sb = tb;
+        }
+    }
+    constexpr int N = Piece<T>::N;
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+        const int64_t row = tile.p0 + (wm * WM + i) * 16 + r;
+        if (row >= tile.p1)
+            continue;
+#pragma unroll
+        for (int j = 0; j < WN; j += N / 4) {
+            const int n = n0 + wn * WN * 16 + (PAIR ? j * 16 + g * 8 : j * 16 + g * 4);
+            Piece<T> o;
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+                o.v[q] = acc[i][j + q / 4][q % 4];
+            o.store(out + row * p.n + n, p.n - n);
+        }
+    }
+}
+
+template <typename T, bool LIST, int WM, int WN>
+static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
+{
+    const int64_t nt = (p.n + 32ll * WN - 1) / (32 * WN);
+    int64_t mt = (p.m + 32ll * WM - 1) / (32 * WM);
+    if (LIST) // every list may end inside a tile, and so may the last rows
+        mt = p.m / (32 * WM) + (p.m < (int64_t)p.nlist + 1 ? p.m : (int64_t)p.nlist + 1);
+    hipLaunchKernelGGL((mx4_tile_kernel<T, LIST, WM, WN>), dim3((unsigned)(nt * mt)), dim3(256), 0,
+                       stream, p, (uint32_t)mt, (uint32_t)nt);
+    return hipGetLastError();
+}
+
 template <typename T>
 static hipError_t product_as(const Mx4Product &p, hipStream_t stream)
 {
+    if (p.m > 64) {
+        if (p.offsets)
+            return tiles_as<T, true, 4, 4>(p, stream);
+        if (p.m > 1024)
+            return tiles_as<T, false, 8, 8>(p, stream);
+        return tiles_as<T, false, 4, 4>(p, stream);
+    }
     const int64_t nt = ((int64_t)p.n + 15) / 16;
     int64_t mt = (p.m + 15) / 16;
     if (p.offsets) // every list may end inside a tile, and so may the last rows
