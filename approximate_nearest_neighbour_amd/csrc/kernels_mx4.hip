@@ -15,6 +15,7 @@ namespace ivfpq {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ---------------------------------------------------------------------------
 // rows to 4 bits and back
@@ -281,109 +282,100 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_direct_kernel(Mx4Product p)
 
 // Large tiles.
 //
-// A workgroup of four waves forms a (32 WM) x (32 WN) tile, each wave a
-// quarter of it: WM x WN sums of 16 x 16 in accumulator registers.  A row's
-// blocks come eight at a time (a chunk, 128 bytes of codes), both operands'
-// rows copied from memory into LDS without passing through registers; while
-// the matrix cores work on one chunk the next one arrives in the other half
-// of the LDS.  Inside a chunk the operands of the second half are read from
-// LDS while the first half is multiplied, and those of the next chunk's first
-// half while the second is.
+// A workgroup of MW x NW waves forms a tile of (32 WM MW) x (32 WN NW) results,
+// each wave its share of WM x WN sums of 32 x 32 in accumulator registers.  A
+// row's blocks come eight at a time (a chunk: 128 bytes of codes, four matrix
+// instructions deep), both operands' rows copied from memory into LDS without
+// passing through registers; one chunk is multiplied while the next arrives in
+// the other LDS object.  Inside a chunk the operands of one step are read from
+// LDS while those of the step before are multiplied.
 //
 // Code rows lie in LDS 128 bytes apart, their eight 16-byte blocks permuted by
-// an exclusive or with three bits of the row, so that eight lanes that read
-// the same block of eight rows touch all banks once.  Exponent bytes lie as
-// the lanes want them: the bytes of all of a lane's operands side by side, so
-// that one read brings them and the instruction's byte selector picks.
+// an exclusive or with three bits of the row, so that sixteen lanes that read
+// the same block of sixteen rows touch all banks once.  A row's exponent bytes
+// lie as two words, the even blocks' and the odd ones': a lane's four steps are
+// the four bytes of one word, picked by the instruction's byte selector.
 //
-// Results of a lane are consecutive columns: four for each sum, or eight over
-// two sums for 16-bit outputs, whose B rows are dealt to the sums accordingly
-// (pair_row); every store is then 16 bytes, 64 side by side.
+// A lane holds four times four consecutive columns of one row of results; for
+// 16-bit outputs B's rows are dealt to the sums so that pairs of these are
+// eight consecutive columns (deal_row), and every store is 16 bytes.
 
-__device__ const uint32_t kZeroBlock[4] = {0, 0, 0, 0};
-
-__device__ __forceinline__ void copy16_to_lds(const uint8_t *src, uint8_t *lds)
+// A value that is the same in every lane, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v)
 {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                     (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | lo);
 }
 
-// The product with the exponent bytes' selectors as run-time values that are
-// constants after unrolling.
-__device__ __forceinline__ f32x4 mfma_mx4_sel(i32x4 a, uint32_t sa, int sel_a, i32x4 b, uint32_t sb,
-                                              int sel_b, f32x4 c)
+// A memory range for the copies: reads past it give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t *base, int64_t from,
+                                                            int64_t bytes)
 {
-#define MX4_CASE(A, B)                                                                             \
-    case A * 4 + B:                                                                                \
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(low_half(a), low_half(b), c, 4, 4, \
-                                                                A, (int)sa, B, (int)sb);
-    switch (sel_a * 4 + sel_b) {
-        MX4_CASE(0, 0) MX4_CASE(0, 1) MX4_CASE(0, 2) MX4_CASE(0, 3)
-        MX4_CASE(1, 0) MX4_CASE(1, 1) MX4_CASE(1, 2) MX4_CASE(1, 3)
-        MX4_CASE(2, 0) MX4_CASE(2, 1) MX4_CASE(2, 2) MX4_CASE(2, 3)
-        MX4_CASE(3, 0) MX4_CASE(3, 1) MX4_CASE(3, 2) MX4_CASE(3, 3)
+    from = uniform(from);
+    const uint32_t size = (uint32_t)uniform(min(bytes - from, (int64_t)0xFFFFFFFF));
+    const uint8_t *p = base + from;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)size, 0x00027000);
+}
+
+// 16 bytes a lane to consecutive LDS addresses, from byte off (a lane's) + at.
+__device__ __forceinline__ void copy16_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t off, int at,
+                                              uint8_t *lds)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        from, (__attribute__((address_space(3))) void *)lds, 16, (int)off, at, 0, 0);
+}
+
+// Until at most N of this wave's memory operations are under way (the
+// compiler knows the instruction, and so what need not be waited for again).
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+    __asm__ volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ f32x16 mfma_mx4_32(i32x4 a, uint32_t sa, i32x4 b, uint32_t sb, int step,
+                                              f32x16 c)
+{
+#define MX4_CASE(S)                                                                               \
+    case S:                                                                                       \
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(low_half(a), low_half(b), c, 4, 4, \
+                                                               S, (int)sa, S, (int)sb);
+    switch (step) { // a constant after unrolling
+        MX4_CASE(0) MX4_CASE(1) MX4_CASE(2) MX4_CASE(3)
     }
 #undef MX4_CASE
     return c;
 }
 
-// Row of a wave's 16 W that operand row r of sum f holds, and back.  PAIR:
-// rows 32 h + 8 q + 4 o + i for f = 2 h + o, r = 4 q + i.
+// Row of B's 32 that operand row r of a sum holds.  A lane's results i = 4 a + c
+// are operand rows 8 a + 4 half + c; PAIR makes them rows 16 (a / 2) + 8 half +
+// 4 (a % 2) + c, else they are those rows themselves.
 template <bool PAIR>
-__device__ __forceinline__ int pair_row(int f, int r)
+__device__ __forceinline__ int deal_row(int r)
 {
-    return PAIR ? (f >> 1) * 32 + (r >> 2) * 8 + (f & 1) * 4 + (r & 3) : f * 16 + r;
+    return PAIR ? (r >> 4) * 16 + ((r >> 2) & 1) * 8 + ((r >> 3) & 1) * 4 + (r & 3) : r;
 }
 
-template <bool PAIR>
-__device__ __forceinline__ void pair_row_back(int n, int &f, int &r)
-{
-    f = PAIR ? (n >> 5) * 2 + ((n >> 2) & 1) : n >> 4;
-    r = PAIR ? ((n >> 3) & 3) * 4 + (n & 3) : n & 15;
-}
-
-// The three bits of a row that permute its blocks: different for lanes 0..7
-// (and 8..15) of an operand read.
-template <bool PAIR>
-__device__ __forceinline__ int block_swizzle(int row)
-{
-    return PAIR ? (row & 3) | ((row >> 1) & 4) : row & 7;
-}
-
-// Eight exponent bytes from byte c0 of a row's kb, zero past its end.
-__device__ __forceinline__ uint64_t scale_bytes(const uint8_t *row, int c0, int kb)
+// Eight exponent bytes from `at` on, in two steps so that the load need not be
+// waited for at once.  The load never passes `total` (at least 8): near the end
+// it starts earlier.
+__device__ __forceinline__ uint64_t load_scale_bytes(const uint8_t *scales, int64_t at,
+                                                     int64_t total)
 {
     typedef uint64_t U __attribute__((aligned(1)));
-    if (c0 + 8 <= kb)
-        return *reinterpret_cast<const U *>(row + c0);
-    uint64_t v = 0;
-    for (int i = 0; c0 + i < kb; ++i)
-        v |= (uint64_t)row[c0 + i] << (8 * i);
-    return v;
+    return *reinterpret_cast<const U *>(scales + min(at, total - 8));
 }
 
-// W exponent byte pairs of a lane, two a register.
-template <int W>
-struct ScaleRegs {
-    uint32_t v[(W + 1) / 2];
-    __device__ __forceinline__ void read(const uint16_t *p)
-    {
-        if constexpr (W == 8) {
-            const u32x4 t = *reinterpret_cast<const u32x4 *>(p);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = t[i];
-        } else if constexpr (W == 4) {
-            const u32x2 t = *reinterpret_cast<const u32x2 *>(p);
-            v[0] = t[0];
-            v[1] = t[1];
-        } else if constexpr (W == 2) {
-            v[0] = *reinterpret_cast<const uint32_t *>(p);
-        } else {
-            v[0] = *p;
-        }
-    }
-};
+// Bytes past the first `left` become zero, which makes their blocks vanish from
+// the sums (two factors of 2^-127) whatever codes stand there.
+__device__ __forceinline__ uint64_t trim_scale_bytes(uint64_t v, int64_t at, int64_t total,
+                                                     int left)
+{
+    v >>= (8 * max(at - (total - 8), (int64_t)0)) & 63;
+    return left >= 8 ? v : v & ((1ull << (8 * left)) - 1);
+}
 
 // Tile numbers: the workgroups of one XCD (every eighth) take a contiguous
 // range of tiles, and that range runs through groups of kGroup tiles along m
@@ -404,14 +396,18 @@ __device__ __forceinline__ void tile_of_block(uint32_t mt, uint32_t nt, uint32_t
     n = in / rows;
 }
 
-template <typename T, bool LIST, int WM, int WN>
-__global__ __launch_bounds__(256) void mx4_tile_kernel(Mx4Product p, uint32_t mtiles,
-                                                       uint32_t ntiles)
+template <typename T, bool LIST, int WM, int WN, int MW, int NW>
+__global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, uint32_t mtiles,
+                                                                uint32_t ntiles)
 {
     constexpr bool PAIR = sizeof(T) == 2;
-    constexpr int TM = 32 * WM, TN = 32 * WN;
-    __shared__ __align__(16) uint8_t code[2][(TM + TN) * 128];
-    __shared__ __align__(16) uint16_t scale[2][(TM + TN) * 4];
+    constexpr int WAVES = MW * NW, TM = 32 * WM * MW, TN = 32 * WN * NW;
+    constexpr int CA = TM / (8 * WAVES), CB = TN / (8 * WAVES); // copies of a wave, of a chunk
+    static_assert(TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0 && WAVES % 2 == 0, "copies");
+    static_assert(TM + TN <= 64 * WAVES, "a thread per row brings the exponent bytes");
+    // two objects, so that the compiler knows a copy into one from a read of the other
+    __shared__ __align__(16) uint8_t code0[(TM + TN) * 128], code1[(TM + TN) * 128];
+    __shared__ uint32_t scale[2][2][TM + TN];
 
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -423,16 +419,18 @@ __global__ __launch_bounds__(256) void mx4_tile_kernel(Mx4Product p, uint32_t mt
         tile = find_tile<TM>(p.offsets, p.nlist, p.m, mt);
     if (tile.p0 >= tile.p1)
         return;
-    const int wm = wave & 1, wn = wave >> 1;
-    const int r = lane & 15, g = lane >> 4;
+    const int wm = wave % MW, wn = wave / MW;
+    const int r = lane & 31, half = lane >> 5;
     T *out = static_cast<T *>(p.out);
 
-    f32x4 acc[WM][WN];
+    f32x16 acc[WM][WN];
 #pragma unroll
     for (int i = 0; i < WM; ++i)
 #pragma unroll
         for (int j = 0; j < WN; ++j)
-            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                acc[i][j][q] = 0.f;
 
     if (!LIST || tile.e < p.nlist) {
         // rows past the tile's end repeat its last row; their results are not stored
@@ -450,178 +448,164 @@ __global__ __launch_bounds__(256) void mx4_tile_kernel(Mx4Product p, uint32_t mt
         auto b_row = [&](int row) -> int64_t {
             return (LIST ? (int64_t)tile.e * p.n : 0) + min(n0 + row, p.n - 1);
         };
-        // copies: instruction j of a wave brings rows 8 (4 j + wave) .. + 7, a lane one block
+        // copies: instruction j of a wave brings rows 8 (WAVES j + wave) .. + 7, a lane one block
         const int sub = lane >> 3;
-        const int ablk = (lane & 7) ^ sub;
-        const int bblk = (lane & 7) ^ block_swizzle<PAIR>(wave * 8 + sub);
-        const uint8_t *src[WM + WN];
+        const int blk = (lane & 7) ^ (((wave & 1) * 8 + sub) >> 1);
+        const int64_t arow0 = LIST && p.order ? 0 : tile.p0; // rows are counted from here
+        const int64_t brow0 = b_row(0);
+        uint32_t off[CA + CB]; // byte of the lane's block in its row's first chunk
 #pragma unroll
-        for (int j = 0; j < WM; ++j)
-            src[j] = p.a + (a_row((j * 4 + wave) * 8 + sub) * p.kb + ablk) * 16;
+        for (int j = 0; j < CA; ++j)
+            off[j] = (uint32_t)(a_row((j * WAVES + wave) * 8 + sub) - arow0) *
+                         (uint32_t)p.kb * 16 + blk * 16;
 #pragma unroll
-        for (int j = 0; j < WN; ++j)
-            src[WM + j] = p.b + (b_row((j * 4 + wave) * 8 + sub) * p.kb + bblk) * 16;
-        // exponent bytes: a thread per row of either operand
-        const uint8_t *asrc = p.as + a_row(min((int)threadIdx.x, TM - 1)) * p.kb;
-        const uint8_t *bsrc = p.bs + b_row(min((int)threadIdx.x, TN - 1)) * p.kb;
-        int bf, br;
-        pair_row_back<PAIR>((int)threadIdx.x % (16 * WN), bf, br);
-        const int aput = (int)threadIdx.x / (16 * WM) * 64 * WM + ((int)threadIdx.x & 15) * WM +
-                         (int)threadIdx.x % (16 * WM) / 16;
-        const int bput = TM * 4 + (int)threadIdx.x / (16 * WN) * 64 * WN + br * WN + bf;
-
+        for (int j = 0; j < CB; ++j)
+            off[CA + j] = (uint32_t)(b_row((j * WAVES + wave) * 8 + sub) - brow0) *
+                              (uint32_t)p.kb * 16 + blk * 16;
+        const auto abuf = buffer_of(p.a, arow0 * p.kb * 16, p.arows * p.kb * 16);
+        const auto bbuf = buffer_of(p.b, brow0 * p.kb * 16,
+                                    (LIST ? (int64_t)p.nlist : 1) * p.n * p.kb * 16);
         const int chunks = (p.kb + 7) >> 3;
-        uint64_t asc = 0, bsc = 0;
-        auto fetch = [&](int c) {
-            uint8_t *to = code[c & 1] + wave * 1024;
-            const int left = p.kb - c * 8;
-            const uint8_t *zero = reinterpret_cast<const uint8_t *>(kZeroBlock);
+        // Chunk c into its LDS object.  What lies past a row's end (the next
+        // row's blocks, or zeros past the matrix) is multiplied too, with
+        // exponent bytes of zero; past the last chunk nobody reads it.
+        auto fetch = [&](int c, uint8_t *to) {
+            to += wave * 1024;
+            const int at = __builtin_amdgcn_readfirstlane(c * 128);
 #pragma unroll
-            for (int j = 0; j < WM + WN; ++j) {
-                const uint8_t *from = src[j];
-                if (left < 8) // blocks past the row's end are zero
-                    from = (j < WM ? ablk : bblk) < left ? from : zero;
-                copy16_to_lds(from, to + (j < WM ? j * 4096 : TM * 128 + (j - WM) * 4096));
-                src[j] += 128;
-            }
-            asc = scale_bytes(asrc, c * 8, p.kb);
-            bsc = scale_bytes(bsrc, c * 8, p.kb);
+            for (int j = 0; j < CA; ++j)
+                copy16_to_lds(abuf, off[j], at, to + j * WAVES * 1024);
+#pragma unroll
+            for (int j = 0; j < CB; ++j)
+                copy16_to_lds(bbuf, off[CA + j], at, to + TM * 128 + j * WAVES * 1024);
+        };
+        // exponent bytes: a thread per row of A, then of B
+        const int srow = (int)threadIdx.x;
+        const bool of_a = srow < TM;
+        const uint8_t *sfrom = of_a ? p.as : p.bs;
+        const int64_t sat = (of_a ? a_row(srow) : b_row(min(srow - TM, TN - 1))) * p.kb;
+        const int64_t stotal = of_a ? p.arows * p.kb : (LIST ? (int64_t)p.nlist : 1) * p.n * p.kb;
+        uint64_t bytes = 0;
+        auto load_scales = [&](int c) {
+            bytes = load_scale_bytes(sfrom, sat + min(c, chunks - 1) * 8, stotal);
         };
         auto put_scales = [&](int c) {
-            uint16_t *to = scale[c & 1];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (TM == 256 || (int)threadIdx.x < TM)
-                    to[aput + q * 16 * WM] =
-                        (uint16_t)((asc >> (8 * q) & 255) | (asc >> (24 + 8 * q) & 0xFF00));
-                if (TN == 256 || (int)threadIdx.x < TN)
-                    to[bput + q * 16 * WN] =
-                        (uint16_t)((bsc >> (8 * q) & 255) | (bsc >> (24 + 8 * q) & 0xFF00));
+            const int at = min(c, chunks - 1) * 8;
+            const uint64_t v = trim_scale_bytes(bytes, sat + at, stotal, p.kb - at);
+            if (TM + TN == 64 * WAVES || srow < TM + TN) {
+                const uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
+                scale[c & 1][0][srow] = __builtin_amdgcn_perm(hi, lo, 0x06040200);
+                scale[c & 1][1][srow] = __builtin_amdgcn_perm(hi, lo, 0x07050301);
             }
         };
-        // operand reads: half h of a chunk is blocks 4 h .. 4 h + 3, one a lane group
-        int aoff[2], boff[2][2];
+        // operand reads: step s takes blocks 2 s and 2 s + 1, one a half wave
+        const int brow = deal_row<PAIR>(r);
+        int aoff[4], boff[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            aoff[h] = wm * WM * 2048 + r * 128 + (((4 * h + g) ^ (r & 7)) * 16);
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                const int row = pair_row<PAIR>(o, r);
-                boff[h][o] = TM * 128 + wn * WN * 2048 + row * 128 +
-                             (((4 * h + g) ^ block_swizzle<PAIR>(row)) * 16);
-            }
+        for (int s = 0; s < 4; ++s) {
+            aoff[s] = wm * WM * 4096 + r * 128 + (((2 * s + half) ^ ((r >> 1) & 7)) * 16);
+            boff[s] = TM * 128 + wn * WN * 4096 + brow * 128 +
+                      (((2 * s + half) ^ ((brow >> 1) & 7)) * 16);
         }
+        const int sa_at = wm * WM * 32 + r, sb_at = TM + wn * WN * 32 + brow;
         struct Operands {
             i32x4 a[WM], b[WN];
         };
-        auto read_a = [&](const uint8_t *from, int h, int i) {
-            return *reinterpret_cast<const i32x4 *>(from + aoff[h] + i * 2048);
-        };
-        auto read_b = [&](const uint8_t *from, int h, int j) {
-            return *reinterpret_cast<const i32x4 *>(
-                from + boff[h][j & 1] + (PAIR ? (j >> 1) * 4096 : (j & ~1) * 2048));
-        };
-        ScaleRegs<WM> sa;
-        ScaleRegs<WN> sb;
-        const int sa_at = wm * 64 * WM + (g * 16 + r) * WM;
-        const int sb_at = TM * 4 + wn * 64 * WN + (g * 16 + r) * WN;
-
-        fetch(0);
-        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        put_scales(0);
-        lds_barrier();
-        if (chunks > 1)
-            fetch(1);
-        Operands x, y;
-#pragma unroll
-        for (int i = 0; i < WM; ++i)
-            x.a[i] = read_a(code[0], 0, i);
-#pragma unroll
-        for (int j = 0; j < WN; ++j)
-            x.b[j] = read_b(code[0], 0, j);
-        sa.read(scale[0] + sa_at);
-        sb.read(scale[0] + sb_at);
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            const uint8_t *now = code[c & 1], *next = code[(c + 1) & 1];
+        auto read = [&](const uint8_t *from, int s, Operands &o) {
 #pragma unroll
             for (int i = 0; i < WM; ++i)
-                y.a[i] = read_a(now, 1, i);
+                o.a[i] = *reinterpret_cast<const i32x4 *>(from + aoff[s] + i * 4096);
 #pragma unroll
             for (int j = 0; j < WN; ++j)
-                y.b[j] = read_b(now, 1, j);
+                o.b[j] = *reinterpret_cast<const i32x4 *>(from + boff[s] + j * 4096);
+        };
+        // Chunk c, lying in `here`, while the next one is copied into `next`.
+        auto chunk = [&](int c, const uint8_t *here, uint8_t *next) {
+            wait_vm<0>();  // this chunk and the next one's exponent bytes are here,
+            lds_barrier(); // and every wave is done with `next`
+            Operands o[2];
+            uint32_t sa[WM], sb[WN];
+            read(here, 0, o[0]);
 #pragma unroll
             for (int i = 0; i < WM; ++i)
+                sa[i] = scale[c & 1][half][sa_at + i * 32];
 #pragma unroll
-                for (int j = 0; j < WN; ++j)
-                    acc[i][j] = mfma_mx4_sel(x.b[j], sb.v[j / 2], (j & 1) * 2, x.a[i], sa.v[i / 2],
-                                             (i & 1) * 2, acc[i][j]);
-            if (c + 1 < chunks) {
-                __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-                put_scales(c + 1);
+            for (int j = 0; j < WN; ++j)
+                sb[j] = scale[c & 1][half][sb_at + j * 32];
+            __builtin_amdgcn_sched_barrier(0);
+            fetch(c + 1, next);
+            put_scales(c + 1);
+            load_scales(c + 2);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (s < 3)
+                    read(here, s + 1, o[(s + 1) & 1]);
+#pragma unroll
+                for (int i = 0; i < WM; ++i)
+#pragma unroll
+                    for (int j = 0; j < WN; ++j)
+                        acc[i][j] = mfma_mx4_32(o[s & 1].b[j], sb[j], o[s & 1].a[i], sa[i], s,
+                                                acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            lds_barrier(); // everyone has read this chunk and brought the next one
-            if (c + 2 < chunks)
-                fetch(c + 2);
-            ScaleRegs<WM> ta;
-            ScaleRegs<WN> tb;
-            ta.read(scale[(c + 1) & 1] + sa_at);
-            tb.read(scale[(c + 1) & 1] + sb_at);
-#pragma unroll
-            for (int i = 0; i < WM; ++i)
-                x.a[i] = read_a(next, 0, i);
-#pragma unroll
-            for (int j = 0; j < WN; ++j)
-                x.b[j] = read_b(next, 0, j);
-#pragma unroll
-            for (int i = 0; i < WM; ++i)
-#pragma unroll
-                for (int j = 0; j < WN; ++j)
-                    acc[i][j] = mfma_mx4_sel(y.b[j], sb.v[j / 2], (j & 1) * 2 + 1, y.a[i],
-                                             sa.v[i / 2], (i & 1) * 2 + 1, acc[i][j]);
-            sa = ta;
-            sb = tb;
+        };
+        load_scales(0);
+        fetch(0, code0);
+        put_scales(0);
+        load_scales(1);
+#pragma unroll 1
+        for (int c = 0; c < chunks; c += 2) {
+            chunk(c, code0, code1);
+            if (c + 1 < chunks)
+                chunk(c + 1, code1, code0);
         }
+        // copies still under way must not outlive the workgroup's LDS
+        wait_vm<0>();
     }
     constexpr int N = Piece<T>::N;
 #pragma unroll
     for (int i = 0; i < WM; ++i) {
-        const int64_t row = tile.p0 + (wm * WM + i) * 16 + r;
+        const int64_t row = tile.p0 + (wm * WM + i) * 32 + r;
         if (row >= tile.p1)
             continue;
 #pragma unroll
-        for (int j = 0; j < WN; j += N / 4) {
-            const int n = n0 + wn * WN * 16 + (PAIR ? j * 16 + g * 8 : j * 16 + g * 4);
-            Piece<T> o;
+        for (int j = 0; j < WN; ++j)
 #pragma unroll
-            for (int q = 0; q < N; ++q)
-                o.v[q] = acc[i][j + q / 4][q % 4];
-            o.store(out + row * p.n + n, p.n - n);
-        }
+            for (int q = 0; q < 16 / N; ++q) {
+                const int n = n0 + (wn * WN + j) * 32 + 2 * N * q + N * half;
+                Piece<T> o;
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    o.v[e] = acc[i][j][q * N + e];
+                o.store(out + row * p.n + n, p.n - n);
+            }
     }
 }
 
-template <typename T, bool LIST, int WM, int WN>
+template <typename T, bool LIST, int WM, int WN, int MW, int NW>
 static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
 {
-    const int64_t nt = (p.n + 32ll * WN - 1) / (32 * WN);
-    int64_t mt = (p.m + 32ll * WM - 1) / (32 * WM);
+    constexpr int64_t TM = 32 * WM * MW, TN = 32 * WN * NW;
+    const int64_t nt = (p.n + TN - 1) / TN;
+    int64_t mt = (p.m + TM - 1) / TM;
     if (LIST) // every list may end inside a tile, and so may the last rows
-        mt = p.m / (32 * WM) + (p.m < (int64_t)p.nlist + 1 ? p.m : (int64_t)p.nlist + 1);
-    hipLaunchKernelGGL((mx4_tile_kernel<T, LIST, WM, WN>), dim3((unsigned)(nt * mt)), dim3(256), 0,
-                       stream, p, (uint32_t)mt, (uint32_t)nt);
+        mt = p.m / TM + (p.m < (int64_t)p.nlist + 1 ? p.m : (int64_t)p.nlist + 1);
+    hipLaunchKernelGGL((mx4_tile_kernel<T, LIST, WM, WN, MW, NW>), dim3((unsigned)(nt * mt)),
+                       dim3(64 * MW * NW), 0, stream, p, (uint32_t)mt, (uint32_t)nt);
     return hipGetLastError();
 }
 
 template <typename T>
 static hipError_t product_as(const Mx4Product &p, hipStream_t stream)
 {
-    if (p.m > 64) {
+    const int64_t bbytes = (p.offsets ? (int64_t)p.nlist : 1) * p.n * p.kb;
+    const bool far = p.order && p.arows * p.kb * 16 >= (int64_t)1 << 32;
+    if (p.m > 64 && bbytes >= 8 && p.arows * p.kb >= 8 && !far) {
         if (p.offsets)
-            return tiles_as<T, true, 4, 4>(p, stream);
+            return tiles_as<T, true, 2, 2, 2, 2>(p, stream);
         if (p.m > 1024)
-            return tiles_as<T, false, 8, 8>(p, stream);
-        return tiles_as<T, false, 4, 4>(p, stream);
+            return tiles_as<T, false, 4, 2, 2, 4>(p, stream);
+        return tiles_as<T, false, 2, 2, 2, 2>(p, stream);
     }
     const int64_t nt = ((int64_t)p.n + 15) / 16;
     int64_t mt = (p.m + 15) / 16;
