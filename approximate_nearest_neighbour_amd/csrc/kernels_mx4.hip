@@ -358,24 +358,31 @@ __device__ __forceinline__ int deal_row(int r)
     return PAIR ? (r >> 4) * 16 + ((r >> 2) & 1) * 8 + ((r >> 3) & 1) * 4 + (r & 3) : r;
 }
 
-// Eight exponent bytes from `at` on, in two steps so that the load need not be
-// waited for at once.  The load never passes `total` (at least 8): near the end
-// it starts earlier.
-__device__ __forceinline__ uint64_t load_scale_bytes(const uint8_t *scales, int64_t at,
-                                                     int64_t total)
-{
-    typedef uint64_t U __attribute__((aligned(1)));
-    return *reinterpret_cast<const U *>(scales + min(at, total - 8));
-}
-
-// Bytes past the first `left` become zero, which makes their blocks vanish from
-// the sums (two factors of 2^-127) whatever codes stand there.
-__device__ __forceinline__ uint64_t trim_scale_bytes(uint64_t v, int64_t at, int64_t total,
-                                                     int left)
-{
-    v >>= (8 * max(at - (total - 8), (int64_t)0)) & 63;
-    return left >= 8 ? v : v & ((1ull << (8 * left)) - 1);
-}
+// Sixteen exponent bytes of a row, two chunks' worth.  The load may be waited
+// for later than it is issued, so what depends on its position comes apart.
+struct ScaleBytes {
+    u32x4 v;
+    // from byte `at` on, but never past `total` (at least 16): near the end it starts earlier
+    __device__ __forceinline__ void load(const uint8_t *scales, int64_t at, int64_t total)
+    {
+        typedef uint32_t U __attribute__((ext_vector_type(4), aligned(1)));
+        v = *reinterpret_cast<const U *>(scales + min(at, total - 16));
+    }
+    // The eight bytes from `at` + 8 ODD on, with those past the first `left`
+    // zero: their blocks vanish from the sums (two factors of 2^-127) whatever
+    // codes stand there.
+    template <int ODD>
+    __device__ __forceinline__ uint64_t get(int64_t at, int64_t total, int left) const
+    {
+        const int early = (int)max(at - (total - 16), (int64_t)0) + 8 * ODD; // bytes to skip
+        const uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+        const uint64_t w = early < 8 ? lo : hi;
+        uint64_t r = w >> (8 * (early & 7));
+        r |= early > 0 && early < 8 ? hi << (64 - 8 * (early & 7)) : 0;
+        const uint64_t keep = left >= 8 ? ~0ull : left > 0 ? (1ull << (8 * left)) - 1 : 0;
+        return early < 16 ? r & keep : 0;
+    }
+};
 
 // Tile numbers: the workgroups of one XCD (every eighth) take a contiguous
 // range of tiles, and that range runs through groups of kGroup tiles along m
@@ -485,17 +492,17 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, ui
         const uint8_t *sfrom = of_a ? p.as : p.bs;
         const int64_t sat = (of_a ? a_row(srow) : b_row(min(srow - TM, TN - 1))) * p.kb;
         const int64_t stotal = of_a ? p.arows * p.kb : (LIST ? (int64_t)p.nlist : 1) * p.n * p.kb;
-        uint64_t bytes = 0;
-        auto load_scales = [&](int c) {
-            bytes = load_scale_bytes(sfrom, sat + min(c, chunks - 1) * 8, stotal);
+        ScaleBytes bytes;
+        auto load_scales = [&](int c) { // chunks c and c + 1
+            bytes.load(sfrom, sat + min(c, chunks - 1) * 8, stotal);
         };
-        auto put_scales = [&](int c) {
-            const int at = min(c, chunks - 1) * 8;
-            const uint64_t v = trim_scale_bytes(bytes, sat + at, stotal, p.kb - at);
+        auto put_scales = [&](int c, auto odd) { // chunk c, whose number is odd or not
+            constexpr int ODD = decltype(odd)::value;
+            const uint64_t v = bytes.get<ODD>(sat + (c - ODD) * 8, stotal, p.kb - c * 8);
             if (TM + TN == 64 * WAVES || srow < TM + TN) {
                 const uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
-                scale[c & 1][0][srow] = __builtin_amdgcn_perm(hi, lo, 0x06040200);
-                scale[c & 1][1][srow] = __builtin_amdgcn_perm(hi, lo, 0x07050301);
+                scale[ODD][0][srow] = __builtin_amdgcn_perm(hi, lo, 0x06040200);
+                scale[ODD][1][srow] = __builtin_amdgcn_perm(hi, lo, 0x07050301);
             }
         };
         // operand reads: step s takes blocks 2 s and 2 s + 1, one a half wave
@@ -519,8 +526,11 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, ui
             for (int j = 0; j < WN; ++j)
                 o.b[j] = *reinterpret_cast<const i32x4 *>(from + boff[s] + j * 4096);
         };
+        constexpr std::integral_constant<int, 0> even{};
+        constexpr std::integral_constant<int, 1> odd{};
         // Chunk c, lying in `here`, while the next one is copied into `next`.
-        auto chunk = [&](int c, const uint8_t *here, uint8_t *next) {
+        auto chunk = [&](int c, auto parity, const uint8_t *here, uint8_t *next) {
+            constexpr int ODD = decltype(parity)::value;
             wait_vm<0>();  // this chunk and the next one's exponent bytes are here,
             lds_barrier(); // and every wave is done with `next`
             Operands o[2];
@@ -528,14 +538,18 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, ui
             read(here, 0, o[0]);
 #pragma unroll
             for (int i = 0; i < WM; ++i)
-                sa[i] = scale[c & 1][half][sa_at + i * 32];
+                sa[i] = scale[ODD][half][sa_at + i * 32];
 #pragma unroll
             for (int j = 0; j < WN; ++j)
-                sb[j] = scale[c & 1][half][sb_at + j * 32];
+                sb[j] = scale[ODD][half][sb_at + j * 32];
             __builtin_amdgcn_sched_barrier(0);
             fetch(c + 1, next);
-            put_scales(c + 1);
-            load_scales(c + 2);
+            if constexpr (ODD) {
+                put_scales(c + 1, even);
+            } else {
+                put_scales(c + 1, odd);
+                load_scales(c + 2);
+            }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 if (s < 3)
@@ -551,13 +565,12 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, ui
         };
         load_scales(0);
         fetch(0, code0);
-        put_scales(0);
-        load_scales(1);
+        put_scales(0, even);
 #pragma unroll 1
         for (int c = 0; c < chunks; c += 2) {
-            chunk(c, code0, code1);
+            chunk(c, even, code0, code1);
             if (c + 1 < chunks)
-                chunk(c + 1, code1, code0);
+                chunk(c + 1, odd, code1, code0);
         }
         // copies still under way must not outlive the workgroup's LDS
         wait_vm<0>();
@@ -598,9 +611,9 @@ static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
 template <typename T>
 static hipError_t product_as(const Mx4Product &p, hipStream_t stream)
 {
-    const int64_t bbytes = (p.offsets ? (int64_t)p.nlist : 1) * p.n * p.kb;
+    const int64_t brows = (p.offsets ? (int64_t)p.nlist : 1) * p.n;
     const bool far = p.order && p.arows * p.kb * 16 >= (int64_t)1 << 32;
-    if (p.m > 64 && bbytes >= 8 && p.arows * p.kb >= 8 && !far) {
+    if (p.m > 64 && brows * p.kb >= 16 && p.arows * p.kb >= 16 && !far) {
         if (p.offsets)
             return tiles_as<T, true, 2, 2, 2, 2>(p, stream);
         if (p.m > 1024)
