@@ -1288,9 +1288,11 @@ ivfpq_status ivfpq_route_sort_ex(const int32_t *lists_dev, int64_t nvec, int k, 
         return s;
     if (nlist < 1 || nlist > kMaxRouteLists)
         return fail(IVFPQ_E_INVALID_ARG, "nlist must be in [1, 2^22)");
-    if (!offsets_dev || (nvec > 0 && (!lists_dev || !order_dev || !pos_dev || !workspace_dev)))
+    const size_t need = route_sort_bytes(nvec * k, nlist);
+    if (!offsets_dev || (nvec > 0 && (!lists_dev || !order_dev || !pos_dev)) ||
+        (need > 0 && !workspace_dev))
         return fail(IVFPQ_E_INVALID_ARG, "a required device pointer is NULL");
-    if (workspace_bytes < route_sort_bytes(nvec * k, nlist) || !aligned(workspace_dev, 16))
+    if (workspace_bytes < need || !aligned(workspace_dev, 16))
         return fail(IVFPQ_E_INVALID_ARG, "the workspace is too small or not 16-byte aligned");
     return launched(launch_route_sort(lists_dev, nvec * k, nlist, workspace_dev, offsets_dev,
                                       order_dev, pos_dev, reinterpret_cast<hipStream_t>(stream)),

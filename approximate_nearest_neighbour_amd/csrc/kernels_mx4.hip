@@ -296,9 +296,14 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_direct_kernel(Mx4Product p)
 // lie as two words, the even blocks' and the odd ones': a lane's four steps are
 // the four bytes of one word, picked by the instruction's byte selector.
 //
-// A lane holds four times four consecutive columns of one row of results; for
-// 16-bit outputs B's rows are dealt to the sums so that pairs of these are
-// eight consecutive columns (deal_row), and every store is 16 bytes.
+// Results: for float32 a lane holds one column of sixteen rows, and a store
+// covers 128 bytes of two rows.  For 16-bit outputs the operands change places:
+// a lane holds four times four consecutive columns of one row, B's rows dealt
+// to the sums so that pairs of these are eight consecutive columns (deal_row),
+// and a store is 16 bytes.
+//
+// ONE: rows of at most one chunk (d <= 256) need no second LDS object, and
+// more workgroups fit a CU to overlap one's stores with another's loads.
 
 // A value that is the same in every lane, in scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t v)
@@ -403,7 +408,7 @@ __device__ __forceinline__ void tile_of_block(uint32_t mt, uint32_t nt, uint32_t
     n = in / rows;
 }
 
-template <typename T, bool LIST, int WM, int WN, int MW, int NW>
+template <typename T, bool LIST, int WM, int WN, int MW, int NW, bool ONE>
 __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, uint32_t mtiles,
                                                                 uint32_t ntiles)
 {
@@ -413,8 +418,8 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, ui
     static_assert(TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0 && WAVES % 2 == 0, "copies");
     static_assert(TM + TN <= 64 * WAVES, "a thread per row brings the exponent bytes");
     // two objects, so that the compiler knows a copy into one from a read of the other
-    __shared__ __align__(16) uint8_t code0[(TM + TN) * 128], code1[(TM + TN) * 128];
-    __shared__ uint32_t scale[2][2][TM + TN];
+    __shared__ __align__(16) uint8_t code0[(TM + TN) * 128], code1[ONE ? 16 : (TM + TN) * 128];
+    __shared__ uint32_t scale[ONE ? 1 : 2][2][TM + TN];
 
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -543,12 +548,14 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, ui
             for (int j = 0; j < WN; ++j)
                 sb[j] = scale[ODD][half][sb_at + j * 32];
             __builtin_amdgcn_sched_barrier(0);
-            fetch(c + 1, next);
-            if constexpr (ODD) {
-                put_scales(c + 1, even);
-            } else {
-                put_scales(c + 1, odd);
-                load_scales(c + 2);
+            if constexpr (!ONE) {
+                fetch(c + 1, next);
+                if constexpr (ODD) {
+                    put_scales(c + 1, even);
+                } else {
+                    put_scales(c + 1, odd);
+                    load_scales(c + 2);
+                }
             }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
@@ -558,22 +565,46 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, ui
                 for (int i = 0; i < WM; ++i)
 #pragma unroll
                     for (int j = 0; j < WN; ++j)
-                        acc[i][j] = mfma_mx4_32(o[s & 1].b[j], sb[j], o[s & 1].a[i], sa[i], s,
-                                                acc[i][j]);
+                        acc[i][j] = PAIR ? mfma_mx4_32(o[s & 1].b[j], sb[j], o[s & 1].a[i], sa[i],
+                                                       s, acc[i][j])
+                                         : mfma_mx4_32(o[s & 1].a[i], sa[i], o[s & 1].b[j], sb[j],
+                                                       s, acc[i][j]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
         load_scales(0);
         fetch(0, code0);
         put_scales(0, even);
+        if constexpr (ONE) {
+            chunk(0, even, code0, code1);
+        } else {
 #pragma unroll 1
-        for (int c = 0; c < chunks; c += 2) {
-            chunk(c, even, code0, code1);
-            if (c + 1 < chunks)
-                chunk(c + 1, odd, code1, code0);
+            for (int c = 0; c < chunks; c += 2) {
+                chunk(c, even, code0, code1);
+                if (c + 1 < chunks)
+                    chunk(c + 1, odd, code1, code0);
+            }
         }
         // copies still under way must not outlive the workgroup's LDS
         wait_vm<0>();
+    }
+    if constexpr (!PAIR) {
+#pragma unroll
+        for (int j = 0; j < WN; ++j) {
+            const int n = n0 + (wn * WN + j) * 32 + r;
+            if (n >= p.n)
+                continue;
+#pragma unroll
+            for (int i = 0; i < WM; ++i)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const int64_t row =
+                        tile.p0 + (wm * WM + i) * 32 + (q >> 2) * 8 + half * 4 + (q & 3);
+                    if (row < tile.p1)
+                        out[row * p.n + n] = (T)acc[i][j][q];
+                }
+        }
+        return;
     }
     constexpr int N = Piece<T>::N;
 #pragma unroll
@@ -595,7 +626,7 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, ui
     }
 }
 
-template <typename T, bool LIST, int WM, int WN, int MW, int NW>
+template <typename T, bool LIST, int WM, int WN, int MW, int NW, bool ONE = false>
 static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
 {
     constexpr int64_t TM = 32 * WM * MW, TN = 32 * WN * NW;
@@ -603,7 +634,7 @@ static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
     int64_t mt = (p.m + TM - 1) / TM;
     if (LIST) // every list may end inside a tile, and so may the last rows
         mt = p.m / TM + (p.m < (int64_t)p.nlist + 1 ? p.m : (int64_t)p.nlist + 1);
-    hipLaunchKernelGGL((mx4_tile_kernel<T, LIST, WM, WN, MW, NW>), dim3((unsigned)(nt * mt)),
+    hipLaunchKernelGGL((mx4_tile_kernel<T, LIST, WM, WN, MW, NW, ONE>), dim3((unsigned)(nt * mt)),
                        dim3(64 * MW * NW), 0, stream, p, (uint32_t)mt, (uint32_t)nt);
     return hipGetLastError();
 }
@@ -614,8 +645,13 @@ static hipError_t product_as(const Mx4Product &p, hipStream_t stream)
     const int64_t brows = (p.offsets ? (int64_t)p.nlist : 1) * p.n;
     const bool far = p.order && p.arows * p.kb * 16 >= (int64_t)1 << 32;
     if (p.m > 64 && brows * p.kb >= 16 && p.arows * p.kb >= 16 && !far) {
-        if (p.offsets)
+        if (p.offsets) {
+            if (p.m >= 256ll * p.nlist)
+                return tiles_as<T, true, 4, 2, 2, 4>(p, stream);
             return tiles_as<T, true, 2, 2, 2, 2>(p, stream);
+        }
+        if (p.kb <= 8)
+            return tiles_as<T, false, 2, 2, 2, 2, true>(p, stream);
         if (p.m > 1024)
             return tiles_as<T, false, 4, 2, 2, 4>(p, stream);
         return tiles_as<T, false, 2, 2, 2, 2>(p, stream);

@@ -85,29 +85,40 @@ __global__ __launch_bounds__(256) void route_scan_kernel(SortPass s)
 
 // Every slot to its place: start of its bin, plus the bin's slots of earlier
 // workgroups, of earlier waves of this one (each wave has a contiguous part of
-// the chunk) and of earlier lanes.
-__global__ __launch_bounds__(64 * kSortWaves) void route_scatter_kernel(SortPass s)
+// the chunk) and of earlier lanes.  SOLO: the one workgroup of a small sort,
+// which has all counts itself, and so is the whole sort in one launch.
+template <int WAVES, int BINS, bool SOLO>
+__global__ __launch_bounds__(64 * WAVES) void route_scatter_kernel(SortPass s)
 {
-    __shared__ uint32_t at[kSortWaves][kSortBins];
-    __shared__ uint32_t sums[kSortWaves];
+    __shared__ uint32_t at[WAVES][BINS];
+    __shared__ uint32_t sums[WAVES];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    for (uint32_t b = threadIdx.x; b < s.bins; b += blockDim.x)
+    for (uint32_t b = threadIdx.x; b < s.bins; b += 64 * WAVES)
 #pragma unroll
-        for (int w = 0; w < kSortWaves; ++w)
+        for (int w = 0; w < WAVES; ++w)
             at[w][b] = 0;
     __syncthreads();
-    constexpr uint32_t kPart = kSortChunk / kSortWaves;
-    const uint32_t first = min(blockIdx.x * (uint32_t)kSortChunk + wave * kPart, s.n);
-    const uint32_t end = min(first + kPart, s.n);
+    const uint32_t part = SOLO ? (s.n + WAVES - 1) / WAVES : kSortChunk / WAVES;
+    const uint32_t first = min(blockIdx.x * (uint32_t)kSortChunk + wave * part, s.n);
+    const uint32_t end = min(first + part, s.n);
     for (uint32_t i = first + lane; i < end; i += 64)
         atomicAdd(&at[wave][s.bin(s.key(i))], 1u);
     __syncthreads();
-    // bins in order, 256 at a time: exclusive sums of the totals
+    // bins in order, a thread each: exclusive sums of the totals
     uint32_t base = 0;
-    for (uint32_t b0 = 0; b0 < s.bins; b0 += 64 * kSortWaves) {
+    for (uint32_t b0 = 0; b0 < s.bins; b0 += 64 * WAVES) {
         const uint32_t b = b0 + threadIdx.x;
-        const uint32_t v = b < s.bins ? s.total[b] : 0;
+        uint32_t v = 0;
+        if (b < s.bins) {
+            if constexpr (SOLO) {
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w)
+                    v += at[w][b];
+            } else {
+                v = s.total[b];
+            }
+        }
         const uint32_t upto = wave_inclusive_sum(v);
         if (lane == 63)
             sums[wave] = upto;
@@ -115,7 +126,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void route_scatter_kernel(SortPass
         uint32_t start = base + upto - v;
         uint32_t all = 0;
 #pragma unroll
-        for (int w = 0; w < kSortWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             start += w < wave ? sums[w] : 0;
             all += sums[w];
         }
@@ -123,9 +134,10 @@ __global__ __launch_bounds__(64 * kSortWaves) void route_scatter_kernel(SortPass
         if (b < s.bins) {
             if (s.offsets && blockIdx.x == 0)
                 s.offsets[b] = (int32_t)start;
-            start += s.hist[(size_t)b * s.blocks + blockIdx.x];
+            if constexpr (!SOLO)
+                start += s.hist[(size_t)b * s.blocks + blockIdx.x];
 #pragma unroll
-            for (int w = 0; w < kSortWaves; ++w) {
+            for (int w = 0; w < WAVES; ++w) {
                 const uint32_t c = at[w][b];
                 at[w][b] = start;
                 start += c;
@@ -184,6 +196,12 @@ __global__ __launch_bounds__(256) void route_bounds_kernel(const uint32_t *__res
     offsets[l] = (int32_t)lo;
 }
 
+// Up to this many slots and lists the sort is one workgroup.
+constexpr int64_t kSoloSlots = 16384;
+constexpr int kSoloBins = 1088;
+
+static bool sort_solo(int64_t n, int nlist) { return n <= kSoloSlots && nlist < kSoloBins; }
+
 static uint32_t sort_blocks(int64_t n)
 {
     return (uint32_t)((n + kSortChunk - 1) / kSortChunk);
@@ -191,6 +209,8 @@ static uint32_t sort_blocks(int64_t n)
 
 size_t route_sort_bytes(int64_t n, int nlist)
 {
+    if (sort_solo(n, nlist))
+        return 0;
     const size_t blocks = sort_blocks(n);
     const size_t bins = nlist < kSortBins ? (size_t)nlist + 1 : (size_t)kSortBins;
     size_t b = (bins * blocks + bins) * 4;
@@ -217,6 +237,14 @@ hipError_t launch_route_sort(const int32_t *lists, int64_t n, int nlist, void *w
                            stream, nullptr, 0u, (uint32_t)nlist, offsets);
         return hipGetLastError();
     }
+    if (sort_solo(n, nlist)) {
+        s.order = order;
+        s.pos = pos;
+        s.offsets = offsets;
+        hipLaunchKernelGGL((route_scatter_kernel<16, kSoloBins, true>), dim3(1), dim3(1024), 0,
+                           stream, s);
+        return hipGetLastError();
+    }
     for (int pass = 0; pass < (two ? 2 : 1); ++pass) {
         if (pass == 1) {
             s.shift = kSortBits;
@@ -232,8 +260,8 @@ hipError_t launch_route_sort(const int32_t *lists, int64_t n, int nlist, void *w
         s.offsets = two ? nullptr : offsets;
         hipLaunchKernelGGL(route_count_kernel, dim3(s.blocks), dim3(64 * kSortWaves), 0, stream, s);
         hipLaunchKernelGGL(route_scan_kernel, dim3((s.bins + 3) / 4), dim3(256), 0, stream, s);
-        hipLaunchKernelGGL(route_scatter_kernel, dim3(s.blocks), dim3(64 * kSortWaves), 0, stream,
-                           s);
+        hipLaunchKernelGGL((route_scatter_kernel<kSortWaves, kSortBins, false>), dim3(s.blocks),
+                           dim3(64 * kSortWaves), 0, stream, s);
     }
     if (two)
         hipLaunchKernelGGL(route_bounds_kernel, dim3((unsigned)nlist / 256 + 1), dim3(256), 0,
@@ -256,67 +284,108 @@ static int row_lanes(int d)
     return l;
 }
 
-// rows[p] = w x[t] of the slot at p, zero where no slot is.
+// rows[p] = w x[t] of the slot at p, zero where no slot is.  A thread has one
+// piece of kRowsAtOnce rows that lie `step` apart, so that as many loads are
+// under way: they wait for their slot numbers, and the stores for them.
+constexpr int kRowsAtOnce = 4;
+
 template <typename T>
 __global__ __launch_bounds__(256) void route_gather_kernel(const T *__restrict__ x, int64_t n,
-                                                           int d, int lanes, FastDiv k,
+                                                           int64_t step, int d, FastDiv pieces,
+                                                           FastDiv k,
                                                            const int32_t *__restrict__ order,
                                                            const float *__restrict__ weights,
-                                                           T *__restrict__ rows)
+                                                           T *__restrict__ rows, int64_t row0)
 {
     constexpr int N = Piece<T>::N;
-    const int64_t p = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
-    if (p >= n)
+    const uint32_t g = blockIdx.x * 256u + threadIdx.x;
+    const int64_t p0 = row0 + pieces.div(g);
+    if (p0 >= step)
         return;
-    const uint32_t u = (uint32_t)order[p];
-    const bool kept = u < (uint64_t)n;
-    const T *src = x + (kept ? (int64_t)k.div(u) : 0) * d;
-    const float w = kept && weights ? weights[u] : 1.f;
-    for (int c = (threadIdx.x & (lanes - 1)) * N; c < d; c += lanes * N) {
-        Piece<T> v;
-        if (kept)
-            v.load(src + c, d - c);
-        else
-            v.zero();
-        if (weights) {
+    const int c = (int)(g - (uint32_t)(p0 - row0) * pieces.c) * N;
+    uint32_t u[kRowsAtOnce];
+    Piece<T> v[kRowsAtOnce];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                v.v[i] *= w;
+    for (int i = 0; i < kRowsAtOnce; ++i)
+        u[i] = p0 + i * step < n ? (uint32_t)order[p0 + i * step] : ~0u;
+    if (d - c >= N) {
+#pragma unroll
+        for (int i = 0; i < kRowsAtOnce; ++i)
+            v[i].load(x + (int64_t)k.div(u[i] < (uint64_t)n ? u[i] : 0) * d + c, N);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kRowsAtOnce; ++i)
+            v[i].load(x + (int64_t)k.div(u[i] < (uint64_t)n ? u[i] : 0) * d + c, d - c);
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsAtOnce; ++i) {
+        const int64_t p = p0 + i * step;
+        if (p >= n)
+            break;
+        if (u[i] >= (uint64_t)n) {
+            v[i].zero();
+        } else if (weights) {
+            const float w = weights[u[i]];
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                v[i].v[e] *= w;
         }
-        v.store(rows + p * d + c, d - c);
+        v[i].store(rows + p * d + c, d - c);
     }
 }
 
 // y[t] = sum over j of w[t][j] rows[pos[t][j]], j ascending in float32,
-// rounded once; slots without a position are skipped.
+// rounded once; slots without a position add nothing (row 0 is read in their
+// place and dropped, so that a batch of loads has no branch in it).  A thread
+// has one piece of a vector, kSlotsAtOnce of its rows under way together.
+constexpr int kSlotsAtOnce = 8;
+
 template <typename T>
 __global__ __launch_bounds__(256) void route_combine_kernel(const T *__restrict__ rows,
-                                                            int64_t nvec, int d, int lanes, int k,
+                                                            int64_t nvec, int d, FastDiv pieces,
+                                                            int k,
                                                             const int32_t *__restrict__ pos,
                                                             const float *__restrict__ weights,
-                                                            T *__restrict__ out)
+                                                            T *__restrict__ out, int64_t row0)
 {
     constexpr int N = Piece<T>::N;
-    const int64_t t = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+    const uint32_t g = blockIdx.x * 256u + threadIdx.x;
+    const int64_t t = row0 + pieces.div(g);
     if (t >= nvec)
         return;
+    const int c = (int)(g - (uint32_t)(t - row0) * pieces.c) * N;
     const int64_t n = nvec * k;
-    for (int c = (threadIdx.x & (lanes - 1)) * N; c < d; c += lanes * N) {
-        Piece<T> sum;
-        sum.zero();
-        for (int j = 0; j < k; ++j) {
-            const int64_t p = pos[t * k + j];
-            if (p < 0 || p >= n)
-                continue;
-            const float w = weights ? weights[t * k + j] : 1.f;
-            Piece<T> v;
-            v.load(rows + p * d + c, d - c);
+    const bool whole = d - c >= N;
+    Piece<T> sum;
+    sum.zero();
+    for (int j0 = 0; j0 < k; j0 += kSlotsAtOnce) {
+        int64_t p[kSlotsAtOnce];
+        float w[kSlotsAtOnce];
+        Piece<T> v[kSlotsAtOnce];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                sum.v[i] = fmaf(w, v.v[i], sum.v[i]);
+        for (int j = 0; j < kSlotsAtOnce; ++j) {
+            const int at = min(j0 + j, k - 1);
+            p[j] = j0 + j < k ? pos[t * k + at] : -1;
+            w[j] = weights ? weights[t * k + at] : 1.f;
         }
-        sum.store(out + t * d + c, d - c);
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < kSlotsAtOnce; ++j)
+                v[j].load(rows + ((uint64_t)p[j] < (uint64_t)n ? p[j] : 0) * d + c, N);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kSlotsAtOnce; ++j)
+                v[j].load(rows + ((uint64_t)p[j] < (uint64_t)n ? p[j] : 0) * d + c, d - c);
+        }
+#pragma unroll
+        for (int j = 0; j < kSlotsAtOnce; ++j) {
+            const bool kept = (uint64_t)p[j] < (uint64_t)n;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                sum.v[e] = kept ? fmaf(w[j], v[j].v[e], sum.v[e]) : sum.v[e];
+        }
     }
+    sum.store(out + t * d + c, d - c);
 }
 
 // Gradient of the weighted sum, a group of lanes a slot: d_rows[p] = w dy[t]
@@ -372,10 +441,16 @@ template <typename T>
 static hipError_t gather_as(const void *x, int64_t nvec, int d, const int32_t *order,
                             const float *weights, int k, void *rows, hipStream_t stream)
 {
-    const int lanes = row_lanes<T>(d);
-    hipLaunchKernelGGL(route_gather_kernel<T>, row_grid(nvec * k, lanes), dim3(256), 0, stream,
-                       static_cast<const T *>(x), nvec * k, d, lanes, FastDiv((uint32_t)k), order,
-                       weights, static_cast<T *>(rows));
+    const int64_t pieces = (d + Piece<T>::N - 1) / Piece<T>::N, n = nvec * k;
+    const int64_t step = (n + kRowsAtOnce - 1) / kRowsAtOnce;
+    const int64_t most = 0x7FFFFF00ll / pieces; // rows of one launch: 32-bit piece numbers
+    for (int64_t r = 0; r < step; r += most) {
+        const int64_t now = (step - r < most ? step - r : most) * pieces;
+        hipLaunchKernelGGL(route_gather_kernel<T>, dim3((unsigned)((now + 255) / 256)), dim3(256),
+                           0, stream, static_cast<const T *>(x), n, step, d,
+                           FastDiv((uint32_t)pieces), FastDiv((uint32_t)k), order, weights,
+                           static_cast<T *>(rows), r);
+    }
     return hipGetLastError();
 }
 
@@ -383,10 +458,14 @@ template <typename T>
 static hipError_t combine_as(const void *rows, int64_t nvec, int d, const int32_t *pos,
                              const float *weights, int k, void *out, hipStream_t stream)
 {
-    const int lanes = row_lanes<T>(d);
-    hipLaunchKernelGGL(route_combine_kernel<T>, row_grid(nvec, lanes), dim3(256), 0, stream,
-                       static_cast<const T *>(rows), nvec, d, lanes, k, pos, weights,
-                       static_cast<T *>(out));
+    const int64_t pieces = (d + Piece<T>::N - 1) / Piece<T>::N;
+    const int64_t most = 0x7FFFFF00ll / pieces;
+    for (int64_t r = 0; r < nvec; r += most) {
+        const int64_t now = (nvec - r < most ? nvec - r : most) * pieces;
+        hipLaunchKernelGGL(route_combine_kernel<T>, dim3((unsigned)((now + 255) / 256)), dim3(256),
+                           0, stream, static_cast<const T *>(rows), nvec, d,
+                           FastDiv((uint32_t)pieces), k, pos, weights, static_cast<T *>(out), r);
+    }
     return hipGetLastError();
 }
 

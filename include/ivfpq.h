@@ -466,8 +466,8 @@ ivfpq_status ivfpq_mx4_list_product_ex(const uint8_t *a_codes_dev, const uint8_t
  * All calls are asynchronous on `stream`, allocate nothing and may be captured
  * in a graph.  Rows are row-major and contiguous. */
 
-/* Bytes of device workspace for ivfpq_route_sort_ex; 0 for arguments that it
- * rejects. */
+/* Bytes of device workspace for ivfpq_route_sort_ex: 0 for small sorts, which
+ * need none, and for arguments that it rejects. */
 size_t ivfpq_route_sort_bytes(int64_t nvec, int k, int nlist);
 
 /* Stable sort of the slots by list: offsets_dev [nlist + 1] receives each
@@ -494,8 +494,8 @@ ivfpq_status ivfpq_route_gather_ex(const void *vectors_dev, int type, int64_t nv
 
 /* out_dev [nvec][d]: the sum over j of weights[t][j] (1 when weights_dev is
  * NULL) times row pos[t][j] of rows_dev [n][d], j ascending in float32, rounded
- * once; slots whose position is outside [0, n) are skipped and their rows never
- * read.  A vector without kept slots gets zeros.  Errors as above. */
+ * once; slots whose position is outside [0, n) add nothing, whatever the rows
+ * past the kept ones hold.  A vector without kept slots gets zeros.  Errors as above. */
 ivfpq_status ivfpq_route_combine_ex(const void *rows_dev, int type, int64_t nvec, int d,
                                     const int32_t *pos_dev, const float *weights_dev, int k,
                                     void *out_dev, void *stream);

@@ -40,7 +40,8 @@ def sort(lists, nlist):
     (1, 1, 1, 0.0, 0.0), (1, 8, 64, 0.0, 0.0), (3, 2, 5, 0.3, 0.0), (64, 1, 2, 0.0, 0.9),
     (100, 3, 1, 0.5, 0.0), (700, 3, 129, 0.1, 0.2), (683, 3, 7, 0.0, 0.0), (4097, 1, 8, 0.0, 1.0),
     (5000, 8, 1024, 0.02, 0.3), (9999, 1, 2047, 0.0, 0.0), (3000, 4, 2048, 0.1, 0.5),
-    (2500, 2, 100000, 0.1, 0.3), (500, 2, (1 << 22) - 1, 0.1, 0.1), (50, 4, 16, 1.0, 0.0),
+    (2500, 2, 100000, 0.1, 0.3), (500, 2, (1 << 22) - 1, 0.1, 0.1), (50, 4, 16, 1.0, 0.0), (16384, 1, 1087, 0.05, 0.1),
+    (16385, 1, 1087, 0.05, 0.1), (2000, 8, 1088, 0.0, 0.0), (5, 200, 3, 0.2, 0.0),
     (70000, 2, 3000, 0.01, 0.2)])
 def test_sort(t, k, nlist, drop, hot):
     lists = make_lists(np.random.default_rng(t * k + nlist), t, k, nlist, drop, hot)
@@ -53,13 +54,14 @@ def test_sort_empty_and_given_buffers():
     offsets, order, pos = A.ivfpq_route_sort_ex(torch.empty((0, 3), dtype=torch.int32,
                                                             device="cuda"), 5000)
     assert offsets.tolist() == [0] * 5001 and order.shape == (0,) and pos.shape == (0, 3)
-    lists = make_lists(np.random.default_rng(1), 333, 5, 20, 0.1)
+    lists = make_lists(np.random.default_rng(1), 3331, 5, 20, 0.1)
     t = torch.from_numpy(lists).cuda()
-    ws = torch.full((A.ivfpq_route_sort_bytes(333, 5, 20),), 0xA5, dtype=torch.uint8,
+    ws = torch.full((A.ivfpq_route_sort_bytes(3331, 5, 20),), 0xA5, dtype=torch.uint8,
                     device="cuda")
+    assert ws.numel() > 0
     out = (torch.full((21,), 9, dtype=torch.int32, device="cuda"),
-           torch.full((1665,), 9, dtype=torch.int32, device="cuda"),
-           torch.full((333, 5), 9, dtype=torch.int32, device="cuda"))
+           torch.full((16655,), 9, dtype=torch.int32, device="cuda"),
+           torch.full((3331, 5), 9, dtype=torch.int32, device="cuda"))
     got = A.ivfpq_route_sort_ex(t, 20, out=out, workspace=ws)
     for g, r in zip(got, R.route_sort(lists, 20)):
         assert np.array_equal(g.cpu().numpy(), r)

@@ -24,7 +24,7 @@ GOOD = {
     "ivfpq_mx4_dequantize_ex": [P, P, 4, 64, 0, P, None],
     "ivfpq_mx4_product_ex": [P, P, 4, P, P, 4, 64, 0, P, None],
     "ivfpq_mx4_list_product_ex": [P, P, 4, P, P, 2, 4, 64, P, P, 2, 8, 0, P, None],
-    "ivfpq_route_sort_ex": [P, 4, 2, 8, P, 4096, P, P, P, None],
+    "ivfpq_route_sort_ex": [P, 20000, 2, 8, P, 1 << 20, P, P, P, None],
     "ivfpq_route_gather_ex": [P, 0, 4, 8, P, P, 2, P, None],
     "ivfpq_route_combine_ex": [P, 0, 4, 8, P, P, 2, P, None],
     "ivfpq_route_combine_grad_ex": [P, P, 0, 4, 8, P, P, P, 2, P, P, None],
@@ -97,7 +97,8 @@ def test_nothing_to_do_is_ok(name, zero):
 
 
 def test_sort_workspace_size():
-    assert A.ivfpq_route_sort_bytes(100, 4, 64) > 0
+    assert A.ivfpq_route_sort_bytes(20000, 2, 8) > 0
+    assert A.ivfpq_route_sort_bytes(100, 4, 64) == 0   # a small sort needs none
     for bad in ((-1, 4, 64), (100, 0, 64), (1 << 30, 4, 64), (100, 4, 0), (100, 4, 1 << 22)):
         assert A.ivfpq_route_sort_bytes(*bad) == 0
 
