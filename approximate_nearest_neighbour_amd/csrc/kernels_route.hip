@@ -398,11 +398,25 @@ __global__ __launch_bounds__(256) void route_combine_kernel(const T *__restrict_
         int64_t p[kSlotsAtOnce];
         float w[kSlotsAtOnce];
         Piece<T> v[kSlotsAtOnce];
+        if (j0 + kSlotsAtOnce <= k) { // eight numbers in two loads, at any alignment
+            typedef int32_t I8 __attribute__((ext_vector_type(8), aligned(4)));
+            typedef float F8 __attribute__((ext_vector_type(8), aligned(4)));
+            const I8 pv = *reinterpret_cast<const I8 *>(pos + t * k + j0);
+            F8 wv = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+            if (weights)
+                wv = *reinterpret_cast<const F8 *>(weights + t * k + j0);
 #pragma unroll
-        for (int j = 0; j < kSlotsAtOnce; ++j) {
-            const int at = min(j0 + j, k - 1);
-            p[j] = j0 + j < k ? pos[t * k + at] : -1;
-            w[j] = weights ? weights[t * k + at] : 1.f;
+            for (int j = 0; j < kSlotsAtOnce; ++j) {
+                p[j] = pv[j];
+                w[j] = wv[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kSlotsAtOnce; ++j) {
+                const int at = min(j0 + j, k - 1);
+                p[j] = j0 + j < k ? pos[t * k + at] : -1;
+                w[j] = weights ? weights[t * k + at] : 1.f;
+            }
         }
         if (whole) {
 #pragma unroll
