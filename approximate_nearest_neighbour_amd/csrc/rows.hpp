@@ -43,6 +43,8 @@ struct Piece {
                 v[i] = i < valid ? (float)p[i] : 0.f;
         }
     }
+    // NT: past the caches, for rows that nothing reads soon
+    template <bool NT = false>
     __device__ __forceinline__ void store(T *p, int valid) const
     {
         if (valid >= N) {
@@ -50,7 +52,10 @@ struct Piece {
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 w[i] = (T)v[i];
-            *reinterpret_cast<V *>(p) = w;
+            if constexpr (NT)
+                __builtin_nontemporal_store(w, reinterpret_cast<V *>(p));
+            else
+                *reinterpret_cast<V *>(p) = w;
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i)
