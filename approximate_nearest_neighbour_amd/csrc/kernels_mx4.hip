@@ -302,8 +302,14 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_direct_kernel(Mx4Product p)
 // to the sums so that pairs of these are eight consecutive columns (deal_row),
 // and a store is 16 bytes.
 //
-// ONE: rows of at most one chunk (d <= 256) need no second LDS object, and
-// more workgroups fit a CU to overlap one's stores with another's loads.
+// A workgroup makes a run of tiles along n with the same rows of A: the next
+// tile's first chunk arrives while the last one of a tile is multiplied, and a
+// tile's stores are under way while the next is begun.
+//
+// ONE: rows of at most one chunk (d <= 256) and single tiles; the LDS is small
+// enough for three workgroups a CU, one storing while others load.  (Runs of
+// such tiles, B's chunks taking turns, were slower: a tile would wait for the
+// stores of the one before.)
 
 // A value that is the same in every lane, in scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t v)
@@ -317,7 +323,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t *base,
                                                             int64_t bytes)
 {
     from = uniform(from);
-    const uint32_t size = (uint32_t)uniform(min(bytes - from, (int64_t)0xFFFFFFFF));
+    const uint32_t size = (uint32_t)uniform(min(max(bytes - from, (int64_t)0), (int64_t)0xFFFFFFFF));
     const uint8_t *p = base + from;
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)size, 0x00027000);
 }
@@ -367,25 +373,28 @@ __device__ __forceinline__ int deal_row(int r)
 // for later than it is issued, so what depends on its position comes apart.
 struct ScaleBytes {
     u32x4 v;
+    int early; // bytes that the load began early
     // from byte `at` on, but never past `total` (at least 16): near the end it starts earlier
     __device__ __forceinline__ void load(const uint8_t *scales, int64_t at, int64_t total)
     {
         typedef uint32_t U __attribute__((ext_vector_type(4), aligned(1)));
-        v = *reinterpret_cast<const U *>(scales + min(at, total - 16));
+        const int64_t from = min(at, total - 16);
+        early = (int)(at - from);
+        v = *reinterpret_cast<const U *>(scales + from);
     }
-    // The eight bytes from `at` + 8 ODD on, with those past the first `left`
+    // The first eight of them (ODD: the others), those past the first `left`
     // zero: their blocks vanish from the sums (two factors of 2^-127) whatever
     // codes stand there.
     template <int ODD>
-    __device__ __forceinline__ uint64_t get(int64_t at, int64_t total, int left) const
+    __device__ __forceinline__ uint64_t get(int left) const
     {
-        const int early = (int)max(at - (total - 16), (int64_t)0) + 8 * ODD; // bytes to skip
+        const int skip = early + 8 * ODD;
         const uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
-        const uint64_t w = early < 8 ? lo : hi;
-        uint64_t r = w >> (8 * (early & 7));
-        r |= early > 0 && early < 8 ? hi << (64 - 8 * (early & 7)) : 0;
+        const uint64_t w = skip < 8 ? lo : hi;
+        uint64_t r = w >> (8 * (skip & 7));
+        r |= skip > 0 && skip < 8 ? hi << (64 - 8 * (skip & 7)) : 0;
         const uint64_t keep = left >= 8 ? ~0ull : left > 0 ? (1ull << (8 * left)) - 1 : 0;
-        return early < 16 ? r & keep : 0;
+        return skip < 16 ? r & keep : 0;
     }
 };
 
@@ -410,7 +419,7 @@ __device__ __forceinline__ void tile_of_block(uint32_t mt, uint32_t nt, uint32_t
 
 template <typename T, bool LIST, int WM, int WN, int MW, int NW, bool ONE>
 __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, uint32_t mtiles,
-                                                                uint32_t ntiles)
+                                                                uint32_t nruns, int most)
 {
     constexpr bool PAIR = sizeof(T) == 2;
     constexpr int WAVES = MW * NW, TM = 32 * WM * MW, TN = 32 * WN * NW;
@@ -423,207 +432,262 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, ui
 
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    uint32_t mt, nt;
-    tile_of_block(mtiles, ntiles, mt, nt);
-    const int n0 = (int)nt * TN;
+    uint32_t mt, nr;
+    tile_of_block(mtiles, nruns, mt, nr);
+    const int n0 = (int)nr * most * TN;
+    const int run = min(most, (p.n - n0 + TN - 1) / TN);
     ListTile tile{0, (int64_t)mt * TM, min((int64_t)mt * TM + TM, p.m)};
     if constexpr (LIST)
         tile = find_tile<TM>(p.offsets, p.nlist, p.m, mt);
     if (tile.p0 >= tile.p1)
         return;
+    tile.p0 = uniform(tile.p0);
     const int wm = wave % MW, wn = wave / MW;
     const int r = lane & 31, half = lane >> 5;
     T *out = static_cast<T *>(p.out);
 
     f32x16 acc[WM][WN];
+    auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < WM; ++i)
-#pragma unroll
-        for (int j = 0; j < WN; ++j)
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-                acc[i][j][q] = 0.f;
-
-    if (!LIST || tile.e < p.nlist) {
-        // rows past the tile's end repeat its last row; their results are not stored
-        auto a_row = [&](int row) -> int64_t {
-            int64_t q = min(tile.p0 + row, tile.p1 - 1);
-            if constexpr (LIST) {
-                if (p.order) {
-                    const int32_t slot = p.order[q];
-                    q = slot >= 0 ? slot / p.k : -1;
-                }
-                q = q >= 0 && q < p.arows ? q : 0;
-            }
-            return q;
-        };
-        auto b_row = [&](int row) -> int64_t {
-            return (LIST ? (int64_t)tile.e * p.n : 0) + min(n0 + row, p.n - 1);
-        };
-        // copies: instruction j of a wave brings rows 8 (WAVES j + wave) .. + 7, a lane one block
-        const int sub = lane >> 3;
-        const int blk = (lane & 7) ^ (((wave & 1) * 8 + sub) >> 1);
-        const int64_t arow0 = LIST && p.order ? 0 : tile.p0; // rows are counted from here
-        const int64_t brow0 = b_row(0);
-        uint32_t off[CA + CB]; // byte of the lane's block in its row's first chunk
-#pragma unroll
-        for (int j = 0; j < CA; ++j)
-            off[j] = (uint32_t)(a_row((j * WAVES + wave) * 8 + sub) - arow0) *
-                         (uint32_t)p.kb * 16 + blk * 16;
-#pragma unroll
-        for (int j = 0; j < CB; ++j)
-            off[CA + j] = (uint32_t)(b_row((j * WAVES + wave) * 8 + sub) - brow0) *
-                              (uint32_t)p.kb * 16 + blk * 16;
-        const auto abuf = buffer_of(p.a, arow0 * p.kb * 16, p.arows * p.kb * 16);
-        const auto bbuf = buffer_of(p.b, brow0 * p.kb * 16,
-                                    (LIST ? (int64_t)p.nlist : 1) * p.n * p.kb * 16);
-        const int chunks = (p.kb + 7) >> 3;
-        // Chunk c into its LDS object.  What lies past a row's end (the next
-        // row's blocks, or zeros past the matrix) is multiplied too, with
-        // exponent bytes of zero; past the last chunk nobody reads it.
-        auto fetch = [&](int c, uint8_t *to) {
-            to += wave * 1024;
-            const int at = __builtin_amdgcn_readfirstlane(c * 128);
-#pragma unroll
-            for (int j = 0; j < CA; ++j)
-                copy16_to_lds(abuf, off[j], at, to + j * WAVES * 1024);
-#pragma unroll
-            for (int j = 0; j < CB; ++j)
-                copy16_to_lds(bbuf, off[CA + j], at, to + TM * 128 + j * WAVES * 1024);
-        };
-        // exponent bytes: a thread per row of A, then of B
-        const int srow = (int)threadIdx.x;
-        const bool of_a = srow < TM;
-        const uint8_t *sfrom = of_a ? p.as : p.bs;
-        const int64_t sat = (of_a ? a_row(srow) : b_row(min(srow - TM, TN - 1))) * p.kb;
-        const int64_t stotal = of_a ? p.arows * p.kb : (LIST ? (int64_t)p.nlist : 1) * p.n * p.kb;
-        ScaleBytes bytes;
-        auto load_scales = [&](int c) { // chunks c and c + 1
-            bytes.load(sfrom, sat + min(c, chunks - 1) * 8, stotal);
-        };
-        auto put_scales = [&](int c, auto odd) { // chunk c, whose number is odd or not
-            constexpr int ODD = decltype(odd)::value;
-            const uint64_t v = bytes.get<ODD>(sat + (c - ODD) * 8, stotal, p.kb - c * 8);
-            if (TM + TN == 64 * WAVES || srow < TM + TN) {
-                const uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
-                scale[ODD][0][srow] = __builtin_amdgcn_perm(hi, lo, 0x06040200);
-                scale[ODD][1][srow] = __builtin_amdgcn_perm(hi, lo, 0x07050301);
-            }
-        };
-        // operand reads: step s takes blocks 2 s and 2 s + 1, one a half wave
-        const int brow = deal_row<PAIR>(r);
-        int aoff[4], boff[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            aoff[s] = wm * WM * 4096 + r * 128 + (((2 * s + half) ^ ((r >> 1) & 7)) * 16);
-            boff[s] = TM * 128 + wn * WN * 4096 + brow * 128 +
-                      (((2 * s + half) ^ ((brow >> 1) & 7)) * 16);
-        }
-        const int sa_at = wm * WM * 32 + r, sb_at = TM + wn * WN * 32 + brow;
-        struct Operands {
-            i32x4 a[WM], b[WN];
-        };
-        auto read = [&](const uint8_t *from, int s, Operands &o) {
-#pragma unroll
-            for (int i = 0; i < WM; ++i)
-                o.a[i] = *reinterpret_cast<const i32x4 *>(from + aoff[s] + i * 4096);
+        for (int i = 0; i < WM; ++i)
 #pragma unroll
             for (int j = 0; j < WN; ++j)
-                o.b[j] = *reinterpret_cast<const i32x4 *>(from + boff[s] + j * 4096);
-        };
-        constexpr std::integral_constant<int, 0> even{};
-        constexpr std::integral_constant<int, 1> odd{};
-        // Chunk c, lying in `here`, while the next one is copied into `next`.
-        auto chunk = [&](int c, auto parity, const uint8_t *here, uint8_t *next) {
-            constexpr int ODD = decltype(parity)::value;
-            wait_vm<0>();  // this chunk and the next one's exponent bytes are here,
-            lds_barrier(); // and every wave is done with `next`
-            Operands o[2];
-            uint32_t sa[WM], sb[WN];
-            read(here, 0, o[0]);
 #pragma unroll
-            for (int i = 0; i < WM; ++i)
-                sa[i] = scale[ODD][half][sa_at + i * 32];
+                for (int q = 0; q < 16; ++q)
+                    acc[i][j][q] = 0.f;
+    };
+    // the sums to the tile's rows, columns at and on
+    auto put = [&](int at) {
+        at += wn * WN * 32;
+        // not known to be the same from tile to tile, or every address of the
+        // sums is computed once and kept in registers through the products
+        int64_t row0 = tile.p0;
+        __asm__ volatile("" : "+s"(row0));
+        if constexpr (!PAIR) {
 #pragma unroll
-            for (int j = 0; j < WN; ++j)
-                sb[j] = scale[ODD][half][sb_at + j * 32];
-            __builtin_amdgcn_sched_barrier(0);
-            if constexpr (!ONE) {
-                fetch(c + 1, next);
-                if constexpr (ODD) {
-                    put_scales(c + 1, even);
-                } else {
-                    put_scales(c + 1, odd);
-                    load_scales(c + 2);
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (s < 3)
-                    read(here, s + 1, o[(s + 1) & 1]);
+            for (int j = 0; j < WN; ++j) {
+                const int n = at + j * 32 + r;
+                if (n >= p.n)
+                    continue;
 #pragma unroll
                 for (int i = 0; i < WM; ++i)
 #pragma unroll
-                    for (int j = 0; j < WN; ++j)
-                        acc[i][j] = PAIR ? mfma_mx4_32(o[s & 1].b[j], sb[j], o[s & 1].a[i], sa[i],
-                                                       s, acc[i][j])
-                                         : mfma_mx4_32(o[s & 1].a[i], sa[i], o[s & 1].b[j], sb[j],
-                                                       s, acc[i][j]);
-                __builtin_amdgcn_sched_barrier(0);
+                    for (int q = 0; q < 16; ++q) {
+                        const int64_t row =
+                            row0 + (wm * WM + i) * 32 + (q >> 2) * 8 + half * 4 + (q & 3);
+                        if (row < tile.p1)
+                            out[row * p.n + n] = (T)acc[i][j][q];
+                    }
             }
-        };
-        load_scales(0);
-        fetch(0, code0);
-        put_scales(0, even);
-        if constexpr (ONE) {
-            chunk(0, even, code0, code1);
         } else {
-#pragma unroll 1
-            for (int c = 0; c < chunks; c += 2) {
-                chunk(c, even, code0, code1);
-                if (c + 1 < chunks)
-                    chunk(c + 1, odd, code1, code0);
+#pragma unroll
+            for (int i = 0; i < WM; ++i) {
+                const int64_t row = row0 + (wm * WM + i) * 32 + r;
+                if (row >= tile.p1)
+                    continue;
+#pragma unroll
+                for (int j = 0; j < WN; ++j)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int n = at + j * 32 + 16 * q + 8 * half;
+                        Piece<T> o;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o.v[e] = acc[i][j][q * 8 + e];
+                        o.store(out + row * p.n + n, p.n - n);
+                    }
             }
         }
-        // copies still under way must not outlive the workgroup's LDS
-        wait_vm<0>();
+    };
+    clear();
+    if (LIST && tile.e == p.nlist) {
+        for (int t = 0; t < run; ++t)
+            put(n0 + t * TN);
+        return;
     }
-    if constexpr (!PAIR) {
+
+    // rows past the tile's end repeat its last row; their results are not stored
+    auto a_row = [&](int row) -> int64_t {
+        int64_t q = min(tile.p0 + row, tile.p1 - 1);
+        if constexpr (LIST) {
+            if (p.order) {
+                const int32_t slot = p.order[q];
+                q = slot >= 0 ? slot / p.k : -1;
+            }
+            q = q >= 0 && q < p.arows ? q : 0;
+        }
+        return q;
+    };
+    // copies: instruction j of a wave brings rows 8 (WAVES j + wave) .. + 7, a lane one block
+    const int sub = lane >> 3;
+    const int blk = (lane & 7) ^ (((wave & 1) * 8 + sub) >> 1);
+    const int64_t arow0 = LIST && p.order ? 0 : tile.p0; // rows are counted from here
+    const int64_t brow0 = (LIST ? (int64_t)tile.e * p.n : 0) + n0;
+    const int64_t brows = (LIST ? (int64_t)p.nlist : 1) * p.n;
+    uint32_t off[CA + CB]; // byte of the lane's block in its row's first chunk
 #pragma unroll
-        for (int j = 0; j < WN; ++j) {
-            const int n = n0 + (wn * WN + j) * 32 + r;
-            if (n >= p.n)
-                continue;
+    for (int j = 0; j < CA; ++j)
+        off[j] = (uint32_t)(a_row((j * WAVES + wave) * 8 + sub) - arow0) * (uint32_t)p.kb * 16 +
+                 blk * 16;
+#pragma unroll
+    for (int j = 0; j < CB; ++j)
+        off[CA + j] = (uint32_t)((j * WAVES + wave) * 8 + sub) * (uint32_t)p.kb * 16 + blk * 16;
+    const auto abuf = buffer_of(p.a, arow0 * p.kb * 16, p.arows * p.kb * 16);
+    auto b_of = [&](int t) { // B's rows from tile t of the run on
+        return buffer_of(p.b, (brow0 + t * TN) * p.kb * 16, brows * p.kb * 16);
+    };
+    const int chunks = (p.kb + 7) >> 3;
+    // Chunk c into its LDS place.  What lies past a row's end (the next row's
+    // blocks, or zeros past the matrix) is multiplied too, with exponent bytes
+    // of zero; rows past the last one of B give results that are not stored.
+    auto fetch_a = [&](int c, uint8_t *to) {
+        const int at = __builtin_amdgcn_readfirstlane(c * 128);
+#pragma unroll
+        for (int j = 0; j < CA; ++j)
+            copy16_to_lds(abuf, off[j], at, to + wave * 1024 + j * WAVES * 1024);
+    };
+    auto fetch_b = [&](__amdgpu_buffer_rsrc_t from, int c, uint8_t *to) {
+        const int at = __builtin_amdgcn_readfirstlane(c * 128);
+#pragma unroll
+        for (int j = 0; j < CB; ++j)
+            copy16_to_lds(from, off[CA + j], at, to + wave * 1024 + j * WAVES * 1024);
+    };
+    // exponent bytes: a thread per row of A, then of B
+    const int srow = (int)threadIdx.x;
+    const bool of_a = srow < TM;
+    const uint8_t *sfrom = of_a ? p.as : p.bs;
+    const int64_t sline = of_a ? a_row(srow) : brow0 + srow - TM;
+    const int64_t slast = (of_a ? p.arows : brows) - 1;
+    ScaleBytes bytes;
+    auto load_scales = [&](int t, int c) { // chunks c and c + 1 of tile t
+        const int64_t line = min(of_a ? sline : sline + t * TN, slast);
+        bytes.load(sfrom, line * p.kb + min(c, chunks - 1) * 8, (slast + 1) * p.kb);
+    };
+    auto put_scales = [&](int c, auto odd) { // chunk c, the first or the other one loaded
+        constexpr int ODD = decltype(odd)::value;
+        const uint64_t v = bytes.get<ODD>(p.kb - c * 8);
+        if (TM + TN == 64 * WAVES || srow < TM + TN) {
+            const uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
+            scale[ODD][0][srow] = __builtin_amdgcn_perm(hi, lo, 0x06040200);
+            scale[ODD][1][srow] = __builtin_amdgcn_perm(hi, lo, 0x07050301);
+        }
+    };
+    // operand reads: step s takes blocks 2 s and 2 s + 1, one a half wave
+    const int brow = deal_row<PAIR>(r);
+    int aoff[4], boff[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        aoff[s] = wm * WM * 4096 + r * 128 + (((2 * s + half) ^ ((r >> 1) & 7)) * 16);
+        boff[s] = wn * WN * 4096 + brow * 128 + (((2 * s + half) ^ ((brow >> 1) & 7)) * 16);
+    }
+    const int sa_at = wm * WM * 32 + r, sb_at = TM + wn * WN * 32 + brow;
+    struct Operands {
+        i32x4 a[WM], b[WN];
+    };
+    auto read = [&](const uint8_t *froma, const uint8_t *fromb, int s, Operands &o) {
+#pragma unroll
+        for (int i = 0; i < WM; ++i)
+            o.a[i] = *reinterpret_cast<const i32x4 *>(froma + aoff[s] + i * 4096);
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+            o.b[j] = *reinterpret_cast<const i32x4 *>(fromb + boff[s] + j * 4096);
+    };
+    constexpr std::integral_constant<int, 0> even{};
+    constexpr std::integral_constant<int, 1> odd{};
+    // The chunk that lies in the places given, while `copies` brings the next
+    // one and `scales` its exponent bytes.
+    auto chunk = [&](auto parity, const uint8_t *froma, const uint8_t *fromb, auto copies,
+                     auto scales) {
+        constexpr int ODD = decltype(parity)::value;
+        lds_barrier(); // every wave's part of this chunk is here, and its last reads done
+        Operands o[2];
+        uint32_t sa[WM], sb[WN];
+        read(froma, fromb, 0, o[0]);
+#pragma unroll
+        for (int i = 0; i < WM; ++i)
+            sa[i] = scale[ODD][half][sa_at + i * 32];
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+            sb[j] = scale[ODD][half][sb_at + j * 32];
+        __builtin_amdgcn_sched_barrier(0);
+        copies();
+        scales();
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (s < 3)
+                read(froma, fromb, s + 1, o[(s + 1) & 1]);
 #pragma unroll
             for (int i = 0; i < WM; ++i)
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const int64_t row =
-                        tile.p0 + (wm * WM + i) * 32 + (q >> 2) * 8 + half * 4 + (q & 3);
-                    if (row < tile.p1)
-                        out[row * p.n + n] = (T)acc[i][j][q];
-                }
+                for (int j = 0; j < WN; ++j)
+                    acc[i][j] = PAIR ? mfma_mx4_32(o[s & 1].b[j], sb[j], o[s & 1].a[i], sa[i], s,
+                                                   acc[i][j])
+                                     : mfma_mx4_32(o[s & 1].a[i], sa[i], o[s & 1].b[j], sb[j], s,
+                                                   acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        return;
-    }
-    constexpr int N = Piece<T>::N;
-#pragma unroll
-    for (int i = 0; i < WM; ++i) {
-        const int64_t row = tile.p0 + (wm * WM + i) * 32 + r;
-        if (row >= tile.p1)
-            continue;
-#pragma unroll
-        for (int j = 0; j < WN; ++j)
-#pragma unroll
-            for (int q = 0; q < 16 / N; ++q) {
-                const int n = n0 + (wn * WN + j) * 32 + 2 * N * q + N * half;
-                Piece<T> o;
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    o.v[e] = acc[i][j][q * N + e];
-                o.store(out + row * p.n + n, p.n - n);
+        wait_vm<0>(); // the next chunk (and what was stored before this one)
+    };
+    auto bnow = b_of(0);
+    load_scales(0, 0);
+    fetch_a(0, code0);
+    fetch_b(bnow, 0, code0 + TM * 128);
+    put_scales(0, even);
+    if constexpr (ONE) {
+        wait_vm<0>();
+        chunk(even, code0, code0 + TM * 128, [] {}, [] {});
+        put(n0);
+    } else {
+        wait_vm<0>();
+#pragma unroll 1
+        for (int t = 0; t < run; ++t) { // more than one only if a row's chunks are even in number
+            const auto bnext = b_of(t + 1);
+#pragma unroll 1
+            for (int c = 0; c < chunks; c += 2) {
+                const bool last = c + 2 >= chunks;
+                const int after = last ? 0 : c + 2;
+                chunk(
+                    even, code0, code0 + TM * 128,
+                    [&] {
+                        fetch_a(c + 1, code1);
+                        fetch_b(bnow, c + 1, code1 + TM * 128);
+                    },
+                    [&] {
+                        put_scales(c + 1, odd);
+                        load_scales(last ? t + 1 : t, after);
+                    });
+                if (c + 1 < chunks)
+                    chunk(
+                        odd, code1, code1 + TM * 128,
+                        [&] {
+                            fetch_a(after, code0);
+                            fetch_b(last ? bnext : bnow, after, code0 + TM * 128);
+                        },
+                        [&] { put_scales(after, even); });
             }
+            bnow = bnext;
+            put(n0 + t * TN);
+            clear();
+        }
     }
+}
+
+// Tiles of a run: of 1, 2, 4 and 8 the one that ends first when `slots`
+// workgroups are under way together, a tile taking its chunks and a run as
+// long again as about three chunks (first copies, last stores).
+static int run_length(int64_t mt, int64_t nt, int chunks, int64_t slots)
+{
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int run = 1; run <= 8 && (run == 1 || chunks % 2 == 0); run *= 2) {
+        const int64_t rounds = (mt * ((nt + run - 1) / run) + slots - 1) / slots;
+        const int64_t cost = rounds * ((int64_t)run * (chunks + 1) + 3);
+        if (cost < least) {
+            least = cost;
+            best = run;
+        }
+    }
+    return best;
 }
 
 template <typename T, bool LIST, int WM, int WN, int MW, int NW, bool ONE = false>
@@ -634,8 +698,11 @@ static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
     int64_t mt = (p.m + TM - 1) / TM;
     if (LIST) // every list may end inside a tile, and so may the last rows
         mt = p.m / TM + (p.m < (int64_t)p.nlist + 1 ? p.m : (int64_t)p.nlist + 1);
-    hipLaunchKernelGGL((mx4_tile_kernel<T, LIST, WM, WN, MW, NW, ONE>), dim3((unsigned)(nt * mt)),
-                       dim3(64 * MW * NW), 0, stream, p, (uint32_t)mt, (uint32_t)nt);
+    const int run = ONE ? 1 : run_length(mt, nt, (p.kb + 7) / 8, MW * NW == 8 ? 256 : 512);
+    const int64_t nruns = (nt + run - 1) / run;
+    hipLaunchKernelGGL((mx4_tile_kernel<T, LIST, WM, WN, MW, NW, ONE>),
+                       dim3((unsigned)(nruns * mt)), dim3(64 * MW * NW), 0, stream, p, (uint32_t)mt,
+                       (uint32_t)nruns, run);
     return hipGetLastError();
 }
 
