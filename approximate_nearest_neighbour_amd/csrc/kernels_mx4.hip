@@ -218,17 +218,22 @@ __device__ __forceinline__ f32x4 mfma_mx4(i32x4 a, uint32_t sa, i32x4 b, uint32_
                                                             (int)sa, 0, (int)sb);
 }
 
-// One workgroup: 16 rows of A by 16 rows of B, its waves splitting the blocks
-// of a row between them and joining their sums through LDS.
-template <typename T, bool LIST, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void mx4_direct_kernel(Mx4Product p)
+// Few rows of A: bound by the bytes of B, which go from memory straight to
+// registers.  A wave forms 16 rows by 16 columns; of a workgroup's eight, KS
+// share the blocks of the same columns out between them and join their sums
+// through LDS.  Sixteen blocks a turn, a lane group g taking blocks 4 s + g of
+// the four steps s (64 bytes side by side a row and step); the next turn's
+// operands are under way while this one's are multiplied.  The exponent bytes
+// of a turn are one 16-byte load, of which word s, byte g is the lane's.
+template <typename T, bool LIST, int KS>
+__global__ __launch_bounds__(512) void mx4_direct_kernel(Mx4Product p, uint32_t ntiles)
 {
-    __shared__ f32x4 part[WAVES][64];
+    constexpr int GROUPS = 8 / KS;
+    __shared__ f32x4 part[KS == 1 ? 1 : 8][64];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const uint32_t nt = ((uint32_t)p.n + 15) / 16;
-    const uint32_t mt = blockIdx.x / nt;
-    const int n0 = (int)(blockIdx.x - mt * nt) * 16;
+    const uint32_t mt = blockIdx.x / ntiles;
+    const int n0 = ((int)(blockIdx.x - mt * ntiles) * GROUPS + wave / KS) * 16;
     ListTile tile{0, (int64_t)mt * 16, min((int64_t)mt * 16 + 16, p.m)};
     if constexpr (LIST)
         tile = find_tile<16>(p.offsets, p.nlist, p.m, mt);
@@ -237,6 +242,8 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_direct_kernel(Mx4Product p)
     const int r = lane & 15, g = lane >> 4;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     if (tile.e < p.nlist || !LIST) {
+        const int64_t brow = (LIST ? (int64_t)tile.e * p.n : 0) + min(n0 + r, p.n - 1);
+        const uint8_t *b = p.b + brow * p.kb * 16, *bs = p.bs + brow * p.kb;
         // rows past the tile's end repeat its last row; their results are not stored
         int64_t arow = min(tile.p0 + r, tile.p1 - 1);
         if constexpr (LIST) {
@@ -247,37 +254,78 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_direct_kernel(Mx4Product p)
             if (arow >= p.arows || arow < 0)
                 arow = 0;
         }
-        const int64_t brow = (LIST ? (int64_t)tile.e * p.n : 0) + min(n0 + r, p.n - 1);
         const uint8_t *a = p.a + arow * p.kb * 16, *as = p.as + arow * p.kb;
-        const uint8_t *b = p.b + brow * p.kb * 16, *bs = p.bs + brow * p.kb;
-        for (int k0 = wave * 4; k0 < p.kb; k0 += 4 * WAVES) {
-            const int k = k0 + g;
-            i32x4 va = {0, 0, 0, 0}, vb = {0, 0, 0, 0};
-            uint32_t sa = 127, sb = 127;
-            if (k < p.kb) {
-                va = *reinterpret_cast<const i32x4 *>(a + (int64_t)k * 16);
-                vb = *reinterpret_cast<const i32x4 *>(b + (int64_t)k * 16);
-                sa = as[k];
-                sb = bs[k];
+        struct Turn {
+            i32x4 b[4], a[4];
+            u32x4 sb, sa;
+        };
+        auto load = [&](int k0, Turn &t) {
+            typedef uint32_t U __attribute__((ext_vector_type(4), aligned(1)));
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int64_t at = (int64_t)min(k0 + 4 * s + g, p.kb - 1) * 16;
+                t.b[s] = *reinterpret_cast<const i32x4 *>(b + at);
+                t.a[s] = *reinterpret_cast<const i32x4 *>(a + at);
             }
-            acc = mfma_mx4(vb, sb, va, sa, acc);
+            if (k0 + 16 <= p.kb) {
+                t.sb = *reinterpret_cast<const U *>(bs + k0) >> (8 * g);
+                t.sa = *reinterpret_cast<const U *>(as + k0) >> (8 * g);
+            } else { // the row's end: bytes of zero past it (two factors of 2^-127)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int k = k0 + 4 * s + g;
+                    t.sb[s] = k < p.kb ? bs[k] : 0;
+                    t.sa[s] = k < p.kb ? as[k] : 0;
+                }
+            }
+        };
+        auto multiply = [&](const Turn &t) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                acc = mfma_mx4(t.b[s], t.sb[s], t.a[s], t.sa[s], acc);
+        };
+        int k0 = wave % KS * 16;
+        Turn x, y;
+        if (k0 < p.kb)
+            load(k0, x);
+        for (; k0 < p.kb; k0 += 32 * KS) {
+            if (k0 + 16 * KS < p.kb)
+                load(k0 + 16 * KS, y);
+            multiply(x);
+            if (k0 + 16 * KS >= p.kb)
+                break;
+            if (k0 + 32 * KS < p.kb)
+                load(k0 + 32 * KS, x);
+            multiply(y);
         }
     }
-    part[wave][lane] = acc;
-    __syncthreads();
-    if (wave != 0)
-        return;
+    if constexpr (KS > 1) {
+        part[wave][lane] = acc;
+        __syncthreads();
+        if (wave % KS != 0)
+            return;
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w)
-        acc += part[w][lane];
+        for (int w = 1; w < KS; ++w)
+            acc += part[wave + w][lane];
+    }
+    typedef T V __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+    const int n = n0 + 4 * g;
     const int64_t row = tile.p0 + r;
-    if (row >= tile.p1)
+    if (row >= tile.p1 || n >= p.n)
         return;
-    T *out = static_cast<T *>(p.out) + row * p.n + n0 + 4 * g;
+    T *out = static_cast<T *>(p.out) + row * p.n + n;
+    if (n + 4 <= p.n) {
+        V v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (n0 + 4 * g + i < p.n)
-            out[i] = (T)acc[i];
+        for (int i = 0; i < 4; ++i)
+            v[i] = (T)acc[i];
+        *reinterpret_cast<V *>(out) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.n)
+                out[i] = (T)acc[i];
+    }
 }
 
 // Large tiles.
@@ -713,35 +761,61 @@ static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <typename T>
-static hipError_t product_as(const Mx4Product &p, hipStream_t stream)
+template <typename T, bool LIST, int KS>
+static hipError_t direct_as(const Mx4Product &p, int64_t mt, hipStream_t stream)
 {
-    const int64_t brows = (p.offsets ? (int64_t)p.nlist : 1) * p.n;
-    const bool far = p.order && p.arows * p.kb * 16 >= (int64_t)1 << 32;
-    if (p.m > 64 && brows * p.kb >= 16 && p.arows * p.kb >= 16 && !far) {
-        if (p.offsets) {
-            if (p.m >= 256ll * p.nlist)
-                return tiles_as<T, true, 4, 2, 2, 4>(p, stream);
-            return tiles_as<T, true, 2, 2, 2, 2>(p, stream);
-        }
+    const int64_t nt = (p.n + 16ll * 8 / KS - 1) / (16 * 8 / KS);
+    hipLaunchKernelGGL((mx4_direct_kernel<T, LIST, KS>), dim3((unsigned)(nt * mt)), dim3(512), 0,
+                       stream, p, (uint32_t)nt);
+    return hipGetLastError();
+}
+
+// Which kernel.  The direct one reads B once for every 16 rows of A, the tiles
+// once for 128 or 256, but they take 13 us and more for their chunks one after
+// the other (d 4096).  So the direct one where a matrix has few rows to
+// multiply, or all is small: 32 rows by 8192, d 4096 (11.5 us, tiles 13.7 us) is
+// about the limit (48 rows: 15.7 and 13.8 us).  In lists of 8 rows on average
+// 33 us against 40 us (64 lists, 2048 x 2048), in lists of 16 49 us against 39 us.
+template <typename T, bool LIST>
+static hipError_t product_of(const Mx4Product &p, hipStream_t stream)
+{
+    int64_t mt = (p.m + 15) / 16;
+    if (LIST) // every list may end inside a tile, and so may the last rows
+        mt = p.m / 16 + (p.m < (int64_t)p.nlist + 1 ? p.m : (int64_t)p.nlist + 1);
+    const int64_t waves = mt * (((int64_t)p.n + 15) / 16);
+    const int64_t brows = (LIST ? (int64_t)p.nlist : 1) * p.n;
+    // what the tiles' 32-bit offsets and 16-byte reads of exponent bytes take
+    const bool fits = !(LIST && p.order && p.arows * p.kb * 16 >= (int64_t)1 << 32) &&
+                      brows * p.kb >= 16 && p.arows * p.kb >= 16;
+    const bool few = LIST ? p.m <= 8ll * p.nlist : p.m <= 16 || waves * p.kb <= 1024 * 128;
+    if (few || !fits) {
+        // blocks of a row are split only as far as it takes to have 16 waves a
+        // CU, with 8 KB each under way, or a turn for each
+        if (waves >= 4096 || p.kb <= 16)
+            return direct_as<T, LIST, 1>(p, mt, stream);
+        if (waves >= 1024 || p.kb <= 64)
+            return direct_as<T, LIST, 4>(p, mt, stream);
+        return direct_as<T, LIST, 8>(p, mt, stream);
+    }
+    if constexpr (LIST) {
+        // large tiles once the lists fill them: 512 rows a list 275 us against
+        // 328 us, 97 rows 20 us against 14 us
+        if (p.m >= 256ll * p.nlist)
+            return tiles_as<T, true, 4, 2, 2, 4>(p, stream);
+        return tiles_as<T, true, 2, 2, 2, 2>(p, stream);
+    } else {
         if (p.kb <= 8)
             return tiles_as<T, false, 1, 1, 2, 4, true>(p, stream);
         if (p.m > 1024)
             return tiles_as<T, false, 4, 2, 2, 4>(p, stream);
         return tiles_as<T, false, 2, 2, 2, 2>(p, stream);
     }
-    const int64_t nt = ((int64_t)p.n + 15) / 16;
-    int64_t mt = (p.m + 15) / 16;
-    if (p.offsets) // every list may end inside a tile, and so may the last rows
-        mt = p.m / 16 + (p.m < (int64_t)p.nlist + 1 ? p.m : (int64_t)p.nlist + 1);
-    if (nt * mt > 0x7FFFFFFFll)
-        return hipErrorInvalidValue;
-    const dim3 grid((unsigned)(nt * mt));
-    if (p.offsets)
-        hipLaunchKernelGGL((mx4_direct_kernel<T, true, 4>), grid, dim3(256), 0, stream, p);
-    else
-        hipLaunchKernelGGL((mx4_direct_kernel<T, false, 4>), grid, dim3(256), 0, stream, p);
-    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t product_as(const Mx4Product &p, hipStream_t stream)
+{
+    return p.offsets ? product_of<T, true>(p, stream) : product_of<T, false>(p, stream);
 }
 
 hipError_t launch_mx4_product(const Mx4Product &p, int type, hipStream_t stream)
