@@ -463,13 +463,15 @@ def _out(out, shape, dtype, device) -> torch.Tensor:
 
 
 def _mx4(pair, dims: int):
+    """Checked (codes, scales, shape of scales) of 4-bit rows."""
     codes, scales = pair
     _dev(codes, torch.uint8)
     _dev(scales, torch.uint8)
-    if codes.dim() != dims or codes.shape[:-1] != scales.shape[:-1] or scales.dim() != dims or \
-            codes.shape[-1] != 16 * scales.shape[-1] or scales.shape[-1] < 1:
+    c, s = codes.shape, scales.shape
+    if len(c) != dims or len(s) != dims or c[0] != s[0] or c[dims - 2] != s[dims - 2] or \
+            c[dims - 1] != 16 * s[dims - 1] or s[dims - 1] < 1:
         raise ValueError("expected 4-bit rows: codes [..., n, 16 kb] and scales [..., n, kb]")
-    return codes, scales
+    return codes, scales, s
 
 
 def ivfpq_mx4_quantize_ex(x: torch.Tensor, out=None, stream=None):
@@ -494,12 +496,12 @@ def ivfpq_mx4_dequantize_ex(codes: torch.Tensor, scales: torch.Tensor, d: int,
                             dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """The values [n, d] that 4-bit rows stand for."""
     kind = _row_type(dtype)
-    codes, scales = _mx4((codes, scales), 2)
-    if d < 1 or (d + 31) // 32 != scales.shape[1]:
+    codes, scales, (n, kb) = _mx4((codes, scales), 2)
+    if d < 1 or (d + 31) // 32 != kb:
         raise ValueError("d does not fit the rows' blocks")
-    out = _out(out, (codes.shape[0], d), dtype, codes.device)
-    _check(lib().ivfpq_mx4_dequantize_ex(_ptr(codes), _ptr(scales), codes.shape[0], d, kind,
-                                         _ptr(out), _raw_stream(stream)))
+    out = _out(out, (n, d), dtype, codes.device)
+    _check(lib().ivfpq_mx4_dequantize_ex(codes.data_ptr(), scales.data_ptr(), n, d, kind,
+                                         out.data_ptr(), _raw_stream(stream)))
     return out
 
 
@@ -507,13 +509,13 @@ def ivfpq_mx4_product_ex(a, b, dtype=torch.float32, out=None, stream=None) -> to
     """A B^T of 4-bit rows a = (codes, scales) of [m, d] and b of [n, d]:
     [m, n] of dtype, summed in float32."""
     kind = _row_type(dtype)
-    (ac, as_), (bc, bs) = _mx4(a, 2), _mx4(b, 2)
-    if as_.shape[1] != bs.shape[1]:
+    (ac, as_, (m, kb)), (bc, bs, (n, kb_b)) = _mx4(a, 2), _mx4(b, 2)
+    if kb != kb_b:
         raise ValueError("the operands' rows have different lengths")
-    m, n = ac.shape[0], bc.shape[0]
     out = _out(out, (m, n), dtype, ac.device)
-    _check(lib().ivfpq_mx4_product_ex(_ptr(ac), _ptr(as_), m, _ptr(bc), _ptr(bs), n,
-                                      32 * as_.shape[1], kind, _ptr(out), _raw_stream(stream)))
+    _check(lib().ivfpq_mx4_product_ex(ac.data_ptr(), as_.data_ptr(), m, bc.data_ptr(),
+                                      bs.data_ptr(), n, 32 * kb, kind, out.data_ptr(),
+                                      _raw_stream(stream)))
     return out
 
 
@@ -525,20 +527,19 @@ def ivfpq_mx4_list_product_ex(a, b, offsets: torch.Tensor, order: torch.Tensor =
     of a, without it row p.  Returns [rows, n] of dtype, zero past
     offsets[nlist]."""
     kind = _row_type(dtype)
-    (ac, as_), (bc, bs) = _mx4(a, 2), _mx4(b, 3)
+    (ac, as_, (arows, kb)), (bc, bs, (nlist, n, kb_b)) = _mx4(a, 2), _mx4(b, 3)
     offsets = _dev(offsets, torch.int32)
-    nlist, n = bc.shape[:2]
-    if as_.shape[1] != bs.shape[2]:
+    if kb != kb_b:
         raise ValueError("the operands' rows have different lengths")
     if offsets.shape != (nlist + 1,):
         raise ValueError("expected offsets [nlist + 1]")
     if order is not None and _dev(order, torch.int32).dim() != 1:
         raise ValueError("expected order [rows]")
-    rows = ac.shape[0] if order is None else order.shape[0]
+    rows = arows if order is None else order.shape[0]
     out = _out(out, (rows, n), dtype, ac.device)
-    _check(lib().ivfpq_mx4_list_product_ex(_ptr(ac), _ptr(as_), ac.shape[0], _ptr(bc), _ptr(bs),
-                                           nlist, n, 32 * as_.shape[1], _ptr(offsets),
-                                           _ptr(order), k, rows, kind, _ptr(out),
+    _check(lib().ivfpq_mx4_list_product_ex(ac.data_ptr(), as_.data_ptr(), arows, bc.data_ptr(),
+                                           bs.data_ptr(), nlist, n, 32 * kb, offsets.data_ptr(),
+                                           _ptr(order), k, rows, kind, out.data_ptr(),
                                            _raw_stream(stream)))
     return out
 

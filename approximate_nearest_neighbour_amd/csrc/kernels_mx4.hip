@@ -797,19 +797,20 @@ static hipError_t product_of(const Mx4Product &p, hipStream_t stream)
             return direct_as<T, LIST, 4>(p, mt, stream);
         return direct_as<T, LIST, 8>(p, mt, stream);
     }
-    if constexpr (LIST) {
-        // large tiles once the lists fill them: 512 rows a list 275 us against
-        // 328 us, 97 rows 20 us against 14 us
-        if (p.m >= 256ll * p.nlist)
-            return tiles_as<T, true, 4, 2, 2, 4>(p, stream);
-        return tiles_as<T, true, 2, 2, 2, 2>(p, stream);
-    } else {
+    // Large tiles (256 x 256) take about three times as long as small ones (128 x
+    // 128) a round of 256: 40 us against 14 us a quarter of the results (d 4096).
+    auto rounds = [&](int64_t size) {
+        const int64_t parts = LIST ? (p.m < p.nlist ? p.m : p.nlist) / 2 : 0; // lists end inside
+        return (((p.m + size - 1) / size + parts) * ((p.n + size - 1) / size) + 255) / 256;
+    };
+    const bool large = 3 * rounds(256) <= rounds(128);
+    if constexpr (!LIST) {
         if (p.kb <= 8)
             return tiles_as<T, false, 1, 1, 2, 4, true>(p, stream);
-        if (p.m > 1024)
-            return tiles_as<T, false, 4, 2, 2, 4>(p, stream);
-        return tiles_as<T, false, 2, 2, 2, 2>(p, stream);
     }
+    if (large)
+        return tiles_as<T, LIST, 4, 2, 2, 4>(p, stream);
+    return tiles_as<T, LIST, 2, 2, 2, 2>(p, stream);
 }
 
 template <typename T>
