@@ -1248,9 +1248,9 @@ ivfpq_status ivfpq_mx4_list_product_ex(const uint8_t *a_codes_dev, const uint8_t
         return fail(IVFPQ_E_INVALID_ARG, "type must be an ivfpq_type");
     if (arows < 0 || arows > (int64_t)0x7FFFFFFF || rows < 0 || rows > (int64_t)0x7FFFFFFF ||
         n < 0 || n > (int64_t)0x7FFFFFF0 || d < 1 || d > kMaxRowDim ||
-        (rows / 8 + 1) * (n / 16 + 1) > (int64_t)0x7FFFFFFF)
+        (rows + 1) * (n / 16 + 1) > (int64_t)1 << 30)
         return fail(IVFPQ_E_INVALID_ARG,
-                    "rows and n must be in [0, 2^31), rows n below 2^38 and d in [1, 2^20]");
+                    "rows and n must be in [0, 2^31), rows n below 2^34 and d in [1, 2^20]");
     if (nlist < 1 || nlist > (1 << 16) || k < 1)
         return fail(IVFPQ_E_INVALID_ARG, "nlist must be in [1, 2^16] and k at least 1");
     if (rows > 0 && n > 0 && !offsets_dev)

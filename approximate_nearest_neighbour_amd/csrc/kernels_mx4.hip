@@ -448,28 +448,35 @@ struct ScaleBytes {
     }
 };
 
-// Tile numbers: the workgroups of one XCD (every eighth) take a contiguous
-// range of tiles, and that range runs through groups of kGroup tiles along m
-// by all tiles along n, so that tiles in flight together share operands in
-// the XCD's cache.
-constexpr uint32_t kGroup = 8;
-
-__device__ __forceinline__ void tile_of_block(uint32_t mt, uint32_t nt, uint32_t &m, uint32_t &n)
-{
-    const uint32_t all = gridDim.x, x = blockIdx.x & 7, i = blockIdx.x >> 3;
-    const uint32_t per = all >> 3, extra = all & 7;
-    const uint32_t id = x * per + min(x, extra) + i;
-    const uint32_t group = id / (kGroup * nt);
-    const uint32_t first = group * kGroup;
-    const uint32_t rows = min(kGroup, mt - first);
-    const uint32_t in = id - group * kGroup * nt;
-    m = first + in % rows;
-    n = in / rows;
-}
+// Tile numbers.  Tiles go in groups of `high` along m by all runs along n, so
+// that those in flight together on one XCD share operands in its cache.  The
+// workgroups of an XCD (every eighth) take a contiguous range of them; for
+// lists, whose number of tiles is only bounded, every eighth group, so that the
+// tiles that turn out empty, the last ones, are the same share for all.
+struct TileOrder {
+    uint32_t mt, nruns, high;
+    template <bool LIST>
+    __device__ __forceinline__ void of_block(uint32_t &m, uint32_t &n) const
+    {
+        const uint32_t x = blockIdx.x & 7, i = blockIdx.x >> 3, size = high * nruns;
+        uint32_t id;
+        if constexpr (LIST) {
+            id = (i / size * 8 + x) * size + i % size;
+        } else {
+            const uint32_t per = gridDim.x >> 3, extra = gridDim.x & 7;
+            id = x * per + min(x, extra) + i;
+        }
+        const uint32_t first = id / size * high;
+        const uint32_t rows = first < mt ? min(high, mt - first) : high;
+        const uint32_t in = id % size;
+        m = first + in % rows;
+        n = in / rows;
+    }
+};
 
 template <typename T, bool LIST, int WM, int WN, int MW, int NW, bool ONE>
-__global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, uint32_t mtiles,
-                                                                uint32_t nruns, int most)
+__global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, TileOrder order,
+                                                                int most)
 {
     constexpr bool PAIR = sizeof(T) == 2;
     constexpr int WAVES = MW * NW, TM = 32 * WM * MW, TN = 32 * WN * NW;
@@ -484,11 +491,13 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, ui
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     uint32_t mt, nr;
     if constexpr (ONE) { // bound by its stores: workgroups side by side write side by side
-        mt = blockIdx.x / nruns;
-        nr = blockIdx.x - mt * nruns;
+        mt = blockIdx.x / order.nruns;
+        nr = blockIdx.x - mt * order.nruns;
     } else {
-        tile_of_block(mtiles, nruns, mt, nr);
+        order.of_block<LIST>(mt, nr);
     }
+    if (mt >= order.mt || nr >= order.nruns)
+        return;
     const int n0 = (int)nr * most * TN;
     const int run = min(most, (p.n - n0 + TN - 1) / TN);
     ListTile tile{0, (int64_t)mt * TM, min((int64_t)mt * TM + TM, p.m)};
@@ -750,14 +759,22 @@ static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
 {
     constexpr int64_t TM = 32 * WM * MW, TN = 32 * WN * NW;
     const int64_t nt = (p.n + TN - 1) / TN;
-    int64_t mt = (p.m + TM - 1) / TM;
-    if (LIST) // every list may end inside a tile, and so may the last rows
-        mt = p.m / TM + (p.m < (int64_t)p.nlist + 1 ? p.m : (int64_t)p.nlist + 1);
-    const int run = ONE ? 1 : run_length(mt, nt, (p.kb + 7) / 8, MW * NW == 8 ? 256 : 512);
-    const int64_t nruns = (nt + run - 1) / run;
-    hipLaunchKernelGGL((mx4_tile_kernel<T, LIST, WM, WN, MW, NW, ONE>),
-                       dim3((unsigned)(nruns * mt)), dim3(64 * MW * NW), 0, stream, p, (uint32_t)mt,
-                       (uint32_t)nruns, run);
+    int64_t mt = (p.m + TM - 1) / TM, likely = mt;
+    if (LIST) { // every list may end inside a tile, and so may the last rows; half may be
+        const int64_t ends = p.m < (int64_t)p.nlist + 1 ? p.m : (int64_t)p.nlist + 1;
+        mt = p.m / TM + ends;
+        likely = p.m / TM + ends / 2 + 1;
+    }
+    const int run = ONE ? 1 : run_length(likely, nt, (p.kb + 7) / 8, MW * NW == 8 ? 256 : 512);
+    TileOrder order;
+    order.mt = (uint32_t)mt;
+    order.nruns = (uint32_t)((nt + run - 1) / run);
+    order.high = LIST ? (uint32_t)(likely < 32 ? 1 : likely < 64 ? 2 : 4) : 8;
+    int64_t blocks = mt * order.nruns;
+    if (LIST) // whole groups, the same number for every XCD
+        blocks = ((mt + order.high - 1) / order.high + 7) / 8 * 8 * order.high * order.nruns;
+    hipLaunchKernelGGL((mx4_tile_kernel<T, LIST, WM, WN, MW, NW, ONE>), dim3((unsigned)blocks),
+                       dim3(64 * MW * NW), 0, stream, p, order, run);
     return hipGetLastError();
 }
 

@@ -437,7 +437,7 @@ ivfpq_status ivfpq_mx4_dequantize_ex(const uint8_t *codes_dev, const uint8_t *sc
  * matrix of n rows.  Products on the matrix cores, summed in float32, rounded
  * once to `type`.  A result with a NaN block on either side is NaN.  m = 0 or
  * n = 0 is a no-op.  Errors: IVFPQ_E_INVALID_ARG (m or n outside [0, 2^31),
- * m n >= 2^39, d outside [1, 2^20], a bad type, a NULL or misaligned
+ * (m / 16 + 1) (n / 16 + 1) >= 2^31, d outside [1, 2^20], a bad type, a NULL or misaligned
  * pointer), IVFPQ_E_DEVICE. */
 ivfpq_status ivfpq_mx4_product_ex(const uint8_t *a_codes_dev, const uint8_t *a_scales_dev,
                                   int64_t m, const uint8_t *b_codes_dev,
@@ -451,8 +451,8 @@ ivfpq_status ivfpq_mx4_product_ex(const uint8_t *a_codes_dev, const uint8_t *a_s
  * row order[p] / k of A times matrix e, or row p of A when order_dev is NULL
  * (then arows >= rows).  Rows from offsets[nlist] to `rows` are zero.  out_dev
  * [rows][n] of `type`.  An entry of order outside A reads row 0.  Errors as
- * above, and IVFPQ_E_INVALID_ARG for nlist outside [1, 2^16], k < 1 or
- * rows n >= 2^38. */
+ * above, and IVFPQ_E_INVALID_ARG for nlist outside [1, 2^16], k < 1 or (rows +
+ * 1) (n / 16 + 1) > 2^30. */
 ivfpq_status ivfpq_mx4_list_product_ex(const uint8_t *a_codes_dev, const uint8_t *a_scales_dev,
                                        int64_t arows, const uint8_t *b_codes_dev,
                                        const uint8_t *b_scales_dev, int nlist, int64_t n, int d,

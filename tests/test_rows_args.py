@@ -56,6 +56,7 @@ BAD = [
     ("ivfpq_mx4_list_product_ex", {9: None}),  # 8 rows of a first operand of 4
     ("ivfpq_mx4_list_product_ex", {12: 7}), ("ivfpq_mx4_list_product_ex", {13: None}),
     ("ivfpq_mx4_list_product_ex", {3: P + 4}), ("ivfpq_mx4_list_product_ex", {7: -3}),
+    ("ivfpq_mx4_list_product_ex", {2: BIG - 1, 6: 1 << 20, 11: 1 << 16}),
     ("ivfpq_route_sort_ex", {0: None}), ("ivfpq_route_sort_ex", {1: -1}),
     ("ivfpq_route_sort_ex", {1: 1 << 30}), ("ivfpq_route_sort_ex", {2: 0}),
     ("ivfpq_route_sort_ex", {3: 0}), ("ivfpq_route_sort_ex", {3: 1 << 22}),
