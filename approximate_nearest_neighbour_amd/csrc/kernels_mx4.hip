@@ -814,19 +814,25 @@ static hipError_t product_of(const Mx4Product &p, hipStream_t stream)
             return direct_as<T, LIST, 4>(p, mt, stream);
         return direct_as<T, LIST, 8>(p, mt, stream);
     }
-    // Large tiles (256 x 256) take about three times as long as small ones (128 x
+    // Large tiles (256 x 256) take about three times as long as middle ones (128 x
     // 128) a round of 256: 40 us against 14 us a quarter of the results (d 4096).
-    auto rounds = [&](int64_t size) {
+    // Small ones (64 x 128) where few tiles wait for their chunks more than for
+    // the matrix cores: 512 x 1024 x 4096 11.7 us against 14.4 us, 1024 x 4096 x
+    // 4096, which is 512 of them, 28.8 us against 18.8 us.
+    auto tiles = [&](int64_t high, int64_t wide) {
         const int64_t parts = LIST ? (p.m < p.nlist ? p.m : p.nlist) / 2 : 0; // lists end inside
-        return (((p.m + size - 1) / size + parts) * ((p.n + size - 1) / size) + 255) / 256;
+        return ((p.m + high - 1) / high + parts) * ((p.n + wide - 1) / wide);
     };
-    const bool large = 3 * rounds(256) <= rounds(128);
+    const bool large = 3 * ((tiles(256, 256) + 255) / 256) <= (tiles(128, 128) + 255) / 256;
+    const bool small = tiles(64, 128) <= (p.kb <= 32 ? 512 : 256);
     if constexpr (!LIST) {
         if (p.kb <= 8)
             return tiles_as<T, false, 1, 1, 2, 4, true>(p, stream);
     }
     if (large)
         return tiles_as<T, LIST, 4, 2, 2, 4>(p, stream);
+    if (small)
+        return tiles_as<T, LIST, 1, 1, 2, 4>(p, stream);
     return tiles_as<T, LIST, 2, 2, 2, 2>(p, stream);
 }
 
