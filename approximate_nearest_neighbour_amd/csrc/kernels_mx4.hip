@@ -737,15 +737,20 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
 }
 
 // Tiles of a run: of 1, 2, 4 and 8 the one that ends first when `slots`
-// workgroups are under way together, a tile taking its chunks and a run as
-// long again as about three chunks (first copies, last stores).
+// workgroups are under way together, a tile taking its chunks and one more, a
+// run about three chunks besides (first copies, last stores).  Tiles of lists
+// are of different cost and end at different times: half a run at the end, not
+// a whole last round (128 lists of 512 rows, 2048 x 2048: runs of 1, 2, 4 and 8
+// 251, 235, 249 and 312 us).
+template <bool LIST>
 static int run_length(int64_t mt, int64_t nt, int chunks, int64_t slots)
 {
     int best = 1;
     int64_t least = INT64_MAX;
     for (int run = 1; run <= 8 && (run == 1 || chunks % 2 == 0); run *= 2) {
-        const int64_t rounds = (mt * ((nt + run - 1) / run) + slots - 1) / slots;
-        const int64_t cost = rounds * ((int64_t)run * (chunks + 1) + 3);
+        const int64_t runs = mt * ((nt + run - 1) / run);
+        const int64_t halves = LIST ? 2 * runs + slots : (runs + slots - 1) / slots * 2 * slots;
+        const int64_t cost = halves * ((int64_t)run * (chunks + 1) + 3);
         if (cost < least) {
             least = cost;
             best = run;
@@ -765,7 +770,7 @@ static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
         mt = p.m / TM + ends;
         likely = p.m / TM + ends / 2 + 1;
     }
-    const int run = ONE ? 1 : run_length(likely, nt, (p.kb + 7) / 8, MW * NW == 8 ? 256 : 512);
+    const int run = ONE ? 1 : run_length<LIST>(likely, nt, (p.kb + 7) / 8, MW * NW == 8 ? 256 : 512);
     TileOrder order;
     order.mt = (uint32_t)mt;
     order.nruns = (uint32_t)((nt + run - 1) / run);
