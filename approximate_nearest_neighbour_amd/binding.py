@@ -442,12 +442,15 @@ def _row_type(dtype) -> int:
     return TYPES[dtype]
 
 
-def _rows(t: torch.Tensor) -> torch.Tensor:
-    _row_type(t.dtype)
-    _dev(t, t.dtype)
-    if t.dim() != 2 or t.shape[1] < 1:
+def _rows(t: torch.Tensor):
+    """The type code and shape of checked rows [n, d]."""
+    kind = TYPES.get(t.dtype)
+    if kind is None or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("expected contiguous device rows of float32, bfloat16 or float16")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] < 1:
         raise ValueError("expected rows [n, d] with d >= 1")
-    return t
+    return kind, shape
 
 
 def _ptr(t):
@@ -457,8 +460,8 @@ def _ptr(t):
 def _out(out, shape, dtype, device) -> torch.Tensor:
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"expected an output of shape {tuple(shape)}")
+    if out.shape != shape:
+        raise ValueError(f"expected an output of shape {shape}")
     return _dev(out, dtype)
 
 
@@ -479,16 +482,17 @@ def ivfpq_mx4_quantize_ex(x: torch.Tensor, out=None, stream=None):
     will do) to microscaled 4-bit rows: (codes [n, 16 kb] uint8, scales [n, kb]
     uint8), kb = ceil(d / 32)."""
     kind = _row_type(x.dtype)
-    if not x.is_cuda or x.dim() != 2 or x.shape[1] < 1 or \
-            (x.shape[1] > 1 and x.stride(1) != 1) or x.stride(0) < 0:
+    shape, strides = x.shape, x.stride()
+    if not x.is_cuda or len(shape) != 2 or shape[1] < 1 or \
+            (shape[1] > 1 and strides[1] != 1) or strides[0] < 0:
         raise ValueError("expected device rows [n, d], d >= 1, each row contiguous")
-    n, d = x.shape
+    n, d = shape
     kb = (d + 31) // 32
     codes, scales = (None, None) if out is None else out
     codes = _out(codes, (n, 16 * kb), torch.uint8, x.device)
     scales = _out(scales, (n, kb), torch.uint8, x.device)
-    _check(lib().ivfpq_mx4_quantize_ex(_ptr(x), kind, n, d, x.stride(0), _ptr(codes),
-                                       _ptr(scales), _raw_stream(stream)))
+    _check(lib().ivfpq_mx4_quantize_ex(x.data_ptr(), kind, n, d, strides[0], codes.data_ptr(),
+                                       scales.data_ptr(), _raw_stream(stream)))
     return codes, scales
 
 
@@ -533,9 +537,12 @@ def ivfpq_mx4_list_product_ex(a, b, offsets: torch.Tensor, order: torch.Tensor =
         raise ValueError("the operands' rows have different lengths")
     if offsets.shape != (nlist + 1,):
         raise ValueError("expected offsets [nlist + 1]")
-    if order is not None and _dev(order, torch.int32).dim() != 1:
-        raise ValueError("expected order [rows]")
-    rows = arows if order is None else order.shape[0]
+    rows = arows
+    if order is not None:
+        shape = _slots(order, "order")
+        if len(shape) != 1:
+            raise ValueError("expected order [rows]")
+        rows = shape[0]
     out = _out(out, (rows, n), dtype, ac.device)
     _check(lib().ivfpq_mx4_list_product_ex(ac.data_ptr(), as_.data_ptr(), arows, bc.data_ptr(),
                                            bs.data_ptr(), nlist, n, 32 * kb, offsets.data_ptr(),
@@ -553,39 +560,43 @@ def ivfpq_route_sort_ex(lists: torch.Tensor, nlist: int, out=None, workspace=Non
     [0, nlist): masked) -> (offsets [nlist + 1], order [nvec k], pos [nvec, k]),
     all int32.  workspace: uint8 device tensor of
     ivfpq_route_sort_bytes (None: allocated here where one is needed)."""
-    lists = _dev(lists, torch.int32)
-    if lists.dim() != 2 or lists.shape[1] < 1:
-        raise ValueError("expected lists [nvec, k], k >= 1")
-    nvec, k = lists.shape
+    shape = _slots(lists, "lists")
+    if len(shape) != 2 or shape[1] < 1 or nlist < 1:
+        raise ValueError("expected lists [nvec, k], k >= 1, and nlist >= 1")
+    nvec, k = shape
     offsets, order, pos = (None, None, None) if out is None else out
-    if nlist < 1:
-        raise ValueError("nlist must be at least 1")
-    offsets = _out(offsets, (nlist + 1,), torch.int32, lists.device)
-    order = _out(order, (nvec * k,), torch.int32, lists.device)
-    pos = _out(pos, (nvec, k), torch.int32, lists.device)
+    device = lists.device
+    offsets = _out(offsets, (nlist + 1,), torch.int32, device)
+    order = _out(order, (nvec * k,), torch.int32, device)
+    pos = _out(pos, shape, torch.int32, device)
     need = ivfpq_route_sort_bytes(nvec, k, nlist)
     if workspace is not None:
         _dev(workspace, torch.uint8)
     elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=lists.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
         if stream is not None:
             workspace.record_stream(stream)
-    _check(lib().ivfpq_route_sort_ex(_ptr(lists), nvec, k, nlist, _ptr(workspace),
-                                     0 if workspace is None else workspace.numel(), _ptr(offsets),
-                                     _ptr(order), _ptr(pos), _raw_stream(stream)))
+    _check(lib().ivfpq_route_sort_ex(lists.data_ptr(), nvec, k, nlist, _ptr(workspace),
+                                     0 if workspace is None else workspace.numel(),
+                                     offsets.data_ptr(), order.data_ptr(), pos.data_ptr(),
+                                     _raw_stream(stream)))
     return offsets, order, pos
 
 
-def _slots(t: torch.Tensor, dims: int, what: str) -> torch.Tensor:
-    if _dev(t, torch.int32).dim() != dims:
-        raise ValueError(f"expected {what}")
-    return t
+def _slots(t: torch.Tensor, what: str):
+    """Shape of checked slot numbers."""
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"expected {what} as a contiguous int32 device tensor")
+    return t.shape
 
 
 def _slot_weights(weights, nvec: int, k: int):
-    if weights is not None and _dev(weights, torch.float32).shape != (nvec, k):
+    """Pointer of checked weights, None without them."""
+    if weights is None:
+        return None
+    if _dev(weights, torch.float32).shape != (nvec, k):
         raise ValueError("expected weights [nvec, k]")
-    return weights
+    return weights.data_ptr()
 
 
 def ivfpq_route_gather_ex(x: torch.Tensor, order: torch.Tensor, k: int,
@@ -593,30 +604,33 @@ def ivfpq_route_gather_ex(x: torch.Tensor, order: torch.Tensor, k: int,
     """Row p = x[order[p] // k] (times weights[order[p]]), zero where order is -1:
     [nvec k, d] from x [nvec, d].  Its gradient with respect to x is
     ivfpq_route_combine_ex of the rows' gradient."""
-    x = _rows(x)
-    nvec, d = x.shape
-    if k < 1 or _slots(order, 1, "order [nvec k]").shape[0] != nvec * k:
+    kind, (nvec, d) = _rows(x)
+    if k < 1 or _slots(order, "order") != (nvec * k,):
         raise ValueError("expected order [nvec k], k >= 1")
-    weights = _slot_weights(weights, nvec, k)
+    w = _slot_weights(weights, nvec, k)
     out = _out(out, (nvec * k, d), x.dtype, x.device)
-    _check(lib().ivfpq_route_gather_ex(_ptr(x), _row_type(x.dtype), nvec, d, _ptr(order),
-                                       _ptr(weights), k, _ptr(out), _raw_stream(stream)))
+    _check(lib().ivfpq_route_gather_ex(x.data_ptr(), kind, nvec, d, order.data_ptr(), w, k,
+                                       out.data_ptr(), _raw_stream(stream)))
     return out
+
+
+def _routed(rows: torch.Tensor, pos: torch.Tensor):
+    kind, (n, d) = _rows(rows)
+    shape = _slots(pos, "pos")
+    if len(shape) != 2 or shape[1] < 1 or n != shape[0] * shape[1]:
+        raise ValueError("expected rows [nvec k, d] and pos [nvec, k], k >= 1")
+    return kind, d, *shape
 
 
 def ivfpq_route_combine_ex(rows: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor = None,
                            out=None, stream=None) -> torch.Tensor:
     """y[t] = sum_j weights[t, j] rows[pos[t, j]] (weights 1 without them), masked
-    slots (pos -1) skipped: [nvec, d] from rows [nvec k, d]."""
-    rows = _rows(rows)
-    nvec, k = _slots(pos, 2, "pos [nvec, k]").shape
-    if k < 1 or rows.shape[0] != nvec * k:
-        raise ValueError("expected rows [nvec k, d] and pos [nvec, k]")
-    weights = _slot_weights(weights, nvec, k)
-    out = _out(out, (nvec, rows.shape[1]), rows.dtype, rows.device)
-    _check(lib().ivfpq_route_combine_ex(_ptr(rows), _row_type(rows.dtype), nvec, rows.shape[1],
-                                        _ptr(pos), _ptr(weights), k, _ptr(out),
-                                        _raw_stream(stream)))
+    slots (pos -1) adding nothing: [nvec, d] from rows [nvec k, d]."""
+    kind, d, nvec, k = _routed(rows, pos)
+    w = _slot_weights(weights, nvec, k)
+    out = _out(out, (nvec, d), rows.dtype, rows.device)
+    _check(lib().ivfpq_route_combine_ex(rows.data_ptr(), kind, nvec, d, pos.data_ptr(), w, k,
+                                        out.data_ptr(), _raw_stream(stream)))
     return out
 
 
@@ -624,22 +638,21 @@ def ivfpq_route_combine_grad_ex(grad: torch.Tensor, rows: torch.Tensor, order: t
                                 pos: torch.Tensor, weights: torch.Tensor, out=None, stream=None):
     """Gradients of ivfpq_route_combine_ex(rows, pos, weights) for the output
     gradient grad [nvec, d]: (of rows [nvec k, d], of weights [nvec, k] float32)."""
-    rows, grad = _rows(rows), _rows(grad)
-    nvec, k = _slots(pos, 2, "pos [nvec, k]").shape
-    d = rows.shape[1]
-    if k < 1 or rows.shape[0] != nvec * k or grad.shape != (nvec, d) or grad.dtype != rows.dtype:
-        raise ValueError("expected grad [nvec, d], rows [nvec k, d] of its type and pos [nvec, k]")
-    if _slots(order, 1, "order [nvec k]").shape[0] != nvec * k:
+    kind, d, nvec, k = _routed(rows, pos)
+    if _rows(grad) != (kind, (nvec, d)):
+        raise ValueError("expected grad [nvec, d] of the rows' type")
+    if _slots(order, "order") != (nvec * k,):
         raise ValueError("expected order [nvec k]")
-    if weights is None:
+    w = _slot_weights(weights, nvec, k)
+    if w is None:
         raise ValueError("expected weights [nvec, k]")
-    weights = _slot_weights(weights, nvec, k)
     d_rows, d_weights = (None, None) if out is None else out
     d_rows = _out(d_rows, (nvec * k, d), rows.dtype, rows.device)
     d_weights = _out(d_weights, (nvec, k), torch.float32, rows.device)
-    _check(lib().ivfpq_route_combine_grad_ex(_ptr(grad), _ptr(rows), _row_type(rows.dtype), nvec,
-                                             d, _ptr(order), _ptr(pos), _ptr(weights), k,
-                                             _ptr(d_rows), _ptr(d_weights), _raw_stream(stream)))
+    _check(lib().ivfpq_route_combine_grad_ex(grad.data_ptr(), rows.data_ptr(), kind, nvec, d,
+                                             order.data_ptr(), pos.data_ptr(), w, k,
+                                             d_rows.data_ptr(), d_weights.data_ptr(),
+                                             _raw_stream(stream)))
     return d_rows, d_weights
 
 

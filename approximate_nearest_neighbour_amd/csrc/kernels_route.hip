@@ -15,7 +15,9 @@ namespace ivfpq {
 // stable sort by list
 // ---------------------------------------------------------------------------
 
-constexpr int kSortWaves = 4;
+// Eight waves a workgroup against four, 320,000 slots of 1024 lists: count 4.9
+// against 6.3 us, scatter 9.1 against 12.2 us.
+constexpr int kSortWaves = 8;
 constexpr int kSortChunk = 2048; // slots of one workgroup
 constexpr int kSortBits = 11;    // bits of one pass
 constexpr int kSortBins = 1 << kSortBits;
