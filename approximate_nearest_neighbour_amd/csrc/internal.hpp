@@ -173,6 +173,7 @@ struct Mx4Product {
     const int32_t *offsets = nullptr; // [nlist + 1]
     const int32_t *order = nullptr;   // [m] or nullptr
     int nlist = 0, k = 1;
+    uint32_t block0 = 0; // number of the launch's first workgroup
 };
 hipError_t launch_mx4_product(const Mx4Product &p, int type, hipStream_t stream);
 

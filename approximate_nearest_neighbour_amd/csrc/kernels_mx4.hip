@@ -232,8 +232,8 @@ __global__ __launch_bounds__(512) void mx4_direct_kernel(Mx4Product p, uint32_t 
     __shared__ f32x4 part[KS == 1 ? 1 : 8][64];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const uint32_t mt = blockIdx.x / ntiles;
-    const int n0 = ((int)(blockIdx.x - mt * ntiles) * GROUPS + wave / KS) * 16;
+    const uint32_t block = blockIdx.x + p.block0, mt = block / ntiles;
+    const int n0 = ((int)(block - mt * ntiles) * GROUPS + wave / KS) * 16;
     ListTile tile{0, (int64_t)mt * 16, min((int64_t)mt * 16 + 16, p.m)};
     if constexpr (LIST)
         tile = find_tile<16>(p.offsets, p.nlist, p.m, mt);
@@ -368,7 +368,8 @@ __device__ __forceinline__ int64_t uniform(int64_t v)
     return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | lo);
 }
 
-// A memory range for the copies: reads past it give zeros.
+// A memory range for the copies: reads past it give zeros (the scalar offset
+// counts in that check).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t *base, int64_t from,
                                                             int64_t bytes)
 {
@@ -454,16 +455,16 @@ struct ScaleBytes {
 // lists, whose number of tiles is only bounded, every eighth group, so that the
 // tiles that turn out empty, the last ones, are the same share for all.
 struct TileOrder {
-    uint32_t mt, nruns, high;
+    uint32_t mt, nruns, high, blocks;
     template <bool LIST>
-    __device__ __forceinline__ void of_block(uint32_t &m, uint32_t &n) const
+    __device__ __forceinline__ void of_block(uint32_t block, uint32_t &m, uint32_t &n) const
     {
-        const uint32_t x = blockIdx.x & 7, i = blockIdx.x >> 3, size = high * nruns;
+        const uint32_t x = block & 7, i = block >> 3, size = high * nruns;
         uint32_t id;
         if constexpr (LIST) {
             id = (i / size * 8 + x) * size + i % size;
         } else {
-            const uint32_t per = gridDim.x >> 3, extra = gridDim.x & 7;
+            const uint32_t per = blocks >> 3, extra = blocks & 7;
             id = x * per + min(x, extra) + i;
         }
         const uint32_t first = id / size * high;
@@ -489,12 +490,13 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
 
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t block = blockIdx.x + p.block0;
     uint32_t mt, nr;
     if constexpr (ONE) { // bound by its stores: workgroups side by side write side by side
-        mt = blockIdx.x / order.nruns;
-        nr = blockIdx.x - mt * order.nruns;
+        mt = block / order.nruns;
+        nr = block - mt * order.nruns;
     } else {
-        order.of_block<LIST>(mt, nr);
+        order.of_block<LIST>(block, mt, nr);
     }
     if (mt >= order.mt || nr >= order.nruns)
         return;
@@ -759,6 +761,19 @@ static int run_length(int64_t mt, int64_t nt, int chunks, int64_t slots)
     return best;
 }
 
+template <typename Kernel, typename... Args>
+static hipError_t launch_blocks(Kernel kernel, int64_t blocks, int threads, hipStream_t stream,
+                                Mx4Product p, Args... args)
+{
+    const int64_t most = most_blocks(threads);
+    for (int64_t b = 0; b < blocks; b += most) {
+        p.block0 = (uint32_t)b;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks - b < most ? blocks - b : most)),
+                           dim3(threads), 0, stream, p, args...);
+    }
+    return hipGetLastError();
+}
+
 template <typename T, bool LIST, int WM, int WN, int MW, int NW, bool ONE = false>
 static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
 {
@@ -778,18 +793,16 @@ static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
     int64_t blocks = mt * order.nruns;
     if (LIST) // whole groups, the same number for every XCD
         blocks = ((mt + order.high - 1) / order.high + 7) / 8 * 8 * order.high * order.nruns;
-    hipLaunchKernelGGL((mx4_tile_kernel<T, LIST, WM, WN, MW, NW, ONE>), dim3((unsigned)blocks),
-                       dim3(64 * MW * NW), 0, stream, p, order, run);
-    return hipGetLastError();
+    order.blocks = (uint32_t)blocks;
+    return launch_blocks(mx4_tile_kernel<T, LIST, WM, WN, MW, NW, ONE>, blocks, 64 * MW * NW, stream,
+                         p, order, run);
 }
 
 template <typename T, bool LIST, int KS>
 static hipError_t direct_as(const Mx4Product &p, int64_t mt, hipStream_t stream)
 {
     const int64_t nt = (p.n + 16ll * 8 / KS - 1) / (16 * 8 / KS);
-    hipLaunchKernelGGL((mx4_direct_kernel<T, LIST, KS>), dim3((unsigned)(nt * mt)), dim3(512), 0,
-                       stream, p, (uint32_t)nt);
-    return hipGetLastError();
+    return launch_blocks(mx4_direct_kernel<T, LIST, KS>, nt * mt, 512, stream, p, (uint32_t)nt);
 }
 
 // Which kernel.  The direct one reads B once for every 16 rows of A, the tiles

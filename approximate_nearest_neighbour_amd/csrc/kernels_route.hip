@@ -447,10 +447,11 @@ template <typename T>
 __global__ __launch_bounds__(256) void route_combine_grad_kernel(
     const T *__restrict__ grad, const T *__restrict__ rows, int64_t n, int d, int lanes, FastDiv k,
     const int32_t *__restrict__ order, const int32_t *__restrict__ pos,
-    const float *__restrict__ weights, T *__restrict__ d_rows, float *__restrict__ d_weights)
+    const float *__restrict__ weights, T *__restrict__ d_rows, float *__restrict__ d_weights,
+    int64_t block0)
 {
     constexpr int N = Piece<T>::N;
-    const int64_t u = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+    const int64_t u = (block0 + blockIdx.x) * (256 / lanes) + threadIdx.x / lanes;
     const int sub = threadIdx.x & (lanes - 1);
     const int64_t p = u < n ? pos[u] : -1;
     const bool kept = p >= 0 && p < n;
@@ -481,12 +482,6 @@ __global__ __launch_bounds__(256) void route_combine_grad_kernel(
             (lane_id() ^ s) << 2, (int)__float_as_uint(dot)));
     if (sub == 0 && u < n)
         d_weights[u] = dot;
-}
-
-static dim3 row_grid(int64_t rows, int lanes)
-{
-    const int64_t per = 256 / lanes;
-    return dim3((unsigned)((rows + per - 1) / per));
 }
 
 template <typename T>
@@ -531,10 +526,14 @@ static hipError_t combine_grad_as(const void *grad, const void *rows, int64_t nv
                                   int k, void *d_rows, float *d_weights, hipStream_t stream)
 {
     const int lanes = row_lanes<T>(d);
-    hipLaunchKernelGGL(route_combine_grad_kernel<T>, row_grid(nvec * k, lanes), dim3(256), 0,
-                       stream, static_cast<const T *>(grad), static_cast<const T *>(rows),
-                       nvec * k, d, lanes, FastDiv((uint32_t)k), order, pos, weights,
-                       static_cast<T *>(d_rows), d_weights);
+    const int64_t n = nvec * k, blocks = (n + 256 / lanes - 1) / (256 / lanes);
+    const int64_t most = most_blocks(256);
+    for (int64_t b = 0; b < blocks; b += most)
+        hipLaunchKernelGGL(route_combine_grad_kernel<T>,
+                           dim3((unsigned)(blocks - b < most ? blocks - b : most)), dim3(256), 0,
+                           stream, static_cast<const T *>(grad), static_cast<const T *>(rows), n, d,
+                           lanes, FastDiv((uint32_t)k), order, pos, weights,
+                           static_cast<T *>(d_rows), d_weights, b);
     return hipGetLastError();
 }
 

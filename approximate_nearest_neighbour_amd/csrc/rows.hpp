@@ -8,6 +8,9 @@
 
 namespace ivfpq {
 
+// Workgroups of one launch (a multiple of 8): a launch takes fewer than 2^32 threads.
+constexpr int64_t most_blocks(int threads) { return (0xFFFFFFFFll / threads) & ~7ll; }
+
 // Element types of the row operators (ivfpq_type of the header).
 enum RowType { kF32 = 0, kBF16 = 1, kF16 = 2 };
 

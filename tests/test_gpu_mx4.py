@@ -235,6 +235,17 @@ def test_product_past_32_bit_offsets():
                   torch.float16)
 
 
+def test_product_past_the_threads_of_one_launch():
+    n = (1 << 30) + 300                           # 2^32 threads and some
+    bc = torch.full((n, 16), 0x22, device="cuda", dtype=torch.uint8)  # ones
+    bs = torch.full((n, 1), 127, device="cuda", dtype=torch.uint8)
+    bs[-300:] = 128
+    a = random_mx4(np.random.default_rng(15), 1, 32)
+    out = A.ivfpq_mx4_product_ex(cuda(a), (bc, bs), dtype=torch.float32)
+    want = float(R.values(*a, 32).sum())          # sums of small multiples of a power of two
+    assert (out[0, :-300] == want).all() and (out[0, -300:] == 2 * want).all()
+
+
 # --- product per list -------------------------------------------------------
 
 def make_lists(rng, t, k, nlist, drop, hot=None):

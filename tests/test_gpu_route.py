@@ -203,3 +203,15 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(d_rows[-100:], x[last])
     norm = (x[-50:].double() ** 2).sum(dim=1)
     assert ((d_w[-50:].double() - norm[:, None]).abs() <= d * 2.0 ** -23 * norm[:, None]).all()
+
+
+def test_gradient_past_the_threads_of_one_launch():
+    k, d = (1 << 29) + 40, 33                     # eight lanes a slot
+    slots = torch.arange(k, device="cuda", dtype=torch.int32)
+    grad = torch.arange(d, device="cuda").to(torch.bfloat16)[None]
+    rows = torch.ones((k, d), device="cuda", dtype=torch.bfloat16)
+    w = torch.full((1, k), 2.0, device="cuda")
+    d_rows, d_w = A.ivfpq_route_combine_grad_ex(grad, rows, slots, slots[None], w)
+    for part in (slice(0, 100), slice(k - 100, k)):
+        assert (d_rows[part] == 2 * grad).all()
+    assert (d_w == d * (d - 1) / 2).all()
