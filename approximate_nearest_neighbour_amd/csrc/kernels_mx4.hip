@@ -660,51 +660,66 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
     };
     constexpr std::integral_constant<int, 0> even{};
     constexpr std::integral_constant<int, 1> odd{};
-    // The chunk that lies in the places given, while `copies` brings the next
-    // one and `scales` its exponent bytes.
-    auto chunk = [&](auto parity, const uint8_t *froma, const uint8_t *fromb, auto copies,
-                     auto scales) {
+    Operands o[2];
+    uint32_t sa[WM], sb[WN]; // exponent bytes of the chunk, a lane's four steps
+    auto multiply = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < WM; ++i)
+#pragma unroll
+            for (int j = 0; j < WN; ++j)
+                acc[i][j] = PAIR ? mfma_mx4_32(o[s & 1].b[j], sb[j], o[s & 1].a[i], sa[i], s,
+                                               acc[i][j])
+                                 : mfma_mx4_32(o[s & 1].a[i], sa[i], o[s & 1].b[j], sb[j], s,
+                                               acc[i][j]);
+    };
+    // The chunk that lies in the places given but for its last step, whose
+    // operands are left in registers: they are multiplied while the next
+    // chunk's first ones are read (`before`: so were those of the chunk before).
+    // `copies` brings the next chunk and `scales` its exponent bytes.
+    auto chunk = [&](auto parity, bool before, const uint8_t *froma, const uint8_t *fromb,
+                     auto copies, auto scales) {
         constexpr int ODD = decltype(parity)::value;
-        lds_barrier(); // every wave's part of this chunk is here, and its last reads done
-        Operands o[2];
-        uint32_t sa[WM], sb[WN];
+        uint32_t na[WM], nb[WN];
         read(froma, fromb, 0, o[0]);
 #pragma unroll
         for (int i = 0; i < WM; ++i)
-            sa[i] = scale[ODD][half][sa_at + i * 32];
+            na[i] = scale[ODD][half][sa_at + i * 32];
 #pragma unroll
         for (int j = 0; j < WN; ++j)
-            sb[j] = scale[ODD][half][sb_at + j * 32];
+            nb[j] = scale[ODD][half][sb_at + j * 32];
         __builtin_amdgcn_sched_barrier(0);
         copies();
+        __builtin_amdgcn_sched_barrier(0);
+        if (before)
+            multiply(3);
+#pragma unroll
+        for (int i = 0; i < WM; ++i)
+            sa[i] = na[i];
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+            sb[j] = nb[j];
         scales();
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if (s < 3)
-                read(froma, fromb, s + 1, o[(s + 1) & 1]);
-#pragma unroll
-            for (int i = 0; i < WM; ++i)
-#pragma unroll
-                for (int j = 0; j < WN; ++j)
-                    acc[i][j] = PAIR ? mfma_mx4_32(o[s & 1].b[j], sb[j], o[s & 1].a[i], sa[i], s,
-                                                   acc[i][j])
-                                     : mfma_mx4_32(o[s & 1].a[i], sa[i], o[s & 1].b[j], sb[j], s,
-                                                   acc[i][j]);
+        for (int s = 0; s < 3; ++s) {
+            read(froma, fromb, s + 1, o[(s + 1) & 1]);
+            multiply(s);
             __builtin_amdgcn_sched_barrier(0);
         }
-        wait_vm<0>(); // the next chunk (and what was stored before this one)
+        wait_vm<0>();  // the next chunk (and what was stored before this one)
+        lds_barrier(); // every wave's part of it is here, and this one's last reads done
     };
     auto bnow = b_of(0);
     load_scales(0, 0);
     fetch_a(0, code0);
     fetch_b(bnow, 0, code0 + TM * 128);
     put_scales(0, even);
+    wait_vm<0>();
+    lds_barrier();
     if constexpr (ONE) {
-        wait_vm<0>();
-        chunk(even, code0, code0 + TM * 128, [] {}, [] {});
+        chunk(even, false, code0, code0 + TM * 128, [] {}, [] {});
+        multiply(3);
         put(n0);
     } else {
-        wait_vm<0>();
 #pragma unroll 1
         for (int t = 0; t < run; ++t) { // more than one only if a row's chunks are even in number
             const auto bnext = b_of(t + 1);
@@ -713,7 +728,7 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
                 const bool last = c + 2 >= chunks;
                 const int after = last ? 0 : c + 2;
                 chunk(
-                    even, code0, code0 + TM * 128,
+                    even, c > 0, code0, code0 + TM * 128,
                     [&] {
                         fetch_a(c + 1, code1);
                         fetch_b(bnow, c + 1, code1 + TM * 128);
@@ -724,7 +739,7 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
                     });
                 if (c + 1 < chunks)
                     chunk(
-                        odd, code1, code1 + TM * 128,
+                        odd, true, code1, code1 + TM * 128,
                         [&] {
                             fetch_a(after, code0);
                             fetch_b(last ? bnext : bnow, after, code0 + TM * 128);
@@ -732,6 +747,7 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
                         [&] { put_scales(after, even); });
             }
             bnow = bnext;
+            multiply(3);
             put(n0 + t * TN);
             clear();
         }
