@@ -25,7 +25,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // largest magnitude minus 2 (the exponent of 4, the largest power of two of
 // e2m1), at least 0; the values times 2^(127 - s) are exact, then rounded to
 // the nearest e2m1, halves to even, saturating at 6.  A block with an
-// infinity or a NaN gets s = 255, which stands for NaN.
+// infinity or a NaN gets s = 255, which stands for NaN.  Bound by the rows'
+// bytes: a lane reads 16 or 32 of them side by side and writes four, a wave 16
+// whole blocks.  1,000,000 x 96 in float32 94 us, 4.6 TB/s (a large copy: 4.8).
 template <typename T>
 __global__ __launch_bounds__(256) void mx4_quantize_kernel(const T *__restrict__ x, uint32_t total,
                                                            int d, int64_t stride, FastDiv per_row,
@@ -100,7 +102,9 @@ __device__ __forceinline__ float scale_value(uint32_t s)
     return __uint_as_float(s == 255 ? 0x7FC00000u : s == 0 ? 0x00400000u : s << 23);
 }
 
-// Eight values a lane: four bytes of codes, one piece of output (float32: two).
+// Eight values a lane: four bytes of codes, one piece of output (float32: two),
+// each value rounded once from its exact float32 product.  Bound by the bytes:
+// 1,000,000 x 96 to float32 93 us, 4.7 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t *__restrict__ codes,
                                                              const uint8_t *__restrict__ scales,
@@ -224,7 +228,10 @@ __device__ __forceinline__ f32x4 mfma_mx4(i32x4 a, uint32_t sa, i32x4 b, uint32_
 // through LDS.  Sixteen blocks a turn, a lane group g taking blocks 4 s + g of
 // the four steps s (64 bytes side by side a row and step); the next turn's
 // operands are under way while this one's are multiplied.  The exponent bytes
-// of a turn are one 16-byte load, of which word s, byte g is the lane's.
+// of a turn are one 16-byte load, of which word s, byte g is the lane's.  Sums
+// are float32, rounded once to the output's type.  One row by 8192 x 4096: 5.8
+// us for 17.8 MB, of which the launch is about half; 4 rows of 8 lists each, 30
+// of 64 matrices of 2048 x 2048: 14 us for 71 MB, 5 TB/s.
 template <typename T, bool LIST, int KS>
 __global__ __launch_bounds__(512) void mx4_direct_kernel(Mx4Product p, uint32_t ntiles)
 {
@@ -335,8 +342,8 @@ __global__ __launch_bounds__(512) void mx4_direct_kernel(Mx4Product p, uint32_t 
 // row's blocks come eight at a time (a chunk: 128 bytes of codes, four matrix
 // instructions deep), both operands' rows copied from memory into LDS without
 // passing through registers; one chunk is multiplied while the next arrives in
-// the other LDS object.  Inside a chunk the operands of one step are read from
-// LDS while those of the step before are multiplied.
+// the other LDS object.  The operands of one step are read from LDS while those
+// of the step before are multiplied, across the chunks' ends too.
 //
 // Code rows lie in LDS 128 bytes apart, their eight 16-byte blocks permuted by
 // an exclusive or with three bits of the row, so that sixteen lanes that read
@@ -353,6 +360,14 @@ __global__ __launch_bounds__(512) void mx4_direct_kernel(Mx4Product p, uint32_t 
 // A workgroup makes a run of tiles along n with the same rows of A: the next
 // tile's first chunk arrives while the last one of a tile is multiplied, and a
 // tile's stores are under way while the next is begun.
+//
+// 8192 x 8192 x 8192 to bfloat16: 275 us, 4.0 PF (the matrix instructions
+// alone, from registers, 6.45 PF: the clock falls to 1.3-1.6 GHz; here 1.8 GHz
+// with the matrix cores busy 53 % of the cycles).  Without the copies of operands
+// it would be 208 us, without the stores 249; operands that all come from the
+// XCD's cache change nothing.  128 lists of 512 rows on average, 2048 x 2048: 240
+// us, of which the stores are 65 (268 MB), the matrices from memory 20, rows that
+// only fill tiles up 28.  128 x 128 tiles for both: 365 and 289 us.
 //
 // ONE: rows of at most one chunk (d <= 256) and single tiles, bound by the
 // stores of the results: small tiles in row order, several workgroups a CU,

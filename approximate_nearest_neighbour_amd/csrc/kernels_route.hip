@@ -22,9 +22,10 @@ constexpr int kSortChunk = 2048; // slots of one workgroup
 constexpr int kSortBits = 11;    // bits of one pass
 constexpr int kSortBins = 1 << kSortBits;
 
-// Up to this many slots and lists the sort is one workgroup of 16 waves (8192
-// slots of 1024 lists: 13.7 us a call, against 15.6 us in three launches; 2048
-// slots: 7.1 us).
+// Up to this many slots and lists the sort is one workgroup of 16 waves: 512
+// slots of 64 lists 3.6 us (5.3 us a call, three launches 10.6).  At 8192 slots a
+// call takes 9.3 us of 64 lists and 12.6 of 1024; 16,384 slots in three launches
+// 10.6 and 12.8.
 constexpr int kSoloSlots = 8192;
 constexpr int kSoloBins = 1088;
 
@@ -116,7 +117,11 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(SortPass s)
     }
 }
 
-// Every slot to its place: start of its bin, plus the bin's slots of earlier
+// Every slot to its place.  Ranks come from ballots, a bit of the bin each, so
+// that equal bins keep their order and no atomic decides it.  320,000 slots of
+// 1024 lists: 8.5 us here, 4.7 us for the counts and 5.2 us for their sums.
+//
+// The place: the start of its bin, plus the bin's slots of earlier
 // workgroups, of earlier waves of this one (each wave has a contiguous part of
 // the chunk) and of earlier lanes.  SOLO: the one workgroup of a small sort,
 // which has all counts itself, and so is the whole sort in one launch.
@@ -322,9 +327,10 @@ static int row_lanes(int d)
     return l;
 }
 
-// rows[p] = w x[t] of the slot at p, zero where no slot is.  A thread has one
-// piece of kRowsAtOnce rows that lie `step` apart, so that as many loads are
-// under way: they wait for their slot numbers, and the stores for them.
+// rows[p] = w x[t] of the slot at p (rounded once), zero where no slot is.  A
+// thread has one piece of kRowsAtOnce rows that lie `step` apart, so that as many
+// loads are under way: they wait for their slot numbers, and the stores for them.
+// Bound by the rows written: 320,000 of 128 float32 35 us, 4.7 TB/s.
 constexpr int kRowsAtOnce = 4;
 
 template <typename T, bool NT>
@@ -375,7 +381,9 @@ __global__ __launch_bounds__(256) void route_gather_kernel(const T *__restrict__
 // y[t] = sum over j of w[t][j] rows[pos[t][j]], j ascending in float32,
 // rounded once; slots without a position add nothing (row 0 is read in their
 // place and dropped, so that a batch of loads has no branch in it).  A thread
-// has one piece of a vector, kSlotsAtOnce of its rows under way together.
+// has one piece of a vector, kSlotsAtOnce of its rows under way together.  Bound
+// by the rows read: 10,000 vectors of 32 rows of 128 float32 33 us, 5.2 TB/s;
+// 16,384 of 8 rows of 2048 bfloat16 133 us, 4.5 TB/s.
 constexpr int kSlotsAtOnce = 8;
 
 template <typename T>
@@ -441,8 +449,10 @@ __global__ __launch_bounds__(256) void route_combine_kernel(const T *__restrict_
 }
 
 // Gradient of the weighted sum, a group of lanes a slot: d_rows[p] = w dy[t]
-// and d_weights[slot] = <dy[t], rows[p]>.  The same group also clears row
-// number slot when no slot sits there.
+// and d_weights[slot] = <dy[t], rows[p]>, summed in float32 in an order that
+// depends on d alone.  The same group also clears row number slot when no slot
+// sits there.  Bound by the rows read and written: 131,072 of 2048 bfloat16 223
+// us, 5.1 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void route_combine_grad_kernel(
     const T *__restrict__ grad, const T *__restrict__ rows, int64_t n, int d, int lanes, FastDiv k,
