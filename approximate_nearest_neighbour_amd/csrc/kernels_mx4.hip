@@ -490,21 +490,27 @@ struct TileOrder {
     }
 };
 
-template <typename T, bool LIST, int WM, int WN, int MW, int NW, bool ONE>
-__global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, TileOrder order,
-                                                                int most)
+// KG: groups of MW x NW waves of a workgroup that share the chunks of one tile
+// out between them (two chunks in a row each) and join their sums through LDS.
+template <typename T, bool LIST, int WM, int WN, int MW, int NW, int KG, bool ONE>
+__global__ __launch_bounds__(64 * MW * NW * KG) void mx4_tile_kernel(Mx4Product p, TileOrder order,
+                                                                     int most)
 {
     constexpr bool PAIR = sizeof(T) == 2;
     constexpr int WAVES = MW * NW, TM = 32 * WM * MW, TN = 32 * WN * NW;
     constexpr int CA = TM / (8 * WAVES), CB = TN / (8 * WAVES); // copies of a wave, of a chunk
     static_assert(TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0 && WAVES % 2 == 0, "copies");
     static_assert(TM + TN <= 64 * WAVES, "a thread per row brings the exponent bytes");
+    constexpr int PLACE = (TM + TN) * 128; // bytes of a chunk
     // two objects, so that the compiler knows a copy into one from a read of the other
-    __shared__ __align__(16) uint8_t code0[(TM + TN) * 128], code1[ONE ? 16 : (TM + TN) * 128];
-    __shared__ uint32_t scale[ONE ? 1 : 2][2][TM + TN];
+    __shared__ __align__(16) uint8_t both0[KG * PLACE], both1[ONE ? 16 : KG * PLACE];
+    __shared__ uint32_t scales[KG][ONE ? 1 : 2][2][TM + TN];
 
     const int lane = lane_id();
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int wave_all = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int kg = KG == 1 ? 0 : wave_all / WAVES, wave = KG == 1 ? wave_all : wave_all % WAVES;
+    uint8_t *const code0 = both0 + kg * PLACE, *const code1 = both1 + kg * PLACE;
+    auto &scale = scales[kg];
     const uint32_t block = blockIdx.x + p.block0;
     uint32_t mt, nr;
     if constexpr (ONE) { // bound by its stores: workgroups side by side write side by side
@@ -582,7 +588,7 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
     };
     clear();
     if (LIST && tile.e == p.nlist) {
-        for (int t = 0; t < run; ++t)
+        for (int t = 0; t < run && kg == 0; ++t)
             put(n0 + t * TN);
         return;
     }
@@ -618,23 +624,26 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
         return buffer_of(p.b, (brow0 + t * TN) * p.kb * 16, brows * p.kb * 16);
     };
     const int chunks = (p.kb + 7) >> 3;
+    // chunks of a group, and which chunk of the row its chunk c is
+    const int own = KG == 1 ? chunks : (chunks + 2 * KG - 1) / (2 * KG) * 2;
+    auto chunk_of = [&](int c) { return KG == 1 ? c : (c & ~1) * KG + 2 * kg + (c & 1); };
     // Chunk c into its LDS place.  What lies past a row's end (the next row's
     // blocks, or zeros past the matrix) is multiplied too, with exponent bytes
     // of zero; rows past the last one of B give results that are not stored.
     auto fetch_a = [&](int c, uint8_t *to) {
-        const int at = __builtin_amdgcn_readfirstlane(c * 128);
+        const int at = __builtin_amdgcn_readfirstlane(chunk_of(c) * 128);
 #pragma unroll
         for (int j = 0; j < CA; ++j)
             copy16_to_lds(abuf, off[j], at, to + wave * 1024 + j * WAVES * 1024);
     };
     auto fetch_b = [&](__amdgpu_buffer_rsrc_t from, int c, uint8_t *to) {
-        const int at = __builtin_amdgcn_readfirstlane(c * 128);
+        const int at = __builtin_amdgcn_readfirstlane(chunk_of(c) * 128);
 #pragma unroll
         for (int j = 0; j < CB; ++j)
             copy16_to_lds(from, off[CA + j], at, to + wave * 1024 + j * WAVES * 1024);
     };
     // exponent bytes: a thread per row of A, then of B
-    const int srow = (int)threadIdx.x;
+    const int srow = (int)threadIdx.x - kg * 64 * WAVES;
     const bool of_a = srow < TM;
     const uint8_t *sfrom = of_a ? p.as : p.bs;
     const int64_t sline = of_a ? a_row(srow) : brow0 + srow - TM;
@@ -642,11 +651,11 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
     ScaleBytes bytes;
     auto load_scales = [&](int t, int c) { // chunks c and c + 1 of tile t
         const int64_t line = min(of_a ? sline : sline + t * TN, slast);
-        bytes.load(sfrom, line * p.kb + min(c, chunks - 1) * 8, (slast + 1) * p.kb);
+        bytes.load(sfrom, line * p.kb + min(chunk_of(c), chunks - 1) * 8, (slast + 1) * p.kb);
     };
     auto put_scales = [&](int c, auto odd) { // chunk c, the first or the other one loaded
         constexpr int ODD = decltype(odd)::value;
-        const uint64_t v = bytes.get<ODD>(p.kb - c * 8);
+        const uint64_t v = bytes.get<ODD>(p.kb - chunk_of(c) * 8);
         if (TM + TN == 64 * WAVES || srow < TM + TN) {
             const uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
             scale[ODD][0][srow] = __builtin_amdgcn_perm(hi, lo, 0x06040200);
@@ -723,6 +732,28 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
         wait_vm<0>();  // the next chunk (and what was stored before this one)
         lds_barrier(); // every wave's part of it is here, and this one's last reads done
     };
+    // the groups' sums into the first one's, in the groups' order; no copy is under
+    // way and every operand read
+    auto join = [&] {
+        static_assert(KG == 1 || (WM == 1 && WN == 1 && WAVES * 8 * 256 <= PLACE), "sums in LDS");
+        float *f0 = reinterpret_cast<float *>(both0), *f1 = reinterpret_cast<float *>(both1);
+        const int at = wave * 512 + lane;
+        if (kg > 0)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                f0[kg * (PLACE / 4) + at + q * 64] = acc[0][0][q];
+                f1[kg * (PLACE / 4) + at + q * 64] = acc[0][0][8 + q];
+            }
+        lds_barrier();
+        if (kg == 0)
+#pragma unroll
+            for (int g = 1; g < KG; ++g)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    acc[0][0][q] += f0[g * (PLACE / 4) + at + q * 64];
+                    acc[0][0][8 + q] += f1[g * (PLACE / 4) + at + q * 64];
+                }
+    };
     auto bnow = b_of(0);
     load_scales(0, 0);
     fetch_a(0, code0);
@@ -739,8 +770,8 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
         for (int t = 0; t < run; ++t) { // more than one only if a row's chunks are even in number
             const auto bnext = b_of(t + 1);
 #pragma unroll 1
-            for (int c = 0; c < chunks; c += 2) {
-                const bool last = c + 2 >= chunks;
+            for (int c = 0; c < own; c += 2) {
+                const bool last = c + 2 >= own;
                 const int after = last ? 0 : c + 2;
                 chunk(
                     even, c > 0, code0, code0 + TM * 128,
@@ -752,7 +783,7 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
                         put_scales(c + 1, odd);
                         load_scales(last ? t + 1 : t, after);
                     });
-                if (c + 1 < chunks)
+                if (KG > 1 || c + 1 < own)
                     chunk(
                         odd, true, code1, code1 + TM * 128,
                         [&] {
@@ -763,6 +794,11 @@ __global__ __launch_bounds__(64 * MW * NW) void mx4_tile_kernel(Mx4Product p, Ti
             }
             bnow = bnext;
             multiply(3);
+            if constexpr (KG > 1) {
+                join();
+                if (kg > 0)
+                    return;
+            }
             put(n0 + t * TN);
             clear();
         }
@@ -805,7 +841,7 @@ static hipError_t launch_blocks(Kernel kernel, int64_t blocks, int threads, hipS
     return hipGetLastError();
 }
 
-template <typename T, bool LIST, int WM, int WN, int MW, int NW, bool ONE = false>
+template <typename T, bool LIST, int WM, int WN, int MW, int NW, int KG = 1, bool ONE = false>
 static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
 {
     constexpr int64_t TM = 32 * WM * MW, TN = 32 * WN * NW;
@@ -816,7 +852,9 @@ static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
         mt = p.m / TM + ends;
         likely = p.m / TM + ends / 2 + 1;
     }
-    const int run = ONE ? 1 : run_length<LIST>(likely, nt, (p.kb + 7) / 8, MW * NW == 8 ? 256 : 512);
+    const int run = ONE || KG > 1 ? 1
+                                  : run_length<LIST>(likely, nt, (p.kb + 7) / 8,
+                                                     MW * NW == 8 ? 256 : 512);
     TileOrder order;
     order.mt = (uint32_t)mt;
     order.nruns = (uint32_t)((nt + run - 1) / run);
@@ -825,8 +863,8 @@ static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
     if (LIST) // whole groups, the same number for every XCD
         blocks = ((mt + order.high - 1) / order.high + 7) / 8 * 8 * order.high * order.nruns;
     order.blocks = (uint32_t)blocks;
-    return launch_blocks(mx4_tile_kernel<T, LIST, WM, WN, MW, NW, ONE>, blocks, 64 * MW * NW, stream,
-                         p, order, run);
+    return launch_blocks(mx4_tile_kernel<T, LIST, WM, WN, MW, NW, KG, ONE>, blocks,
+                         64 * MW * NW * KG, stream, p, order, run);
 }
 
 template <typename T, bool LIST, int KS>
@@ -837,10 +875,11 @@ static hipError_t direct_as(const Mx4Product &p, int64_t mt, hipStream_t stream)
 }
 
 // Which kernel.  The direct one reads B once for every 16 rows of A, the tiles
-// once for 128 or 256, but they take 13 us and more for their chunks one after
+// once for 64 to 256, but they take 10 us and more for their chunks one after
 // the other (d 4096).  So the direct one where a matrix has few rows to
-// multiply, or all is small: 32 rows by 8192, d 4096 (11.5 us, tiles 13.7 us) is
-// about the limit (48 rows: 15.7 and 13.8 us).  In lists of 8 rows on average
+// multiply, or all is small: 32 rows by 8192, d 4096 (11.5 us, tiles of up to 64
+// rows 11.2 us) is about the limit (48 rows: 15.7 us; 32 rows by 4096, d 8192:
+// 12.5 us, tiles 15.7 us).  In lists of 8 rows on average
 // 33 us against 40 us (64 lists, 2048 x 2048), in lists of 16 49 us against 39 us.
 template <typename T, bool LIST>
 static hipError_t product_of(const Mx4Product &p, hipStream_t stream)
@@ -863,21 +902,29 @@ static hipError_t product_of(const Mx4Product &p, hipStream_t stream)
             return direct_as<T, LIST, 4>(p, mt, stream);
         return direct_as<T, LIST, 8>(p, mt, stream);
     }
+    auto tiles = [&](int64_t high, int64_t wide) {
+        const int64_t parts = LIST ? (p.m < p.nlist ? p.m : p.nlist) / 2 : 0; // lists end inside
+        return ((p.m + high - 1) / high + parts) * ((p.n + wide - 1) / wide);
+    };
+    if constexpr (!LIST) {
+        if (p.kb <= 8)
+            return tiles_as<T, false, 1, 1, 2, 4, 1, true>(p, stream);
+    }
+    // Few tiles of long rows wait for their chunks one after the other: tiles of
+    // 64 x 64, their chunks shared out between two groups of four waves, while
+    // all are under way together (two a CU).  128 x 4096 x 8192 24.4 -> 15.8 us,
+    // 512 x 4096 x 8192, which is 512 of them, 29.9 -> 24.7, x 4096 16.6 -> 15.0,
+    // x 2048 10.5 -> 11.0; 768 x 4096 x 8192 29.1 -> 36.5.  16 lists of 32 rows, 512
+    // x 4096: 15.9 -> 13.5 us.
+    if (p.kb > 64 && tiles(64, 64) <= 512)
+        return tiles_as<T, LIST, 1, 1, 2, 2, 2>(p, stream);
     // Large tiles (256 x 256) take about three times as long as middle ones (128 x
     // 128) a round of 256: 40 us against 14 us a quarter of the results (d 4096).
     // Small ones (64 x 128) where few tiles wait for their chunks more than for
     // the matrix cores: 512 x 1024 x 4096 11.7 us against 14.4 us, 1024 x 4096 x
     // 4096, which is 512 of them, 28.8 us against 18.8 us.
-    auto tiles = [&](int64_t high, int64_t wide) {
-        const int64_t parts = LIST ? (p.m < p.nlist ? p.m : p.nlist) / 2 : 0; // lists end inside
-        return ((p.m + high - 1) / high + parts) * ((p.n + wide - 1) / wide);
-    };
     const bool large = 3 * ((tiles(256, 256) + 255) / 256) <= (tiles(128, 128) + 255) / 256;
     const bool small = tiles(64, 128) <= (p.kb <= 32 ? 512 : 256);
-    if constexpr (!LIST) {
-        if (p.kb <= 8)
-            return tiles_as<T, false, 1, 1, 2, 4, true>(p, stream);
-    }
     if (large)
         return tiles_as<T, LIST, 4, 2, 2, 4>(p, stream);
     if (small)

@@ -152,6 +152,44 @@ def test_product(m, n, d, dtype):
     check_product(out, va @ vb.T, np.abs(va) @ np.abs(vb).T, d, dtype)
 
 
+@pytest.mark.parametrize("m,n,d", [
+    (200, 2500, 2080), (130, 1000, 8192), (65, 1700, 8200), (1000, 1030, 2113), (17, 8200, 4100)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_product_of_few_tiles_of_long_rows(m, n, d, dtype):
+    test_product(m, n, d, dtype)
+
+
+# tiles of 128 x 128; of 256 x 256; runs of those along n (an even number of chunks)
+@pytest.mark.parametrize("m,n,d", [
+    (1300, 4100, 1100), (2600, 4200, 1100), (4200, 8200, 512), (2570, 8203, 1024)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_product_of_many_tiles(m, n, d, dtype):
+    rng = np.random.default_rng(m + n + d)
+    a, b = random_mx4(rng, m, d), random_mx4(rng, n, d)
+    if dtype == torch.float16:
+        a = (a[0], (a[1] - 8).astype(np.uint8))
+    out = A.ivfpq_mx4_product_ex(cuda(a), cuda(b), dtype=dtype)
+    rows = np.unique(np.r_[0:m:41, m - 9:m])
+    va, vb = R.values(a[0][rows], a[1][rows], d), R.values(*b, d)
+    check_product(out[torch.from_numpy(rows).cuda()], va @ vb.T, np.abs(va) @ np.abs(vb).T, d,
+                  dtype)
+    # every row: its sum against the product with the columns' sum
+    total = R.values(*a, d) @ vb.sum(axis=0)
+    mag = np.abs(R.values(*a, d)) @ np.abs(vb).sum(axis=0)
+    err = np.abs(np64(out.double().sum(dim=1)) - total)
+    assert (err <= mag * (d * 2.0 ** -22 + 2 * UNIT[dtype]) + n * 2.0 ** -25).all()
+
+
+def test_product_nan_in_each_chunk_of_long_rows():
+    rng = np.random.default_rng(16)
+    m, n, d = 140, 1500, 2592                    # 81 blocks, the last of them alone in its chunk
+    a, b = random_mx4(rng, m, d), random_mx4(rng, n, d)
+    for row, block in enumerate(range(0, 81)):
+        a[1][row, block] = 255
+    out = A.ivfpq_mx4_product_ex(cuda(a), cuda(b)).cpu().numpy()
+    assert np.isnan(out[:81]).all() and np.isfinite(out[81:]).all()
+
+
 def test_product_blocks_land_where_they_belong():
     # one block of one row at a time set: catches any permutation of rows,
     # blocks, nibbles or scales
@@ -259,7 +297,7 @@ def make_lists(rng, t, k, nlist, drop, hot=None):
 @pytest.mark.parametrize("t,k,nlist,n,d,drop", [
     (1, 1, 1, 16, 32, 0.0), (1, 2, 8, 33, 70, 0.0), (5, 2, 4, 130, 128, 0.2),
     (40, 4, 70, 65, 96, 0.1), (300, 2, 3, 257, 256, 0.0), (600, 1, 2, 512, 544, 0.05),
-    (513, 3, 130, 48, 64, 0.3), (20, 2, 8, 40, 1000, 1.0)])
+    (513, 3, 130, 48, 64, 0.3), (20, 2, 8, 40, 1000, 1.0), (130, 2, 3, 200, 2300, 0.1)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_list_product(t, k, nlist, n, d, drop, dtype):
     rng = np.random.default_rng(t + 10 * k + 100 * nlist + n)
@@ -281,6 +319,30 @@ def test_list_product(t, k, nlist, n, d, drop, dtype):
     sorted_a = (a[0][src], a[1][src])
     again = A.ivfpq_mx4_list_product_ex(cuda(sorted_a), cuda(b), off, dtype=dtype)
     assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("t,nlist,n,d", [
+    (1650, 3, 4200, 512), (2500, 5, 2100, 544), (1000, 40, 1100, 1030)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_list_product_of_many_tiles(t, nlist, n, d, dtype):
+    rng = np.random.default_rng(t + nlist + n)
+    lists = make_lists(rng, t, 2, nlist, 0.02)
+    offsets, order, _ = R.route_sort(lists, nlist)
+    a = random_mx4(rng, t, d)
+    bc, bs = random_mx4(rng, nlist * n, d)
+    b = (bc.reshape(nlist, n, -1), bs.reshape(nlist, n, -1))
+    if dtype == torch.float16:
+        a = (a[0], (a[1] - 8).astype(np.uint8))
+    off, orde = torch.from_numpy(offsets).cuda(), torch.from_numpy(order).cuda()
+    out = A.ivfpq_mx4_list_product_ex(cuda(a), cuda(b), off, order=orde, k=2, dtype=dtype)
+    va, vb = R.values(*a, d), R.values(*b, d)
+    for e in range(nlist):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        rows = np.unique(np.r_[lo:hi:17, max(lo, hi - 5):hi])
+        x = va[order[rows] // 2]
+        check_product(out[torch.from_numpy(rows).cuda()], x @ vb[e].T, np.abs(x) @ np.abs(vb[e]).T,
+                      d, dtype)
+    assert (out[offsets[nlist]:] == 0).all()
 
 
 def test_list_product_one_list_takes_all():
