@@ -194,7 +194,8 @@ __device__ __forceinline__ ListTile find_tile(const int32_t *offsets, int nlist,
         const uint64_t past = __ballot(base + upto > t);
         if (past) {
             const int who = __builtin_ctzll(past);
-            const uint32_t before = base + (uint32_t)__builtin_amdgcn_readlane((int)(upto - tiles), who);
+            const uint32_t before =
+                base + (uint32_t)__builtin_amdgcn_readlane((int)(upto - tiles), who);
             const int64_t plo = __builtin_amdgcn_readlane((int)lo, who);
             const int64_t phi = __builtin_amdgcn_readlane((int)hi, who);
             const int64_t p0 = plo + (int64_t)(t - before) * TM;
@@ -389,7 +390,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t *base,
                                                             int64_t bytes)
 {
     from = uniform(from);
-    const uint32_t size = (uint32_t)uniform(min(max(bytes - from, (int64_t)0), (int64_t)0xFFFFFFFF));
+    const uint32_t size =
+        (uint32_t)uniform(min(max(bytes - from, (int64_t)0), (int64_t)0xFFFFFFFF));
     const uint8_t *p = base + from;
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)size, 0x00027000);
 }
@@ -879,8 +881,9 @@ static hipError_t direct_as(const Mx4Product &p, int64_t mt, hipStream_t stream)
 // the other (d 4096).  So the direct one where a matrix has few rows to
 // multiply, or all is small: 32 rows by 8192, d 4096 (11.5 us, tiles of up to 64
 // rows 11.2 us) is about the limit (48 rows: 15.7 us; 32 rows by 4096, d 8192:
-// 12.5 us, tiles 15.7 us).  In lists of 8 rows on average
-// 33 us against 40 us (64 lists, 2048 x 2048), in lists of 16 49 us against 39 us.
+// 12.5 us, tiles 15.7 us).  In 64 lists, 2048 x 2048, of 4 rows on average 29 us
+// against 28 to 32, of 8 rows 33 to 38 us against 32; in 128 lists, 1024 x 1024,
+// of 4 rows 18 us against 15, of 8 rows 21 to 23 us against 15.
 template <typename T, bool LIST>
 static hipError_t product_of(const Mx4Product &p, hipStream_t stream)
 {
@@ -892,7 +895,7 @@ static hipError_t product_of(const Mx4Product &p, hipStream_t stream)
     // what the tiles' 32-bit offsets and 16-byte reads of exponent bytes take
     const bool fits = !(LIST && p.order && p.arows * p.kb * 16 >= (int64_t)1 << 32) &&
                       brows * p.kb >= 16 && p.arows * p.kb >= 16;
-    const bool few = LIST ? p.m <= 8ll * p.nlist : p.m <= 16 || waves * p.kb <= 1024 * 128;
+    const bool few = LIST ? p.m <= 2ll * p.nlist : p.m <= 16 || waves * p.kb <= 1024 * 128;
     if (few || !fits) {
         // blocks of a row are split only as far as it takes to have 16 waves a
         // CU, with 8 KB each under way, or a turn for each
@@ -920,11 +923,17 @@ static hipError_t product_of(const Mx4Product &p, hipStream_t stream)
         return tiles_as<T, LIST, 1, 1, 2, 2, 2>(p, stream);
     // Large tiles (256 x 256) take about three times as long as middle ones (128 x
     // 128) a round of 256: 40 us against 14 us a quarter of the results (d 4096).
+    // Lists have to fill them: 64 lists, 2048 x 2048, of 512 rows on average 135 us
+    // against 147 us, of 256 87 us against 86 us, of 128 71 us against 61 us.
     // Small ones (64 x 128) where few tiles wait for their chunks more than for
     // the matrix cores: 512 x 1024 x 4096 11.7 us against 14.4 us, 1024 x 4096 x
-    // 4096, which is 512 of them, 28.8 us against 18.8 us.
-    const bool large = 3 * ((tiles(256, 256) + 255) / 256) <= (tiles(128, 128) + 255) / 256;
-    const bool small = tiles(64, 128) <= (p.kb <= 32 ? 512 : 256);
+    // 4096, which is 512 of them, 28.8 us against 18.8 us.  And where lists would
+    // leave middle ones empty: 32 rows on average 40 us against 42 us, 64 rows 51
+    // us against 52 us (64 rows each 46 us against 38 us).
+    const bool large = (!LIST || p.m > 256ll * p.nlist) &&
+                       3 * ((tiles(256, 256) + 255) / 256) <= (tiles(128, 128) + 255) / 256;
+    const bool small = tiles(64, 128) <= (p.kb <= 32 ? 512 : 256) ||
+                       (LIST && p.m <= 32ll * p.nlist);
     if (large)
         return tiles_as<T, LIST, 4, 2, 2, 4>(p, stream);
     if (small)
