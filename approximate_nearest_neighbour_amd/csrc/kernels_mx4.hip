@@ -922,12 +922,13 @@ static hipError_t product_of(const Mx4Product &p, hipStream_t stream)
     if (p.kb > 64 && tiles(64, 64) <= 512)
         return tiles_as<T, LIST, 1, 1, 2, 2, 2>(p, stream);
     // Large tiles (256 x 256) take about three times as long as middle ones (128 x
-    // 128) a round of 256: 40 us against 14 us a quarter of the results (d 4096).
+    // 128) a round of 256: 3000 x 4000 x 4096 35.0 us against 41.2 us, 2048 x 4096 x
+    // 4096, which is half a round of them, 32.7 us against 26.3 us.
     // Lists have to fill them: 64 lists, 2048 x 2048, of 512 rows on average 135 us
     // against 147 us, of 256 87 us against 86 us, of 128 71 us against 61 us.
     // Small ones (64 x 128) where few tiles wait for their chunks more than for
-    // the matrix cores: 512 x 1024 x 4096 11.7 us against 14.4 us, 1024 x 4096 x
-    // 4096, which is 512 of them, 28.8 us against 18.8 us.  And where lists would
+    // the matrix cores: 1024 x 2048 x 2048 9.4 us against 9.9 us, 2048 x 2048 x
+    // 4096, which is 512 of them, 29.3 us against 18.4 us.  And where lists would
     // leave middle ones empty: 32 rows on average 40 us against 42 us, 64 rows 51
     // us against 52 us (64 rows each 46 us against 38 us).
     const bool large = (!LIST || p.m > 256ll * p.nlist) &&
