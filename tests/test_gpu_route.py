@@ -40,9 +40,10 @@ def sort(lists, nlist):
     (1, 1, 1, 0.0, 0.0), (1, 8, 64, 0.0, 0.0), (3, 2, 5, 0.3, 0.0), (64, 1, 2, 0.0, 0.9),
     (100, 3, 1, 0.5, 0.0), (700, 3, 129, 0.1, 0.2), (683, 3, 7, 0.0, 0.0), (4097, 1, 8, 0.0, 1.0),
     (5000, 8, 1024, 0.02, 0.3), (9999, 1, 2047, 0.0, 0.0), (3000, 4, 2048, 0.1, 0.5),
-    (2500, 2, 100000, 0.1, 0.3), (500, 2, (1 << 22) - 1, 0.1, 0.1), (50, 4, 16, 1.0, 0.0), (16384, 1, 1087, 0.05, 0.1),
-    (16385, 1, 1087, 0.05, 0.1), (2000, 8, 1088, 0.0, 0.0), (5, 200, 3, 0.2, 0.0),
-    (70000, 2, 3000, 0.01, 0.2)])
+    (2500, 2, 100000, 0.1, 0.3), (500, 2, (1 << 22) - 1, 0.1, 0.1), (50, 4, 16, 1.0, 0.0),
+    (16384, 1, 1087, 0.05, 0.1), (16385, 1, 1087, 0.05, 0.1), (2000, 8, 1088, 0.0, 0.0),
+    (5, 200, 3, 0.2, 0.0), (70000, 2, 3000, 0.01, 0.2), (8192, 1, 1087, 0.1, 0.2),
+    (8193, 1, 1087, 0.1, 0.2), (150001, 8, 700, 0.05, 0.1), (400003, 2, 5000, 0.02, 0.1)])
 def test_sort(t, k, nlist, drop, hot):
     lists = make_lists(np.random.default_rng(t * k + nlist), t, k, nlist, drop, hot)
     want = R.route_sort(lists, nlist)
