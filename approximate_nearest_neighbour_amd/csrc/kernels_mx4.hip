@@ -355,14 +355,15 @@ __global__ __launch_bounds__(512) void mx4_direct_kernel(Mx4Product p, uint32_t 
 // Results: for float32 a lane holds one column of sixteen rows, and a store
 // covers 128 bytes of two rows.  For 16-bit outputs the operands change places:
 // a lane holds four times four consecutive columns of one row, B's rows dealt
-// to the sums so that pairs of these are eight consecutive columns (deal_row),
-// and a store is 16 bytes.
+// to the sums so that pairs of these are eight consecutive columns (deal_row).
+// In all but the small tiles they go through LDS, so that a store covers 64 or 128
+// bytes of each row.
 //
 // A workgroup makes a run of tiles along n with the same rows of A: the next
 // tile's first chunk arrives while the last one of a tile is multiplied, and a
 // tile's stores are under way while the next is begun.
 //
-// 8192 x 8192 x 8192 to bfloat16: 275 us, 4.0 PF (the matrix instructions
+// 8192 x 8192 x 8192 to bfloat16: 266 us, 4.1 PF (the matrix instructions
 // alone, from registers, 6.45 PF: the clock falls to 1.3-1.6 GHz; here 1.8 GHz
 // with the matrix cores busy 53 % of the cycles).  Without the copies of operands
 // it would be 208 us, without the stores 249; operands that all come from the
@@ -545,6 +546,8 @@ __global__ __launch_bounds__(64 * MW * NW * KG) void mx4_tile_kernel(Mx4Product 
                 for (int q = 0; q < 16; ++q)
                     acc[i][j][q] = 0.f;
     };
+    typedef T T8 __attribute__((ext_vector_type(8)));
+    typedef T T8U __attribute__((ext_vector_type(8), aligned(sizeof(T))));
     // the sums to the tile's rows, columns at and on
     auto put = [&](int at) {
         at += wn * WN * 32;
@@ -568,7 +571,7 @@ __global__ __launch_bounds__(64 * MW * NW * KG) void mx4_tile_kernel(Mx4Product 
                             out[row * p.n + n] = (T)acc[i][j][q];
                     }
             }
-        } else {
+        } else if constexpr (WN == 1 && !ONE) {
 #pragma unroll
             for (int i = 0; i < WM; ++i) {
                 const int64_t row = row0 + (wm * WM + i) * 32 + r;
@@ -586,6 +589,55 @@ __global__ __launch_bounds__(64 * MW * NW * KG) void mx4_tile_kernel(Mx4Product 
                         o.store(out + row * p.n + n, p.n - n);
                     }
             }
+        } else {
+            // Through LDS (this wave's part of what no copy is on its way to), so
+            // that a store is whole rows of the wave's columns: 8192 x 8192 x 8192
+            // 281 -> 266 us, 8000 x 8001 x 1024 92 -> 58 us, 1000 x 100,001 x 96 91 ->
+            // 54 us.  Small tiles, which are not bound by their stores, store 16 bytes
+            // a lane themselves: 128 lists of 16 rows, 1024 x 1024, 18.5 us, through
+            // LDS 21.8 us.
+            constexpr int BR = WN * 4, ROWB = BR * 16, PART = (TM + TN) * 128 / WAVES;
+            constexpr int SLAB = PART / (32 * ROWB) < WM ? PART / (32 * ROWB) : WM;
+            static_assert(SLAB >= 1 && WM % SLAB == 0, "rows through LDS");
+            uint8_t *mine = (ONE ? code0 : code1) + wave * PART;
+#pragma unroll
+            for (int i0 = 0; i0 < WM; i0 += SLAB) {
+#pragma unroll
+                for (int i = 0; i < SLAB; ++i)
+#pragma unroll
+                    for (int j = 0; j < WN; ++j)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            T8 o;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                o[e] = (T)acc[i0 + i][j][q * 8 + e];
+                            const int b = (j * 4 + q * 2 + half) ^ (r & (BR - 1));
+                            *reinterpret_cast<T8 *>(mine + (i * 32 + r) * ROWB + b * 16) = o;
+                        }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+                for (int k = 0; k < SLAB * 32 * BR / 64; ++k) {
+                    const int line = (k * 64 + lane) / BR, b = lane % BR;
+                    const T8 o = *reinterpret_cast<const T8 *>(mine + line * ROWB +
+                                                               (b ^ (line & (BR - 1))) * 16);
+                    const int64_t row = row0 + (wm * WM + i0) * 32 + line;
+                    const int n = at + b * 8;
+                    if (row >= tile.p1 || n >= p.n)
+                        continue;
+                    T *to = out + row * p.n + n;
+                    if (n + 8 <= p.n) {
+                        *reinterpret_cast<T8U *>(to) = o;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (n + e < p.n)
+                                to[e] = o[e];
+                    }
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            }
+            lds_barrier(); // before copies to where other waves' rows may still lie
         }
     };
     clear();
