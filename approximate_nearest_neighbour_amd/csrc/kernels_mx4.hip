@@ -8,6 +8,7 @@
 // (MXFP4), which the matrix cores of gfx950 multiply directly.
 #include "common.hpp"
 #include "internal.hpp"
+#include "mx4_plan.hpp"
 #include "rows.hpp"
 
 namespace ivfpq {
@@ -678,20 +679,21 @@ __global__ __launch_bounds__(64 * MW * NW * KG) void mx4_tile_kernel(Mx4Product 
         return buffer_of(p.b, (brow0 + t * TN) * p.kb * 16, brows * p.kb * 16);
     };
     const int chunks = (p.kb + 7) >> 3;
-    // chunks of a group, and which chunk of the row its chunk c is
-    const int own = KG == 1 ? chunks : (chunks + 2 * KG - 1) / (2 * KG) * 2;
-    auto chunk_of = [&](int c) { return KG == 1 ? c : (c & ~1) * KG + 2 * kg + (c & 1); };
+    const int own = own_chunks(chunks, KG);
+    auto chunk_of = [&](int c) { return row_chunk(c, kg, KG); };
     // Chunk c into its LDS place.  What lies past a row's end (the next row's
     // blocks, or zeros past the matrix) is multiplied too, with exponent bytes
     // of zero; rows past the last one of B give results that are not stored.
+    // `at` is less than a row's bytes, and either buffer starts with a row of its
+    // matrix, so the bytes left are always more than `at`.
     auto fetch_a = [&](int c, uint8_t *to) {
-        const int at = __builtin_amdgcn_readfirstlane(chunk_of(c) * 128);
+        const int at = __builtin_amdgcn_readfirstlane(chunk_byte(c, kg, KG, chunks));
 #pragma unroll
         for (int j = 0; j < CA; ++j)
             copy16_to_lds(abuf, off[j], at, to + wave * 1024 + j * WAVES * 1024);
     };
     auto fetch_b = [&](__amdgpu_buffer_rsrc_t from, int c, uint8_t *to) {
-        const int at = __builtin_amdgcn_readfirstlane(chunk_of(c) * 128);
+        const int at = __builtin_amdgcn_readfirstlane(chunk_byte(c, kg, KG, chunks));
 #pragma unroll
         for (int j = 0; j < CB; ++j)
             copy16_to_lds(from, off[CA + j], at, to + wave * 1024 + j * WAVES * 1024);
@@ -830,6 +832,8 @@ __global__ __launch_bounds__(64 * MW * NW * KG) void mx4_tile_kernel(Mx4Product 
                 chunk(
                     even, c > 0, code0, code0 + TM * 128,
                     [&] {
+                        if (KG == 1 && !second_chunk(c, own))
+                            return;
                         fetch_a(c + 1, code1);
                         fetch_b(bnow, c + 1, code1 + TM * 128);
                     },
@@ -837,10 +841,12 @@ __global__ __launch_bounds__(64 * MW * NW * KG) void mx4_tile_kernel(Mx4Product 
                         put_scales(c + 1, odd);
                         load_scales(last ? t + 1 : t, after);
                     });
-                if (KG > 1 || c + 1 < own)
+                if (KG > 1 || second_chunk(c, own))
                     chunk(
                         odd, true, code1, code1 + TM * 128,
                         [&] {
+                            if (!chunk_after(c, own, t, run))
+                                return;
                             fetch_a(after, code0);
                             fetch_b(last ? bnext : bnow, after, code0 + TM * 128);
                         },

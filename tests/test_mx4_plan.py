@@ -1,0 +1,55 @@
+"""The arithmetic of the 4-bit products on the CPU: the functions that the
+device kernels call (csrc/mx4_plan.hpp), compiled for the host and run by
+tests/mx4_driver.cpp."""
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "approximate_nearest_neighbour_amd", "csrc")
+
+
+@pytest.fixture(scope="module")
+def driver(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("mx4") / "mx4_driver")
+    cmd = ["g++", "-std=c++17", "-O1", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
+           "-I", CSRC, os.path.join(ROOT, "tests", "mx4_driver.cpp"), "-o", exe]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[:2000]
+
+    def ask(lines):
+        out = subprocess.run([exe], input="\n".join(lines) + "\n", capture_output=True, text=True,
+                             check=True).stdout.splitlines()
+        assert len(out) == len(lines)
+        return [[int(v) for v in line.split()[1:]] for line in out]
+    return ask
+
+
+# columns of a tile, groups of waves that share its chunks, longest run of tiles
+TILES = [(64, 2, 1), (128, 1, 1), (128, 1, 2), (128, 1, 8), (256, 1, 1), (256, 1, 4)]
+
+
+def test_no_copy_begins_past_its_matrix(driver):
+    """A copy's chunk offset is subtracted from the bytes that are left of the
+    matrix in the hardware's range check: it has to be less than those, also in
+    the last tile of the last matrix and for the chunks past a row's end."""
+    cases = []
+    for tn, groups, most in TILES:
+        for kb in list(range(1, 35)) + [63, 64, 65, 66, 72, 73, 80, 81, 96, 97, 255, 256, 257]:
+            if most > 1 and (kb + 7) // 8 % 2:
+                continue  # runs are of rows with an even number of chunks
+            for n in (1, tn - 1, tn, tn + 1, 2 * tn + 1, 5 * tn + 3, 8 * tn, 9 * tn + 1):
+                for lists in (1, 3):
+                    cases.append(f"copies {n} {lists} {kb} {tn} {groups} {most}")
+    for case, (issued, past, wrong) in zip(cases, driver(cases)):
+        assert issued > 0 and past == 0 and wrong == 0, case
+
+
+def test_only_chunks_that_are_multiplied_are_copied(driver):
+    # one tile of three chunks: three copies of either operand, and none for a tile after it
+    (issued, _, _), = driver(["copies 100 1 24 128 1 1"])
+    assert issued == 2 * 3
+    # a run of three tiles of two chunks
+    (issued, _, _), = driver(["copies 300 1 16 128 1 4"])
+    assert issued == 2 * 6
