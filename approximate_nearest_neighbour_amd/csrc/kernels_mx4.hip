@@ -526,7 +526,7 @@ __global__ __launch_bounds__(64 * MW * NW * KG) void mx4_tile_kernel(Mx4Product 
     if (mt >= order.mt || nr >= order.nruns)
         return;
     const int n0 = (int)nr * most * TN;
-    const int run = min(most, (p.n - n0 + TN - 1) / TN);
+    const int run = run_tiles(p.n, n0, TN, most);
     ListTile tile{0, (int64_t)mt * TM, min((int64_t)mt * TM + TM, p.m)};
     if constexpr (LIST)
         tile = find_tile<TM>(p.offsets, p.nlist, p.m, mt);

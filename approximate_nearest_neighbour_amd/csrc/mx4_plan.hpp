@@ -40,4 +40,12 @@ __host__ __device__ inline bool chunk_after(int c, int own, int tile, int run)
     return c + 2 < own || tile + 1 < run;
 }
 
+// Tiles of `tn` columns in the run of at most `most` that starts at column n0 < n.
+// n may be up to 2^31 - 16: no sum of columns passes n.
+__host__ __device__ inline int run_tiles(int n, int n0, int tn, int most)
+{
+    const int left = (n - n0 - 1) / tn + 1;
+    return left < most ? left : most;
+}
+
 } // namespace ivfpq

@@ -6,6 +6,9 @@
 //       walks every copy of the last matrix's tiles in the kernel's order (runs of
 //       `most` tiles of `tn` columns) and of a first operand with one row left:
 //       "copies <issued> <begun past the bytes left> <chunks not multiplied once>"
+//   run n tn most
+//       the runs of tiles that start along n columns:
+//       "run <runs> <tiles in all> <tiles of the first run> <of the last run>"
 #include "mx4_plan.hpp"
 
 #include <cstdio>
@@ -20,8 +23,7 @@ static void copies(long long n, long long lists, int kb, long long tn, int group
     const long long row = 16ll * kb, brows = lists * n, brow0 = brows - n;
     long long issued = 0, past = 0, wrong = 0;
     for (long long n0 = 0; n0 < n; n0 += most * tn) {
-        const long long tiles = (n - n0 + tn - 1) / tn;
-        const int run = (int)(most < tiles ? most : tiles);
+        const int run = run_tiles((int)n, (int)n0, (int)tn, (int)most);
         for (int g = 0; g < groups; ++g) {
             // a copy of chunk c of tile t's rows and of a last row of the first operand
             auto copy = [&](int t, int c) {
@@ -51,6 +53,18 @@ static void copies(long long n, long long lists, int kb, long long tn, int group
     std::printf("copies %lld %lld %lld\n", issued, past, wrong);
 }
 
+static void runs(int n, int tn, int most)
+{
+    long long count = 0, tiles = 0, first = 0, last = 0;
+    for (long long n0 = 0; n0 < n; n0 += (long long)most * tn) {
+        last = run_tiles(n, (int)n0, tn, most);
+        first = count == 0 ? last : first;
+        tiles += last;
+        ++count;
+    }
+    std::printf("run %lld %lld %lld %lld\n", count, tiles, first, last);
+}
+
 int main()
 {
     char what[32];
@@ -61,6 +75,11 @@ int main()
                 if (std::scanf("%lld", &v[i]) != 1)
                     return 1;
             copies(v[0], v[1], (int)v[2], v[3], (int)v[4], v[5]);
+        } else if (!std::strcmp(what, "run")) {
+            for (int i = 0; i < 3; ++i)
+                if (std::scanf("%lld", &v[i]) != 1)
+                    return 1;
+            runs((int)v[0], (int)v[1], (int)v[2]);
         } else {
             return 1;
         }

@@ -53,3 +53,15 @@ def test_only_chunks_that_are_multiplied_are_copied(driver):
     # a run of three tiles of two chunks
     (issued, _, _), = driver(["copies 300 1 16 128 1 4"])
     assert issued == 2 * 6
+
+
+def test_runs_cover_the_columns_of_the_largest_matrices(driver):
+    # the last columns of a matrix of nearly 2^31 rows, and small ones
+    shapes = [(n, tn, most) for tn, _, _ in TILES for most in (1, 2, 8)
+              for n in (1, tn, tn + 1, 7 * tn + 5, 2 ** 31 - 16, 2 ** 31 - 17, 2 ** 31 - 128,
+                        2 ** 31 - 300)]
+    for (n, tn, most), got in zip(shapes, driver([f"run {n} {tn} {most}" for n, tn, most in
+                                                  shapes])):
+        tiles = -(-n // tn)
+        runs = -(-tiles // most)
+        assert got == [runs, tiles, min(most, tiles), tiles - (runs - 1) * most], (n, tn, most)
