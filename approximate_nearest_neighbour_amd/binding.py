@@ -528,8 +528,8 @@ def ivfpq_mx4_list_product_ex(a, b, offsets: torch.Tensor, order: torch.Tensor =
     """Rows sorted by list times their list's matrix: b = (codes [nlist, n,
     16 kb], scales [nlist, n, kb]), offsets [nlist + 1] int32.  With order
     ([rows] int32, of ivfpq_route_sort_ex) output row p takes row order[p] // k
-    of a, without it row p.  Returns [rows, n] of dtype, zero past
-    offsets[nlist]."""
+    of a, without it row p.  Returns [rows, n] of dtype, zero before offsets[0]
+    and past offsets[nlist]."""
     kind = _row_type(dtype)
     (ac, as_, (arows, kb)), (bc, bs, (nlist, n, kb_b)) = _mx4(a, 2), _mx4(b, 3)
     offsets = _dev(offsets, torch.int32)

@@ -167,13 +167,14 @@ hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, in
 // ---------------------------------------------------------------------------
 
 // The rows of A that tile number t of a list product covers: output rows
-// [p0, p1) of one list e (e = nlist: rows past the last list, which are zero).
+// [p0, p1) of one list e (e = nlist: rows of no list, which are zero).
 struct ListTile {
     int e;
     int64_t p0, p1;
 };
 
-// Tiles of TM rows, list after list, the rows past offsets[nlist] last.  Every
+// Tiles of TM rows, list after list, then the rows before offsets[0] and those
+// past offsets[nlist].  Every
 // wave finds its tile by itself: 64 lists at a time, a lane each, their tile
 // counts summed across the lanes.  Offsets outside [0, rows] are clamped.
 template <int TM>
@@ -204,8 +205,14 @@ __device__ __forceinline__ ListTile find_tile(const int32_t *offsets, int nlist,
         }
         base += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
     }
+    const int64_t begin = min(max((int64_t)offsets[0], (int64_t)0), last);
     const int64_t end = min(max((int64_t)offsets[nlist], (int64_t)0), last);
-    const int64_t p0 = end + (int64_t)(t - base) * TM;
+    const uint32_t before = (uint32_t)((begin + TM - 1) / TM);
+    if (t - base < before) {
+        const int64_t p0 = (int64_t)(t - base) * TM;
+        return {nlist, p0, min(p0 + TM, begin)};
+    }
+    const int64_t p0 = end + (int64_t)(t - base - before) * TM;
     return {nlist, p0, min(p0 + TM, last)};
 }
 
@@ -907,10 +914,9 @@ static hipError_t tiles_as(const Mx4Product &p, hipStream_t stream)
     constexpr int64_t TM = 32 * WM * MW, TN = 32 * WN * NW;
     const int64_t nt = (p.n + TN - 1) / TN;
     int64_t mt = (p.m + TM - 1) / TM, likely = mt;
-    if (LIST) { // every list may end inside a tile, and so may the last rows; half may be
-        const int64_t ends = p.m < (int64_t)p.nlist + 1 ? p.m : (int64_t)p.nlist + 1;
-        mt = p.m / TM + ends;
-        likely = p.m / TM + ends / 2 + 1;
+    if (LIST) { // half of the lists that may end inside a tile
+        mt = most_list_tiles(p.m, p.nlist, TM);
+        likely = p.m / TM + (mt - p.m / TM) / 2 + 1;
     }
     const int run = ONE || KG > 1 ? 1
                                   : run_length<LIST>(likely, nt, (p.kb + 7) / 8,
@@ -945,9 +951,7 @@ static hipError_t direct_as(const Mx4Product &p, int64_t mt, hipStream_t stream)
 template <typename T, bool LIST>
 static hipError_t product_of(const Mx4Product &p, hipStream_t stream)
 {
-    int64_t mt = (p.m + 15) / 16;
-    if (LIST) // every list may end inside a tile, and so may the last rows
-        mt = p.m / 16 + (p.m < (int64_t)p.nlist + 1 ? p.m : (int64_t)p.nlist + 1);
+    const int64_t mt = LIST ? most_list_tiles(p.m, p.nlist, 16) : (p.m + 15) / 16;
     const int64_t waves = mt * (((int64_t)p.n + 15) / 16);
     const int64_t brows = (LIST ? (int64_t)p.nlist : 1) * p.n;
     // what the tiles' 32-bit offsets and 16-byte reads of exponent bytes take

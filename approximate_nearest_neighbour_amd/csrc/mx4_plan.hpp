@@ -48,4 +48,12 @@ __host__ __device__ inline int run_tiles(int n, int n0, int tn, int most)
     return left < most ? left : most;
 }
 
+// Most tiles of `tm` rows that m rows sorted by list can make: every list may end
+// inside a tile, and so may the rows before the first list and past the last one.
+inline int64_t most_list_tiles(int64_t m, int nlist, int64_t tm)
+{
+    const int64_t parts = (int64_t)nlist + 2;
+    return m / tm + (m < parts ? m : parts);
+}
+
 } // namespace ivfpq

@@ -449,10 +449,11 @@ ivfpq_status ivfpq_mx4_product_ex(const uint8_t *a_codes_dev, const uint8_t *a_s
  * lists' first rows (ascending, as ivfpq_route_sort_ex writes them; read on
  * the device).  Output row p of list e (offsets[e] <= p < offsets[e + 1]) is
  * row order[p] / k of A times matrix e, or row p of A when order_dev is NULL
- * (then arows >= rows).  Rows from offsets[nlist] to `rows` are zero.  out_dev
- * [rows][n] of `type`.  An entry of order outside A reads row 0.  Errors as
- * above, and IVFPQ_E_INVALID_ARG for nlist outside [1, 2^16], k < 1 or (rows +
- * 1) (n / 16 + 1) > 2^30. */
+ * (then arows >= rows).  Rows before offsets[0] and from offsets[nlist] to
+ * `rows` are zero: consecutive lists of a larger sort are passed as their part of
+ * its offsets and their matrices.  out_dev [rows][n] of `type`.  An entry of
+ * order outside A reads row 0.  Errors as above, and IVFPQ_E_INVALID_ARG for
+ * nlist outside [1, 2^16], k < 1 or (rows + 1) (n / 16 + 1) > 2^30. */
 ivfpq_status ivfpq_mx4_list_product_ex(const uint8_t *a_codes_dev, const uint8_t *a_scales_dev,
                                        int64_t arows, const uint8_t *b_codes_dev,
                                        const uint8_t *b_scales_dev, int nlist, int64_t n, int d,

@@ -9,6 +9,8 @@
 //   run n tn most
 //       the runs of tiles that start along n columns:
 //       "run <runs> <tiles in all> <tiles of the first run> <of the last run>"
+//   tiles m nlist tm
+//       "tiles <most tiles of m rows sorted by list>"
 #include "mx4_plan.hpp"
 
 #include <cstdio>
@@ -80,6 +82,11 @@ int main()
                 if (std::scanf("%lld", &v[i]) != 1)
                     return 1;
             runs((int)v[0], (int)v[1], (int)v[2]);
+        } else if (!std::strcmp(what, "tiles")) {
+            for (int i = 0; i < 3; ++i)
+                if (std::scanf("%lld", &v[i]) != 1)
+                    return 1;
+            std::printf("tiles %lld\n", (long long)most_list_tiles(v[0], (int)v[1], v[2]));
         } else {
             return 1;
         }

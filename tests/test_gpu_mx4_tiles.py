@@ -55,3 +55,34 @@ def test_shared_chunks_with_one_row_in_the_last_tiles(m, n, d, dtype):
     a, b = operands(rng, m, n, d, dtype)
     out = A.ivfpq_mx4_product_ex(cuda(a), cuda(b), dtype=dtype)
     check_rows(out, a, b, d, dtype, np.arange(m))
+
+
+# part of the lists, as where lists are split over devices: the rows of the lists
+# before and after are zero, whatever the output held; direct kernel, middle, large
+# and small tiles, tiles with shared chunks
+@pytest.mark.parametrize("t,nlist,n,d,e0,e1", [
+    (9, 16, 100, 96, 5, 9), (300, 8, 70, 64, 3, 8), (700, 6, 1300, 544, 2, 5),
+    (2600, 5, 1100, 512, 1, 2), (200, 5, 330, 2300, 2, 4), (50, 6, 40, 64, 3, 3)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_before_the_first_list_are_zero(t, nlist, n, d, e0, e1, dtype):
+    rng = np.random.default_rng(t + nlist + n + e0)
+    offsets, order, _ = R.route_sort(make_lists(rng, t, 2, nlist, 0.05), nlist)
+    a, b = operands(rng, t, n, d, dtype, nlist)
+    ac, bc, o = cuda(a), cuda(b), torch.from_numpy(order).cuda()
+    off = torch.from_numpy(offsets).cuda()
+    whole = A.ivfpq_mx4_list_product_ex(ac, bc, off, order=o, k=2, dtype=dtype)
+    e1 = max(e1, e0 + 1)
+    part = torch.full((2 * t, n), float("nan"), device="cuda", dtype=dtype)
+    A.ivfpq_mx4_list_product_ex(ac, tuple(x[e0:e1].contiguous() for x in bc),
+                                off[e0:e1 + 1].clone(), order=o, k=2, dtype=dtype, out=part)
+    lo, hi = int(offsets[e0]), int(offsets[e1])
+    assert 0 < lo < hi < 2 * t
+    assert (part[:lo] == 0).all() and (part[hi:] == 0).all()
+    # another kernel may take the part, so compare with the definition
+    va, vb = R.values(*a, d), R.values(*b, d)
+    for e in range(e0, e1):
+        rows = np.arange(offsets[e], offsets[e + 1])[::7]
+        x = va[order[rows] // 2]
+        check_product(part[torch.from_numpy(rows).cuda()], x @ vb[e].T,
+                      np.abs(x) @ np.abs(vb[e]).T, d, dtype)
+    assert torch.isfinite(whole.float()).all()

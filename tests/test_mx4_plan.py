@@ -2,6 +2,7 @@
 device kernels call (csrc/mx4_plan.hpp), compiled for the host and run by
 tests/mx4_driver.cpp."""
 import os
+import random
 import subprocess
 
 import pytest
@@ -65,3 +66,20 @@ def test_runs_cover_the_columns_of_the_largest_matrices(driver):
         tiles = -(-n // tn)
         runs = -(-tiles // most)
         assert got == [runs, tiles, min(most, tiles), tiles - (runs - 1) * most], (n, tn, most)
+
+
+def test_the_grid_covers_the_tiles_of_any_lists(driver):
+    # rows before the first list, of each list and past the last one: a tile for
+    # each that begins; the largest number is reached
+    rng = random.Random(1)
+    cases, want, reached = [], [], 0
+    for _ in range(400):
+        m, nlist, tm = rng.choice([1, 2, 5, 17, 100, 513]), rng.randint(1, 9), rng.choice([16, 64])
+        cuts = sorted(rng.randint(0, m) for _ in range(nlist + 1))
+        parts = [b - a for a, b in zip([0] + cuts, cuts + [m])]
+        cases.append(f"tiles {m} {nlist} {tm}")
+        want.append(sum(-(-p // tm) for p in parts))
+    for case, tiles, (most,) in zip(cases, want, driver(cases)):
+        assert tiles <= most, case
+        reached += tiles == most
+    assert reached > 0
