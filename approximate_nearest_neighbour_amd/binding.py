@@ -307,6 +307,19 @@ def _raw_stream(stream) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory that a call on `stream` (None: the current one) writes.  For a given
+    stream it comes from that stream's pool, as what was freed on the current one
+    may still be in use there; and as the caller goes on with the result on the
+    current stream, it is not given out again before that stream is past its end."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def ivfpq_search_ex(index: Index, queries: torch.Tensor, nprobe: int, k: int, lut: str = "f32",
                     mode: int = MODE_NORMAL, chunk_len: int = 0, return_probes: bool = False,
                     out=None, stream=None, metric: str = "l2", noalloc: bool = False):
@@ -431,6 +444,9 @@ def ivfpq_profile_end(index: Index) -> dict:
 
 # ---------------------------------------------------------------------------
 # 4-bit rows, their products, and vectors sorted by list
+#
+# All run on the current stream or the given one, which the caller orders after
+# what writes the inputs; what is allocated here is that stream's.
 # ---------------------------------------------------------------------------
 
 TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -457,9 +473,9 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _out(out, shape, dtype, device) -> torch.Tensor:
+def _out(out, shape, dtype, device, stream) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype, device, stream)
     if out.shape != shape:
         raise ValueError(f"expected an output of shape {shape}")
     return _dev(out, dtype)
@@ -489,8 +505,8 @@ def ivfpq_mx4_quantize_ex(x: torch.Tensor, out=None, stream=None):
     n, d = shape
     kb = (d + 31) // 32
     codes, scales = (None, None) if out is None else out
-    codes = _out(codes, (n, 16 * kb), torch.uint8, x.device)
-    scales = _out(scales, (n, kb), torch.uint8, x.device)
+    codes = _out(codes, (n, 16 * kb), torch.uint8, x.device, stream)
+    scales = _out(scales, (n, kb), torch.uint8, x.device, stream)
     _check(lib().ivfpq_mx4_quantize_ex(x.data_ptr(), kind, n, d, strides[0], codes.data_ptr(),
                                        scales.data_ptr(), _raw_stream(stream)))
     return codes, scales
@@ -503,7 +519,7 @@ def ivfpq_mx4_dequantize_ex(codes: torch.Tensor, scales: torch.Tensor, d: int,
     codes, scales, (n, kb) = _mx4((codes, scales), 2)
     if d < 1 or (d + 31) // 32 != kb:
         raise ValueError("d does not fit the rows' blocks")
-    out = _out(out, (n, d), dtype, codes.device)
+    out = _out(out, (n, d), dtype, codes.device, stream)
     _check(lib().ivfpq_mx4_dequantize_ex(codes.data_ptr(), scales.data_ptr(), n, d, kind,
                                          out.data_ptr(), _raw_stream(stream)))
     return out
@@ -516,7 +532,7 @@ def ivfpq_mx4_product_ex(a, b, dtype=torch.float32, out=None, stream=None) -> to
     (ac, as_, (m, kb)), (bc, bs, (n, kb_b)) = _mx4(a, 2), _mx4(b, 2)
     if kb != kb_b:
         raise ValueError("the operands' rows have different lengths")
-    out = _out(out, (m, n), dtype, ac.device)
+    out = _out(out, (m, n), dtype, ac.device, stream)
     _check(lib().ivfpq_mx4_product_ex(ac.data_ptr(), as_.data_ptr(), m, bc.data_ptr(),
                                       bs.data_ptr(), n, 32 * kb, kind, out.data_ptr(),
                                       _raw_stream(stream)))
@@ -543,7 +559,7 @@ def ivfpq_mx4_list_product_ex(a, b, offsets: torch.Tensor, order: torch.Tensor =
         if len(shape) != 1:
             raise ValueError("expected order [rows]")
         rows = shape[0]
-    out = _out(out, (rows, n), dtype, ac.device)
+    out = _out(out, (rows, n), dtype, ac.device, stream)
     _check(lib().ivfpq_mx4_list_product_ex(ac.data_ptr(), as_.data_ptr(), arows, bc.data_ptr(),
                                            bs.data_ptr(), nlist, n, 32 * kb, offsets.data_ptr(),
                                            _ptr(order), k, rows, kind, out.data_ptr(),
@@ -566,16 +582,14 @@ def ivfpq_route_sort_ex(lists: torch.Tensor, nlist: int, out=None, workspace=Non
     nvec, k = shape
     offsets, order, pos = (None, None, None) if out is None else out
     device = lists.device
-    offsets = _out(offsets, (nlist + 1,), torch.int32, device)
-    order = _out(order, (nvec * k,), torch.int32, device)
-    pos = _out(pos, shape, torch.int32, device)
+    offsets = _out(offsets, (nlist + 1,), torch.int32, device, stream)
+    order = _out(order, (nvec * k,), torch.int32, device, stream)
+    pos = _out(pos, shape, torch.int32, device, stream)
     need = ivfpq_route_sort_bytes(nvec, k, nlist)
     if workspace is not None:
         _dev(workspace, torch.uint8)
     elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _empty((need,), torch.uint8, device, stream)
     _check(lib().ivfpq_route_sort_ex(lists.data_ptr(), nvec, k, nlist, _ptr(workspace),
                                      0 if workspace is None else workspace.numel(),
                                      offsets.data_ptr(), order.data_ptr(), pos.data_ptr(),
@@ -608,7 +622,7 @@ def ivfpq_route_gather_ex(x: torch.Tensor, order: torch.Tensor, k: int,
     if k < 1 or _slots(order, "order") != (nvec * k,):
         raise ValueError("expected order [nvec k], k >= 1")
     w = _slot_weights(weights, nvec, k)
-    out = _out(out, (nvec * k, d), x.dtype, x.device)
+    out = _out(out, (nvec * k, d), x.dtype, x.device, stream)
     _check(lib().ivfpq_route_gather_ex(x.data_ptr(), kind, nvec, d, order.data_ptr(), w, k,
                                        out.data_ptr(), _raw_stream(stream)))
     return out
@@ -628,7 +642,7 @@ def ivfpq_route_combine_ex(rows: torch.Tensor, pos: torch.Tensor, weights: torch
     slots (pos -1) adding nothing: [nvec, d] from rows [nvec k, d]."""
     kind, d, nvec, k = _routed(rows, pos)
     w = _slot_weights(weights, nvec, k)
-    out = _out(out, (nvec, d), rows.dtype, rows.device)
+    out = _out(out, (nvec, d), rows.dtype, rows.device, stream)
     _check(lib().ivfpq_route_combine_ex(rows.data_ptr(), kind, nvec, d, pos.data_ptr(), w, k,
                                         out.data_ptr(), _raw_stream(stream)))
     return out
@@ -647,8 +661,8 @@ def ivfpq_route_combine_grad_ex(grad: torch.Tensor, rows: torch.Tensor, order: t
     if w is None:
         raise ValueError("expected weights [nvec, k]")
     d_rows, d_weights = (None, None) if out is None else out
-    d_rows = _out(d_rows, (nvec * k, d), rows.dtype, rows.device)
-    d_weights = _out(d_weights, (nvec, k), torch.float32, rows.device)
+    d_rows = _out(d_rows, (nvec * k, d), rows.dtype, rows.device, stream)
+    d_weights = _out(d_weights, (nvec, k), torch.float32, rows.device, stream)
     _check(lib().ivfpq_route_combine_grad_ex(grad.data_ptr(), rows.data_ptr(), kind, nvec, d,
                                              order.data_ptr(), pos.data_ptr(), w, k,
                                              d_rows.data_ptr(), d_weights.data_ptr(),
