@@ -334,9 +334,9 @@ def ivfpq_search_ex(index: Index, queries: torch.Tensor, nprobe: int, k: int, lu
     q = _dev(queries, torch.float32)
     nq = q.shape[0]
     if out is None:
-        dist = torch.empty((nq, k), dtype=torch.float32, device=q.device)
-        ids = torch.empty((nq, k), dtype=torch.int64, device=q.device)
-        probes = torch.empty((nq, nprobe), dtype=torch.int32, device=q.device) \
+        dist = _empty((nq, k), torch.float32, q.device, stream)
+        ids = _empty((nq, k), torch.int64, q.device, stream)
+        probes = _empty((nq, nprobe), torch.int32, q.device, stream) \
             if return_probes else None
     else:
         dist, ids, probes = out
@@ -354,8 +354,8 @@ def ivfpq_search_ex(index: Index, queries: torch.Tensor, nprobe: int, k: int, lu
 def ivfpq_coarse_ex(index: Index, queries: torch.Tensor, nprobe: int, stream=None):
     q = _dev(queries, torch.float32)
     nq = q.shape[0]
-    probes = torch.empty((nq, nprobe), dtype=torch.int32, device=q.device)
-    dist = torch.empty((nq, nprobe), dtype=torch.float32, device=q.device)
+    probes = _empty((nq, nprobe), torch.int32, q.device, stream)
+    dist = _empty((nq, nprobe), torch.float32, q.device, stream)
     _check(lib().ivfpq_coarse_ex(index.handle, ctypes.c_void_p(q.data_ptr()), nq, nprobe,
                                  ctypes.c_void_p(probes.data_ptr()),
                                  ctypes.c_void_p(dist.data_ptr()), _stream_ptr(stream)))
@@ -369,8 +369,8 @@ def ivfpq_assign_encode_ex(index: Index, vectors: torch.Tensor, stream=None):
     if x.dim() != 2 or x.shape[1] != index.info["d"]:
         raise ValueError(f"expected vectors of shape [n, {index.info['d']}]")
     n = x.shape[0]
-    lists = torch.empty(n, dtype=torch.int32, device=x.device)
-    codes = torch.empty((n, index.info["m"]), dtype=torch.uint8, device=x.device)
+    lists = _empty((n,), torch.int32, x.device, stream)
+    codes = _empty((n, index.info["m"]), torch.uint8, x.device, stream)
     _check(lib().ivfpq_assign_encode_ex(index.handle, ctypes.c_void_p(x.data_ptr()), n,
                                         ctypes.c_void_p(lists.data_ptr()),
                                         ctypes.c_void_p(codes.data_ptr()), _stream_ptr(stream)))
@@ -386,8 +386,11 @@ def ivfpq_kmeans_ex(vectors: torch.Tensor, centers: torch.Tensor, iters: int, st
     if x.dim() != 2 or c.dim() != 2 or x.shape[1] != c.shape[1]:
         raise ValueError("expected vectors [n, d] and centers [k, d]")
     n, (k, d) = x.shape[0], c.shape
-    assign = torch.full((n,), -1, dtype=torch.int32, device=x.device)
-    counts = torch.zeros(k, dtype=torch.int32, device=x.device)
+    assign = _empty((n,), torch.int32, x.device, stream)
+    counts = _empty((k,), torch.int32, x.device, stream)
+    with torch.cuda.stream(stream):  # None: the current one
+        assign.fill_(-1)
+        counts.zero_()
     _check(lib().ivfpq_kmeans_ex(ctypes.c_void_p(x.data_ptr()), n, d, k, iters,
                                  ctypes.c_void_p(c.data_ptr()), ctypes.c_void_p(assign.data_ptr()),
                                  ctypes.c_void_p(counts.data_ptr()), _stream_ptr(stream)))
@@ -400,7 +403,7 @@ def ivfpq_compute_luts_ex(index: Index, queries: torch.Tensor, probes: torch.Ten
     pr = _dev(probes, torch.int32)
     nq, nprobe = pr.shape
     m = index.info["m"]
-    out = torch.empty((nq, nprobe, m, 256), dtype=torch.float32, device=q.device)
+    out = _empty((nq, nprobe, m, 256), torch.float32, q.device, stream)
     _check(lib().ivfpq_compute_luts_ex(index.handle, ctypes.c_void_p(q.data_ptr()), nq,
                                        ctypes.c_void_p(pr.data_ptr()), nprobe,
                                        LUT_F16 if lut == "f16" else LUT_F32,
@@ -413,8 +416,8 @@ def ivfpq_select_topk_ex(keys: torch.Tensor, k: int, stream=None):
     (values [rows,k] float32, column numbers [rows,k] int32)."""
     x = _dev(keys, torch.float32)
     rows, n = x.shape
-    d = torch.empty((rows, k), dtype=torch.float32, device=x.device)
-    p = torch.empty((rows, k), dtype=torch.int32, device=x.device)
+    d = _empty((rows, k), torch.float32, x.device, stream)
+    p = _empty((rows, k), torch.int32, x.device, stream)
     _check(lib().ivfpq_select_topk_ex(ctypes.c_void_p(x.data_ptr()), rows, n, k,
                                       ctypes.c_void_p(d.data_ptr()), ctypes.c_void_p(p.data_ptr()),
                                       _stream_ptr(stream)))
@@ -726,8 +729,8 @@ def ivfpq_flat_search_bf16_ex(flat: FlatIndex, queries: torch.Tensor, k: int, ou
     q = _bf16_bits(queries)
     nq = q.shape[0]
     if out is None:
-        dist = torch.empty((nq, k), dtype=torch.float32, device=q.device)
-        ids = torch.empty((nq, k), dtype=torch.int64, device=q.device)
+        dist = _empty((nq, k), torch.float32, q.device, stream)
+        ids = _empty((nq, k), torch.int64, q.device, stream)
     else:
         dist, ids = out
     _check(lib().ivfpq_flat_search_bf16_ex(flat.handle, ctypes.c_void_p(q.data_ptr()), nq, k,

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import approximate_nearest_neighbour_amd as A
+from approximate_nearest_neighbour_amd import datagen as G
 from test_gpu_mx4 import cuda, make_lists, random_mx4
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +67,23 @@ def case(name):
                                   "gather", "combine", "combine_grad"])
 def test_rows_and_routing_on_another_stream(name):
     check_beside_busy_stream(*case(name))
+
+
+def test_searches_and_building_on_another_stream():
+    rng = np.random.default_rng(5)
+    ix = A.ivfpq_load_index_host(G.random_index(rng, 64, 32, 8, rng.integers(10, 200, size=64)))
+    q = torch.from_numpy(rng.standard_normal((3000, 32)).astype(np.float32)).cuda()
+    probes, _ = A.ivfpq_coarse_ex(ix, q[:40], 4)
+    flat = A.ivfpq_flat_load_bf16(G.to_bf16_bits(rng.uniform(-1, 1, (2000, 32)).astype(np.float32)))
+    qb = q.to(torch.bfloat16)
+    centers = iter([q[:50].clone(), q[:50].clone()])   # updated in place, a copy for each call
+    for call in (lambda s: A.ivfpq_search_ex(ix, q, 4, 10, return_probes=True, stream=s),
+                 lambda s: A.ivfpq_coarse_ex(ix, q, 4, stream=s),
+                 lambda s: A.ivfpq_assign_encode_ex(ix, q, stream=s),
+                 lambda s: A.ivfpq_kmeans_ex(q, next(centers), 1, stream=s),
+                 lambda s: A.ivfpq_compute_luts_ex(ix, q[:40], probes, stream=s),
+                 lambda s: A.ivfpq_select_topk_ex(q, 5, stream=s),
+                 lambda s: A.ivfpq_flat_search_bf16_ex(flat, qb, 7, stream=s)):
+        check_beside_busy_stream(call)
+    ix.close()
+    flat.close()

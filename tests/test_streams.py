@@ -81,6 +81,30 @@ CALLS = {
 }
 
 
+INDEX = types.SimpleNamespace(handle=1, info={"d": 8, "m": 2})
+SEARCH_CALLS = {
+    "search": (3, lambda s: B.ivfpq_search_ex(INDEX, dev(4, 8), 2, 3, return_probes=True,
+                                              stream=s)),
+    "coarse": (2, lambda s: B.ivfpq_coarse_ex(INDEX, dev(4, 8), 2, stream=s)),
+    "assign_encode": (2, lambda s: B.ivfpq_assign_encode_ex(INDEX, dev(4, 8), stream=s)),
+    "kmeans": (2, lambda s: B.ivfpq_kmeans_ex(dev(9, 8), dev(3, 8), 1, stream=s)),
+    "compute_luts": (1, lambda s: B.ivfpq_compute_luts_ex(INDEX, dev(4, 8), i32(4, 2), stream=s)),
+    "select_topk": (2, lambda s: B.ivfpq_select_topk_ex(dev(4, 8), 2, stream=s)),
+    "flat_search_bf16": (2, lambda s: B.ivfpq_flat_search_bf16_ex(
+        INDEX, dev(4, 8, dtype=torch.int16), 2, stream=s)),
+}
+
+
+@pytest.mark.parametrize("name", SEARCH_CALLS)
+def test_memory_of_a_search_call_on_another_stream_is_that_streams(world, name):
+    count, call = SEARCH_CALLS[name]
+    call(SIDE)
+    assert [stream for _, stream in world.made] == [SIDE] * count
+    assert all(t.__dict__.get("recorded") == [CURRENT] for t, _ in world.made)
+    (called, args), = world.called
+    assert called == f"ivfpq_{name}_ex" and args[-1].value == SIDE.cuda_stream
+
+
 @pytest.mark.parametrize("name", CALLS)
 def test_memory_of_a_call_on_another_stream_is_that_streams(world, name):
     """Memory of the current stream may still be in use there: a kernel on another
