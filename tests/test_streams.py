@@ -1,6 +1,7 @@
 """Where the binding takes memory from when a call is given a stream of its own
 (no GPU needed: tensors, streams and the library are stand-ins)."""
 import contextlib
+import importlib.util
 import types
 
 import pytest
@@ -129,3 +130,16 @@ def test_memory_of_a_call_on_the_current_stream(world, name, monkeypatch):
     assert len(world.made) == count
     assert all(stream is CURRENT and "recorded" not in t.__dict__ for t, stream in world.made)
     assert world.called[0][1][-1] == CURRENT.cuda_stream
+
+
+@pytest.mark.parametrize("missing", ["_cuda_getCurrentRawStream", "_cuda_getDevice"])
+def test_current_stream_without_torchs_private_calls(monkeypatch, missing):
+    monkeypatch.delattr(torch._C, missing)
+    spec = importlib.util.spec_from_file_location("binding_without_private_calls", B.__file__)
+    other = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(other)
+    for handle in (5, 0):
+        monkeypatch.setattr(torch.cuda, "current_stream",
+                            lambda device=None: types.SimpleNamespace(cuda_stream=handle))
+        assert other._raw_stream(None) == handle
+    assert other._raw_stream(SIDE) == SIDE.cuda_stream
