@@ -940,68 +940,23 @@ static hipError_t direct_as(const Mx4Product &p, int64_t mt, hipStream_t stream)
     return launch_blocks(mx4_direct_kernel<T, LIST, KS>, nt * mt, 512, stream, p, (uint32_t)nt);
 }
 
-// Which kernel.  The direct one reads B once for every 16 rows of A, the tiles
-// once for 64 to 256, but they take 10 us and more for their chunks one after
-// the other (d 4096).  So the direct one where a matrix has few rows to
-// multiply, or all is small: 32 rows by 8192, d 4096 (11.5 us, tiles of up to 64
-// rows 11.2 us) is about the limit (48 rows: 15.7 us; 32 rows by 4096, d 8192:
-// 12.5 us, tiles 15.7 us).  In 64 lists, 2048 x 2048, of 4 rows on average 29 us
-// against 28 to 32, of 8 rows 33 to 38 us against 32; in 128 lists, 1024 x 1024,
-// of 4 rows 18 us against 15, of 8 rows 21 to 23 us against 15.
 template <typename T, bool LIST>
 static hipError_t product_of(const Mx4Product &p, hipStream_t stream)
 {
     const int64_t mt = LIST ? most_list_tiles(p.m, p.nlist, 16) : (p.m + 15) / 16;
-    const int64_t waves = mt * (((int64_t)p.n + 15) / 16);
-    const int64_t brows = (LIST ? (int64_t)p.nlist : 1) * p.n;
-    // what the tiles' 32-bit offsets and 16-byte reads of exponent bytes take
-    const bool fits = !(LIST && p.order && p.arows * p.kb * 16 >= (int64_t)1 << 32) &&
-                      brows * p.kb >= 16 && p.arows * p.kb >= 16;
-    const bool few = LIST ? p.m <= 2ll * p.nlist : p.m <= 16 || waves * p.kb <= 1024 * 128;
-    if (few || !fits) {
-        // blocks of a row are split only as far as it takes to have 16 waves a
-        // CU, with 8 KB each under way, or a turn for each
-        if (waves >= 4096 || p.kb <= 16)
-            return direct_as<T, LIST, 1>(p, mt, stream);
-        if (waves >= 1024 || p.kb <= 64)
-            return direct_as<T, LIST, 4>(p, mt, stream);
-        return direct_as<T, LIST, 8>(p, mt, stream);
-    }
-    auto tiles = [&](int64_t high, int64_t wide) {
-        const int64_t parts = LIST ? (p.m < p.nlist ? p.m : p.nlist) / 2 : 0; // lists end inside
-        return ((p.m + high - 1) / high + parts) * ((p.n + wide - 1) / wide);
-    };
-    if constexpr (!LIST) {
-        if (p.kb <= 8)
+    switch (mx4_kernel_of(LIST, p.m, p.n, p.kb, p.nlist, p.arows, p.order != nullptr)) {
+    case kMx4Direct1: return direct_as<T, LIST, 1>(p, mt, stream);
+    case kMx4Direct4: return direct_as<T, LIST, 4>(p, mt, stream);
+    case kMx4Direct8: return direct_as<T, LIST, 8>(p, mt, stream);
+    case kMx4Shared: return tiles_as<T, LIST, 1, 1, 2, 2, 2>(p, stream);
+    case kMx4Small: return tiles_as<T, LIST, 1, 1, 2, 4>(p, stream);
+    case kMx4Middle: return tiles_as<T, LIST, 2, 2, 2, 2>(p, stream);
+    case kMx4Large: return tiles_as<T, LIST, 4, 2, 2, 4>(p, stream);
+    case kMx4One:
+        if constexpr (!LIST)
             return tiles_as<T, false, 1, 1, 2, 4, 1, true>(p, stream);
     }
-    // Few tiles of long rows wait for their chunks one after the other: tiles of
-    // 64 x 64, their chunks shared out between two groups of four waves, while
-    // all are under way together (two a CU).  128 x 4096 x 8192 24.4 -> 15.8 us,
-    // 512 x 4096 x 8192, which is 512 of them, 29.9 -> 24.7, x 4096 16.6 -> 15.0,
-    // x 2048 10.5 -> 11.0; 768 x 4096 x 8192 29.1 -> 36.5.  16 lists of 32 rows, 512
-    // x 4096: 15.9 -> 13.5 us.
-    if (p.kb > 64 && tiles(64, 64) <= 512)
-        return tiles_as<T, LIST, 1, 1, 2, 2, 2>(p, stream);
-    // Large tiles (256 x 256) take about three times as long as middle ones (128 x
-    // 128) a round of 256: 3000 x 4000 x 4096 35.0 us against 41.2 us, 2048 x 4096 x
-    // 4096, which is half a round of them, 32.7 us against 26.3 us.
-    // Lists have to fill them: 64 lists, 2048 x 2048, of 512 rows on average 135 us
-    // against 147 us, of 256 87 us against 86 us, of 128 71 us against 61 us.
-    // Small ones (64 x 128) where few tiles wait for their chunks more than for
-    // the matrix cores: 1024 x 2048 x 2048 9.4 us against 9.9 us, 2048 x 2048 x
-    // 4096, which is 512 of them, 29.3 us against 18.4 us.  And where lists would
-    // leave middle ones empty: 32 rows on average 40 us against 42 us, 64 rows 51
-    // us against 52 us (64 rows each 46 us against 38 us).
-    const bool large = (!LIST || p.m > 256ll * p.nlist) &&
-                       3 * ((tiles(256, 256) + 255) / 256) <= (tiles(128, 128) + 255) / 256;
-    const bool small = tiles(64, 128) <= (p.kb <= 32 ? 512 : 256) ||
-                       (LIST && p.m <= 32ll * p.nlist);
-    if (large)
-        return tiles_as<T, LIST, 4, 2, 2, 4>(p, stream);
-    if (small)
-        return tiles_as<T, LIST, 1, 1, 2, 4>(p, stream);
-    return tiles_as<T, LIST, 2, 2, 2, 2>(p, stream);
+    return hipErrorInvalidValue;
 }
 
 template <typename T>

@@ -11,6 +11,8 @@
 //       "run <runs> <tiles in all> <tiles of the first run> <of the last run>"
 //   tiles m nlist tm
 //       "tiles <most tiles of m rows sorted by list>"
+//   kernel list m n kb nlist arows order
+//       "kernel <number of the kernel that a product takes>"
 #include "mx4_plan.hpp"
 
 #include <cstdio>
@@ -87,6 +89,12 @@ int main()
                 if (std::scanf("%lld", &v[i]) != 1)
                     return 1;
             std::printf("tiles %lld\n", (long long)most_list_tiles(v[0], (int)v[1], v[2]));
+        } else if (!std::strcmp(what, "kernel")) {
+            for (int i = 0; i < 7; ++i)
+                if (std::scanf("%lld", &v[i]) != 1)
+                    return 1;
+            std::printf("kernel %d\n", (int)mx4_kernel_of(v[0], v[1], (int)v[2], (int)v[3],
+                                                          (int)v[4], v[5], v[6]));
         } else {
             return 1;
         }

@@ -7,6 +7,8 @@ import subprocess
 
 import pytest
 
+from test_gpu_mx4_tiles import LIST_PARTS, LIST_PRODUCTS, PRODUCTS
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "approximate_nearest_neighbour_amd", "csrc")
 
@@ -83,3 +85,37 @@ def test_the_grid_covers_the_tiles_of_any_lists(driver):
         assert tiles <= most, case
         reached += tiles == most
     assert reached > 0
+
+
+KERNELS = ["direct1", "direct4", "direct8", "one", "shared", "small", "middle", "large"]
+
+
+def kernels(driver, shapes):
+    """Of products (m, n, d) and products per list (t, k, nlist, n, d)."""
+    lines = []
+    for s in shapes:
+        if len(s) == 3:
+            m, n, d = s
+            lines.append(f"kernel 0 {m} {n} {-(-d // 32)} 0 {m} 0")
+        else:
+            t, k, nlist, n, d = s
+            lines.append(f"kernel 1 {t * k} {n} {-(-d // 32)} {nlist} {t} 1")
+    return [KERNELS[number] for number, in driver(lines)]
+
+
+def test_the_gpu_tests_reach_the_kernels_that_they_name(driver):
+    for cases in (PRODUCTS, LIST_PRODUCTS):
+        named = [c[0] for c in cases]
+        assert kernels(driver, [c[1:] for c in cases]) == named
+    assert {c[0] for c in PRODUCTS} == set(KERNELS)
+    assert {c[0] for c in LIST_PRODUCTS} == set(KERNELS) - {"one"}
+    assert [kernels(driver, [(t, 2, e1 - e0, n, d)])[0] for _, t, _, n, d, e0, e1 in LIST_PARTS] \
+        == [c[0] for c in LIST_PARTS]
+    # what the tests of many lists, of graphs and of rows past 4 GiB name
+    assert kernels(driver, [(3000, 2, 1000, 20, 64), (3500, 2, 3000, 20, 64),
+                            (3000, 2, 1 << 16, 20, 64), (1650, 2, 3, 4200, 512),
+                            (140, 3000, 2592), (1301, 8703, 96)]) == \
+        ["small", "small", "direct1", "large", "shared", "one"]
+    rows = (1 << 20) + 5
+    assert driver([f"kernel 1 600 70 256 2 {rows} 1", "kernel 1 600 70 256 2 600 1"]) == \
+        [[KERNELS.index("direct8")], [KERNELS.index("shared")]]
