@@ -427,8 +427,10 @@ ivfpq_status ivfpq_mx4_quantize_ex(const void *rows_dev, int type, int64_t rows,
                                    int64_t stride, uint8_t *codes_dev, uint8_t *scales_dev,
                                    void *stream);
 
-/* 4-bit rows back to values: out_dev [rows][d] of `type`, rounded to it once
- * (float32 and bfloat16 hold every value exactly).  Errors as above. */
+/* 4-bit rows back to values: out_dev [rows][d] of `type`, rounded to it once.
+ * float32 and bfloat16 hold every value below 2^128 exactly, so all that
+ * ivfpq_mx4_quantize_ex makes; larger ones, which exponent bytes 253 and 254 can
+ * stand for, become infinities.  Errors as above. */
 ivfpq_status ivfpq_mx4_dequantize_ex(const uint8_t *codes_dev, const uint8_t *scales_dev,
                                      int64_t rows, int d, int type, void *out_dev, void *stream);
 
