@@ -624,8 +624,9 @@ def _slot_weights(weights, nvec: int, k: int):
 def ivfpq_route_gather_ex(x: torch.Tensor, order: torch.Tensor, k: int,
                           weights: torch.Tensor = None, out=None, stream=None) -> torch.Tensor:
     """Row p = x[order[p] // k] (times weights[order[p]]), zero where order is -1:
-    [nvec k, d] from x [nvec, d].  Its gradient with respect to x is
-    ivfpq_route_combine_ex of the rows' gradient."""
+    [nvec k, d] from x [nvec, d].  For the rows' gradient g, the gradient of x is
+    ivfpq_route_combine_ex(g, pos, weights), that of the weights the second result
+    of ivfpq_route_combine_grad_ex(x, g, order, pos, weights)."""
     kind, (nvec, d) = _rows(x)
     if k < 1 or _slots(order, "order") != (nvec * k,):
         raise ValueError("expected order [nvec k], k >= 1")

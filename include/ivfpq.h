@@ -487,10 +487,12 @@ ivfpq_status ivfpq_route_sort_ex(const int32_t *lists_dev, int64_t nvec, int k, 
 
 /* rows_dev [n][d]: row p is vector order[p] / k, times weights[order[p]]
  * (float32 [nvec][k], rounded once) when weights_dev is not NULL; a row whose
- * order is outside [0, n) is zero.  Its gradient is ivfpq_route_combine_ex of
- * the rows' gradient (with the same weights).  Errors: IVFPQ_E_INVALID_ARG
- * (a bad type, d outside [1, 2^20], k < 1, n >= 2^31, a NULL or misaligned
- * pointer), IVFPQ_E_DEVICE. */
+ * order is outside [0, n) is zero.  Its gradients: of the vectors,
+ * ivfpq_route_combine_ex of the rows' gradient with the same weights; of the
+ * weights, the grad_weights of ivfpq_route_combine_grad_ex with the vectors in the
+ * place of grad and the rows' gradient in the place of rows.  Errors:
+ * IVFPQ_E_INVALID_ARG (a bad type, d outside [1, 2^20], k < 1, n >= 2^31, a NULL
+ * or misaligned pointer), IVFPQ_E_DEVICE. */
 ivfpq_status ivfpq_route_gather_ex(const void *vectors_dev, int type, int64_t nvec, int d,
                                    const int32_t *order_dev, const float *weights_dev, int k,
                                    void *rows_dev, void *stream);
