@@ -174,9 +174,11 @@ struct ListTile {
 };
 
 // Tiles of TM rows, list after list, then the rows before offsets[0] and those
-// past offsets[nlist].  Every
-// wave finds its tile by itself: 64 lists at a time, a lane each, their tile
-// counts summed across the lanes.  Offsets outside [0, rows] are clamped.
+// past offsets[nlist].  Every wave finds its tile by itself: 64 lists at a time, a
+// lane each, their tile counts summed across the lanes.  Offsets outside [0, rows]
+// are clamped.  The walk grows with the lists and so does the number of waves, so
+// this is made for some hundred lists: 16,384 rows, 256 x 256, of 128 lists 10 us,
+// of 1024 lists 38 us, of 8192 lists 1.4 ms, of 65,536 lists 18 ms.
 template <int TM>
 __device__ __forceinline__ ListTile find_tile(const int32_t *offsets, int nlist, int64_t rows,
                                               uint32_t t)
@@ -239,8 +241,8 @@ __device__ __forceinline__ f32x4 mfma_mx4(i32x4 a, uint32_t sa, i32x4 b, uint32_
 // operands are under way while this one's are multiplied.  The exponent bytes
 // of a turn are one 16-byte load, of which word s, byte g is the lane's.  Sums
 // are float32, rounded once to the output's type.  One row by 8192 x 4096: 5.8
-// us for 17.8 MB, of which the launch is about half; 4 rows of 8 lists each, 30
-// of 64 matrices of 2048 x 2048: 14 us for 71 MB, 5 TB/s.
+// us for 17.8 MB, of which the launch is about half; 4 rows of 8 lists each, 25
+// of 64 matrices of 2048 x 2048: 14 us for 56 MB, 4 TB/s (a streaming read: 6.45).
 template <typename T, bool LIST, int KS>
 __global__ __launch_bounds__(512) void mx4_direct_kernel(Mx4Product p, uint32_t ntiles)
 {
@@ -375,7 +377,11 @@ __global__ __launch_bounds__(512) void mx4_direct_kernel(Mx4Product p, uint32_t 
 // alone, from registers, 6.45 PF: the clock falls to 1.3-1.6 GHz; here 1.8 GHz
 // with the matrix cores busy 53 % of the cycles).  Without the copies of operands
 // it would be 208 us, without the stores 249; operands that all come from the
-// XCD's cache change nothing.  128 lists of 512 rows on average, 2048 x 2048: 240
+// XCD's cache change nothing.  A chunk takes about 3900 cycles, 2048 of them for
+// its products; 64 KB of it are copied into LDS and the waves read 192 KB, 2048
+// cycles as well at 128 bytes a cycle (the counter of LDS reads is active in 24 %
+// of the cycles).  The 16-bit kernels keep 3 (lists: 6) registers of a tile's
+// stores in scratch memory.  128 lists of 512 rows on average, 2048 x 2048: 240
 // us, of which the stores are 65 (268 MB), the matrices from memory 20, rows that
 // only fill tiles up 28.  128 x 128 tiles for both: 365 and 289 us.
 //
@@ -874,7 +880,9 @@ __global__ __launch_bounds__(64 * MW * NW * KG) void mx4_tile_kernel(Mx4Product 
 
 // Tiles of a run: of 1, 2, 4 and 8 the one that ends first when `slots`
 // workgroups are under way together, a tile taking its chunks and one more, a
-// run about three chunks besides (first copies, last stores).  Tiles of lists
+// run about three chunks besides (first copies, last stores).  The callers' slots
+// are those of the large and the middle tiles, one and two workgroups a CU; of the
+// small ones two or three fit a CU, but they are counted as one.  Tiles of lists
 // are of different cost and end at different times: half a run at the end, not
 // a whole last round (128 lists of 512 rows, 2048 x 2048: runs of 1, 2, 4 and 8
 // 251, 235, 249 and 312 us).
