@@ -412,7 +412,8 @@ ivfpq_status ivfpq_flat_profile_end(ivfpq_flat *f, ivfpq_flat_timings *out);
  * sign) and one exponent byte s, and stands for code * 2^(s - 127).  A matrix
  * of such rows is two arrays: codes [rows][16 kb], 16-byte aligned, and scales
  * [rows][kb].  s = 255 makes the whole block NaN; unlike the searches, these
- * calls take infinities and NaN, as described at each. */
+ * calls take infinities and NaN, as described at each.  They run on the current
+ * device, whose memory all pointers name; an output overlaps no input. */
 typedef enum { IVFPQ_F32 = 0, IVFPQ_BF16 = 1, IVFPQ_F16 = 2 } ivfpq_type;
 
 /* Rows to 4 bits (device buffers, asynchronous on `stream`): rows_dev holds
@@ -466,8 +467,9 @@ ivfpq_status ivfpq_mx4_list_product_ex(const uint8_t *a_codes_dev, const uint8_t
  *
  * nvec vectors with k lists each (the probes of ivfpq_coarse_ex, or a router's
  * choices): slot u = t k + j is list j of vector t, n = nvec k < 2^31 slots.
- * All calls are asynchronous on `stream`, allocate nothing and may be captured
- * in a graph.  Rows are row-major and contiguous. */
+ * All calls are asynchronous on `stream` of the current device, allocate nothing
+ * and may be captured in a graph.  Rows are row-major and contiguous; an output
+ * overlaps no input. */
 
 /* Bytes of device workspace for ivfpq_route_sort_ex: 0 for small sorts, which
  * need none, and for arguments that it rejects. */

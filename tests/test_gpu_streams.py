@@ -87,3 +87,34 @@ def test_searches_and_building_on_another_stream():
         check_beside_busy_stream(call)
     ix.close()
     flat.close()
+
+
+def test_given_stream_while_it_is_captured():
+    lists = torch.empty((6000, 2), dtype=torch.int32, device="cuda")
+    x = torch.empty((6000, 96), device="cuda")
+    side = torch.cuda.Stream()
+
+    def step(stream):
+        offsets, order, pos = A.ivfpq_route_sort_ex(lists, 40, stream=stream)
+        rows = A.ivfpq_route_gather_ex(x, order, 2, stream=stream)
+        return offsets, order, pos, A.ivfpq_route_combine_ex(rows, pos, stream=stream)
+
+    def fill(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        lists.copy_(torch.randint(-1, 40, lists.shape, generator=g, device="cuda"))
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+
+    fill(0)
+    step(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        held = step(side)
+    for seed in range(1, 5):
+        fill(seed)
+        want = step(None)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, w in zip(held, want):
+            assert torch.equal(got, w), seed
