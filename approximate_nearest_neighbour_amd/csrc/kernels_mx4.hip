@@ -7,9 +7,9 @@
 // the low nibble.  The format is that of the OCP Microscaling specification
 // (MXFP4), which the matrix cores of gfx950 multiply directly.
 #include "common.hpp"
-#include "internal.hpp"
 #include "mx4_plan.hpp"
 #include "rows.hpp"
+#include "rows_internal.hpp"
 
 namespace ivfpq {
 

@@ -6,8 +6,8 @@
 // position p; order[p] is the slot at p (-1 past the kept ones) and pos[u] the
 // position of slot u (-1 for a slot without a list).
 #include "common.hpp"
-#include "internal.hpp"
 #include "rows.hpp"
+#include "rows_internal.hpp"
 
 namespace ivfpq {
 
