@@ -76,7 +76,10 @@ EXPORTS = ("ivfpq_validate_index_file", "ivfpq_validate_host_index", "ivfpq_load
            "ivfpq_flat_profile_end", "ivfpq_mx4_quantize_ex", "ivfpq_mx4_dequantize_ex",
            "ivfpq_mx4_product_ex", "ivfpq_mx4_list_product_ex", "ivfpq_route_sort_bytes",
            "ivfpq_route_sort_ex", "ivfpq_route_gather_ex", "ivfpq_route_combine_ex",
-           "ivfpq_route_combine_grad_ex", "ivfpq_stream_read", "ivfpq_last_error",
+           "ivfpq_route_combine_grad_ex", "ivfpq_list_product_ex",
+           "ivfpq_list_product_grad_bytes", "ivfpq_list_product_grad_ex",
+           "ivfpq_adapter_product_bytes", "ivfpq_adapter_product_ex", "ivfpq_table_lookup_ex",
+           "ivfpq_table_grad_bytes", "ivfpq_table_grad_ex", "ivfpq_stream_read", "ivfpq_last_error",
            "ivfpq_status_string")
 
 _lib = None
@@ -127,6 +130,18 @@ def lib():
             "ivfpq_route_gather_ex": ([P, i32, i64, i32, P, P, i32, P, P], st),
             "ivfpq_route_combine_ex": ([P, i32, i64, i32, P, P, i32, P, P], st),
             "ivfpq_route_combine_grad_ex": ([P, P, i32, i64, i32, P, P, P, i32, P, P, P], st),
+            "ivfpq_list_product_ex": ([P, i32, i64, i32, P, i32, i32, i32, P, P, i32, i64, P, P],
+                                      st),
+            "ivfpq_list_product_grad_bytes": ([i64, i32, i32, i32], ctypes.c_size_t),
+            "ivfpq_list_product_grad_ex": ([P, P, i32, i64, i32, i32, i32, P, P, i32, i64, i32, P,
+                                            ctypes.c_size_t, P, P], st),
+            "ivfpq_adapter_product_bytes": ([i64, i32], ctypes.c_size_t),
+            "ivfpq_adapter_product_ex": ([P, i32, i64, i32, P, i32, P, P, i32, i32, P, P, P, P, P,
+                                          ctypes.c_size_t, P, P], st),
+            "ivfpq_table_lookup_ex": ([P, i32, i64, i32, P, i64, ctypes.c_float, P, P], st),
+            "ivfpq_table_grad_bytes": ([i64, i32, i32], ctypes.c_size_t),
+            "ivfpq_table_grad_ex": ([P, i32, i64, i32, P, P, i32, i32, ctypes.c_float, i32, P,
+                                     ctypes.c_size_t, P, P], st),
             "ivfpq_stream_read": ([P, ctypes.c_size_t, P, i32, P], st),
             "ivfpq_last_error": ([], ctypes.c_char_p),
             "ivfpq_status_string": ([i32], ctypes.c_char_p),
@@ -677,6 +692,171 @@ def ivfpq_route_combine_grad_ex(grad: torch.Tensor, rows: torch.Tensor, order: t
                                              d_rows.data_ptr(), d_weights.data_ptr(),
                                              _raw_stream(stream)))
     return d_rows, d_weights
+
+
+# ---------------------------------------------------------------------------
+# products per list, adapters, table rows
+#
+# Streams as above.  A workspace that a call needs is allocated here unless one is
+# given; calls that may run at the same time, or graphs replayed at the same time,
+# need one each.
+# ---------------------------------------------------------------------------
+
+def _workspace(workspace, need: int, device, stream):
+    """(pointer, bytes) of the given workspace, or of one made here, and its owner."""
+    if workspace is not None:
+        _dev(workspace, torch.uint8)
+    elif need:
+        workspace = _empty((need,), torch.uint8, device, stream)
+    return _ptr(workspace), 0 if workspace is None else workspace.numel(), workspace
+
+
+def _like(t: torch.Tensor, rows: torch.Tensor, what: str):
+    """Shape of a checked operand of the rows' type."""
+    if t.dtype != rows.dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"expected {what} as a contiguous device tensor of the rows' type")
+    return t.shape
+
+
+def _sorted_rows(x: torch.Tensor, offsets: torch.Tensor, order, nlist: int):
+    """Sorted rows: as many as order has, or as x has without one."""
+    if _slots(offsets, "offsets") != (nlist + 1,):
+        raise ValueError("expected offsets [nlist + 1]")
+    if order is None:
+        return x.shape[0]
+    shape = _slots(order, "order")
+    if len(shape) != 1:
+        raise ValueError("expected order [rows]")
+    return shape[0]
+
+
+def ivfpq_list_product_ex(x: torch.Tensor, matrices: torch.Tensor, offsets: torch.Tensor,
+                          order: torch.Tensor = None, k: int = 1, transposed: bool = False,
+                          out=None, stream=None) -> torch.Tensor:
+    """Rows sorted by list times their list's own matrix: row p of list e is
+    x[order[p] // k] @ matrices[e].T (x[p] without order), with `transposed`
+    x[..] @ matrices[e].  x [arows, d], matrices [nlist, n, d] ([nlist, d, n]) of its
+    type, offsets [nlist + 1] int32, order [rows] int32 of ivfpq_route_sort_ex.
+    Returns [rows, n], zero outside the lists.  The gradient of the sorted rows, for
+    the output's gradient g: ivfpq_list_product_ex(g, matrices, offsets,
+    transposed=not transposed); of the matrices: ivfpq_list_product_grad_ex."""
+    kind, (arows, d) = _rows(x)
+    shape = _like(matrices, x, "matrices")
+    if len(shape) != 3 or shape[0] < 1 or shape[1 if transposed else 2] != d:
+        raise ValueError("expected matrices [nlist, n, d], transposed [nlist, d, n]")
+    nlist, n = shape[0], shape[2 if transposed else 1]
+    rows = _sorted_rows(x, offsets, order, nlist)
+    out = _out(out, (rows, n), x.dtype, x.device, stream)
+    _check(lib().ivfpq_list_product_ex(x.data_ptr(), kind, arows, d, matrices.data_ptr(),
+                                       1 if transposed else 0, nlist, n, offsets.data_ptr(),
+                                       _ptr(order), k, rows, out.data_ptr(), _raw_stream(stream)))
+    return out
+
+
+def ivfpq_list_product_grad_bytes(rows: int, n: int, d: int, nlist: int) -> int:
+    return lib().ivfpq_list_product_grad_bytes(rows, n, d, nlist)
+
+
+def ivfpq_list_product_grad_ex(grad: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                               order: torch.Tensor = None, k: int = 1, dtype=None, out=None,
+                               workspace=None, stream=None) -> torch.Tensor:
+    """The gradient of the matrices of ivfpq_list_product_ex for the output's
+    gradient grad [rows, n]: [nlist, n, d], per list the sum of
+    grad[p, :, None] * x[order[p] // k, None, :] (x[p] without order), zero for
+    an empty list; dtype is x's (the default) or float32.  Transposed matrices, without
+    order: exchange grad and x."""
+    kind, (arows, d) = _rows(x)
+    shape = _like(grad, x, "grad")
+    if len(shape) != 2 or shape[1] < 1 or len(_slots(offsets, "offsets")) != 1:
+        raise ValueError("expected grad [rows, n] and offsets [nlist + 1]")
+    nlist, (rows, n) = offsets.shape[0] - 1, shape
+    if nlist < 1 or _sorted_rows(grad, offsets, order, nlist) != rows or \
+            (order is None and arows < rows):
+        raise ValueError("expected grad [rows, n], order [rows], or x [rows, d] without order")
+    dtype = x.dtype if dtype is None else dtype
+    out_kind = _row_type(dtype)
+    out = _out(out, (nlist, n, d), dtype, x.device, stream)
+    ws, ws_bytes, _keep = _workspace(workspace, ivfpq_list_product_grad_bytes(rows, n, d, nlist),
+                                     x.device, stream)
+    _check(lib().ivfpq_list_product_grad_ex(grad.data_ptr(), x.data_ptr(), kind, arows, d, nlist, n,
+                                            offsets.data_ptr(), _ptr(order), k, rows, out_kind, ws,
+                                            ws_bytes, out.data_ptr(), _raw_stream(stream)))
+    return out
+
+
+def ivfpq_adapter_product_bytes(t: int, r: int) -> int:
+    return lib().ivfpq_adapter_product_bytes(t, r)
+
+
+def ivfpq_adapter_product_ex(x: torch.Tensor, w: torch.Tensor, down: torch.Tensor,
+                             up: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor,
+                             pos: torch.Tensor, scales: torch.Tensor = None, out=None,
+                             workspace=None, stream=None) -> torch.Tensor:
+    """Rows x [t, d] through a shared matrix w [n, d], each with its list's low-rank
+    product (adapter): x[i] @ w.T + scales[a] * (x[i] @ down[a].T) @ up[a].T, a the
+    row's list, w alone for a row whose list is masked.  down [nlist, r, d], up [nlist,
+    n, r], scales [nlist] float32; (offsets, order, pos) of
+    ivfpq_route_sort_ex(lists [t, 1], nlist), made once for all products of the rows."""
+    kind, (t, d) = _rows(x)
+    shape_w, shape_d = _like(w, x, "w"), _like(down, x, "down")
+    if len(shape_w) != 2 or shape_w[0] < 1 or shape_w[1] != d or len(shape_d) != 3 or \
+            shape_d[0] < 1 or shape_d[1] < 1 or shape_d[2] != d:
+        raise ValueError("expected w [n, d] and down [nlist, r, d]")
+    n, (nlist, r, _) = shape_w[0], shape_d
+    if _like(up, x, "up") != (nlist, n, r):
+        raise ValueError("expected up [nlist, n, r]")
+    if scales is not None and _dev(scales, torch.float32).shape != (nlist,):
+        raise ValueError("expected scales [nlist]")
+    if _slots(offsets, "offsets") != (nlist + 1,) or _slots(order, "order") != (t,) or \
+            _slots(pos, "pos").numel() != t:
+        raise ValueError("expected offsets [nlist + 1], order [t] and pos [t, 1]")
+    out = _out(out, (t, n), x.dtype, x.device, stream)
+    ws, ws_bytes, _keep = _workspace(workspace, ivfpq_adapter_product_bytes(t, r), x.device, stream)
+    _check(lib().ivfpq_adapter_product_ex(x.data_ptr(), kind, t, d, w.data_ptr(), n,
+                                          down.data_ptr(), up.data_ptr(), nlist, r, _ptr(scales),
+                                          offsets.data_ptr(), order.data_ptr(), pos.data_ptr(), ws,
+                                          ws_bytes, out.data_ptr(), _raw_stream(stream)))
+    return out
+
+
+def ivfpq_table_lookup_ex(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out=None,
+                          stream=None) -> torch.Tensor:
+    """scale * table[ids]: table [rows, d], ids int32 of any shape; zero where an id is
+    outside the table.  Returns [*ids.shape, d]."""
+    kind, (rows, d) = _rows(table)
+    shape = _slots(ids, "ids")
+    out = _out(out, (*shape, d), table.dtype, table.device, stream)
+    _check(lib().ivfpq_table_lookup_ex(table.data_ptr(), kind, rows, d, ids.data_ptr(),
+                                       shape.numel(), scale, out.data_ptr(), _raw_stream(stream)))
+    return out
+
+
+def ivfpq_table_grad_bytes(nvec: int, d: int, k: int = 1) -> int:
+    return lib().ivfpq_table_grad_bytes(nvec, d, k)
+
+
+def ivfpq_table_grad_ex(grad: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor,
+                        scale: float = 1.0, k: int = 1, dtype=None, out=None, workspace=None,
+                        stream=None) -> torch.Tensor:
+    """The gradient of a table's rows, [nlist, d]: row l is scale times the sum of
+    grad[order[p] // k] over the positions p of list l.  For ivfpq_table_lookup_ex:
+    grad [n, d] of its output and (offsets, order, _) of
+    ivfpq_route_sort_ex(ids.view(-1, 1), rows).  dtype is grad's (the default) or float32."""
+    kind, (nvec, d) = _rows(grad)
+    if len(_slots(offsets, "offsets")) != 1 or offsets.shape[0] < 2:
+        raise ValueError("expected offsets [nlist + 1]")
+    if k < 1 or _slots(order, "order") != (nvec * k,):
+        raise ValueError("expected order [nvec k], k >= 1")
+    nlist = offsets.shape[0] - 1
+    dtype = grad.dtype if dtype is None else dtype
+    out_kind = _row_type(dtype)
+    out = _out(out, (nlist, d), dtype, grad.device, stream)
+    ws, ws_bytes, _keep = _workspace(workspace, ivfpq_table_grad_bytes(nvec, d, k), grad.device,
+                                     stream)
+    _check(lib().ivfpq_table_grad_ex(grad.data_ptr(), kind, nvec, d, offsets.data_ptr(),
+                                     order.data_ptr(), k, nlist, scale, out_kind, ws, ws_bytes,
+                                     out.data_ptr(), _raw_stream(stream)))
+    return out
 
 
 # ---------------------------------------------------------------------------

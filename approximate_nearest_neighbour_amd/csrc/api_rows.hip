@@ -1,31 +1,12 @@
 // Entry points of the 4-bit rows, their products and the list routing: argument
 // checks on the host, then the kernels on the caller's stream.  Declarations and
 // conventions: include/ivfpq.h.
+#include "rows_check.hpp"
 #include "rows_internal.hpp"
-#include "status.hpp"
-
-#include <hip/hip_runtime.h>
-
-#include <string>
 
 using namespace ivfpq;
 
 namespace {
-
-constexpr int kMaxRowDim = 1 << 20;
-
-bool type_ok(int type) { return type == IVFPQ_F32 || type == IVFPQ_BF16 || type == IVFPQ_F16; }
-
-size_t type_size(int type) { return type == IVFPQ_F32 ? 4 : 2; }
-
-bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-ivfpq_status launched(hipError_t e, const char *what)
-{
-    if (e != hipSuccess)
-        return fail(IVFPQ_E_DEVICE, std::string(what) + ": " + hipGetErrorString(e));
-    return ok();
-}
 
 // Shape of the routed rows: nvec vectors of d values, k slots each.
 ivfpq_status check_route(int64_t nvec, int d, int type, int k)

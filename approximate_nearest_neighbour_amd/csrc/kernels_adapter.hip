@@ -1,0 +1,64 @@
+// Rows times one shared matrix, plus each row's own low-rank product.
+//
+// y[t] = W x[t] + s[a] U[a] (D[a] x[t]), a the list (adapter) of row t, in two
+// launches: the hidden rows h[t] = s[a] D[a] x[t], a product per list of the sorted
+// rows, then the shared product with the contraction continued over the hidden rows:
+// after the chunks of x and W come, for each list among a tile's rows, chunks of
+// that list's hidden rows (the other rows zero) and its up matrix.  So the adapters
+// add to sums that are still in registers.
+//
+// Hidden rows of 16-bit types are kept as two parts, h = high + low, side by side,
+// and multiplied with the same up matrix twice: rounded once more to 16 bits they
+// would add an error as large as the result's own rounding.  float32 hidden
+// rows are float32.
+#include "list_tiles.hpp"
+
+namespace ivfpq {
+
+static int hidden_part(int r) { return (r + 7) / 8 * 8; }
+
+template <typename T>
+static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
+{
+    constexpr int KS = std::is_same<T, float>::value ? 32 : 64;
+    ListJob p;
+    p.a = q.x;
+    p.rows = p.arows = q.t;
+    p.kdim = q.d;
+    p.nlist = q.nlist;
+    p.offsets = q.offsets;
+    p.order = q.order;
+    p.pos = q.pos;
+    p.scales = q.scales;
+    p.up = q.up;
+    p.r = q.r;
+    p.rp = hidden_part(q.r);
+    p.width = sizeof(T) == 4 ? p.rp : 2 * p.rp;
+    p.hidden = q.ws;
+    p.row_list = reinterpret_cast<int32_t *>(static_cast<T *>(q.ws) + q.t * p.width);
+    p.b = q.down;
+    p.n = q.r;
+    if (hipError_t e = launch_tiles<T, float, kHidden, KS, 2, 1, 2, 2>(p, stream))
+        return e;
+    p.b = q.w;
+    p.n = q.n;
+    p.out = q.out;
+    return launch_tiles<T, T, kAdapter, KS, 2, 2, 2, 2>(p, stream);
+}
+
+size_t adapter_bytes(int64_t t, int r)
+{
+    // hidden rows, 32 bits a value in either form, and the rows' lists
+    return (size_t)t * ((size_t)hidden_part(r) * 4 + 4);
+}
+
+hipError_t launch_adapter(const AdapterProduct &p, int type, hipStream_t stream)
+{
+    switch (type) {
+    case kF32: return adapter_as<float>(p, stream);
+    case kBF16: return adapter_as<__bf16>(p, stream);
+    default: return adapter_as<_Float16>(p, stream);
+    }
+}
+
+} // namespace ivfpq

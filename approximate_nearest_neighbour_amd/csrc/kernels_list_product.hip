@@ -1,0 +1,78 @@
+// Products of rows sorted by list with their list's own matrix, and the gradient of
+// the matrices.
+#include "list_tiles.hpp"
+
+namespace ivfpq {
+
+template <typename T, int FORM>
+static hipError_t rows_as(const ListJob &p, hipStream_t stream)
+{
+    if constexpr (std::is_same<T, float>::value)
+        return launch_tiles<T, T, FORM, 32, 2, 2, 2, 2>(p, stream);
+    else
+        return launch_tiles<T, T, FORM, 64, 2, 2, 2, 2>(p, stream);
+}
+
+template <typename T>
+static hipError_t product_as(const ListJob &p, bool transposed, hipStream_t stream)
+{
+    return transposed ? rows_as<T, kRowsAcross>(p, stream) : rows_as<T, kRowsAlong>(p, stream);
+}
+
+hipError_t launch_list_product(const ListProduct &q, int type, hipStream_t stream)
+{
+    ListJob p;
+    p.a = q.x;
+    p.arows = q.arows;
+    p.kdim = q.d;
+    p.b = q.matrices;
+    p.n = q.n;
+    p.nlist = q.nlist;
+    p.offsets = q.offsets;
+    p.order = q.order;
+    p.k = FastDiv((uint32_t)q.k);
+    p.rows = q.rows;
+    p.out = q.out;
+    switch (type) {
+    case kF32: return product_as<float>(p, q.transposed, stream);
+    case kBF16: return product_as<__bf16>(p, q.transposed, stream);
+    default: return product_as<_Float16>(p, q.transposed, stream);
+    }
+}
+
+template <typename T, typename TO>
+static hipError_t gradient_as(const ListJob &p, hipStream_t stream)
+{
+    return launch_tiles<T, TO, kGradient, 32, 2, 2, 2, 2>(p, stream);
+}
+
+template <typename T>
+static hipError_t gradient_to(const ListJob &p, int out_type, hipStream_t stream)
+{
+    return out_type == kF32 ? gradient_as<T, float>(p, stream) : gradient_as<T, T>(p, stream);
+}
+
+size_t list_gradient_bytes(int64_t, int, int, int) { return 0; }
+
+hipError_t launch_list_gradient(const ListGradient &q, int type, int out_type, hipStream_t stream)
+{
+    ListJob p;
+    p.a = q.grad;
+    p.m = q.n;
+    p.b = q.x;
+    p.arows = q.arows;
+    p.n = q.d;
+    p.nlist = q.nlist;
+    p.offsets = q.offsets;
+    p.order = q.order;
+    p.k = FastDiv((uint32_t)q.k);
+    p.rows = q.rows;
+    p.out = q.out;
+    switch (type) {
+    case kF32: return gradient_as<float, float>(p, stream);
+    case kBF16: return gradient_to<__bf16>(p, out_type, stream);
+    default: return gradient_to<_Float16>(p, out_type, stream);
+    }
+}
+
+} // namespace ivfpq

@@ -1,4 +1,4 @@
-// Launchers of the 4-bit rows and the list routing, as their entry points call them.
+// Launchers of the row operators, as their entry points call them.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -42,5 +42,51 @@ hipError_t launch_route_combine_grad(const void *grad, const void *rows, int typ
                                      int d, const int32_t *order, const int32_t *pos,
                                      const float *weights, int k, void *d_rows, float *d_weights,
                                      hipStream_t stream);
+
+
+// Products per list of rows in 16 or 32 bits: out [rows][n], output row p of list e is
+// x's row order[p] / k (or p) times matrix e, [n][d] (transposed: [d][n]).
+struct ListProduct {
+    const void *x = nullptr, *matrices = nullptr;
+    void *out = nullptr;
+    int64_t arows = 0, rows = 0;
+    int d = 0, n = 0, nlist = 0, k = 1;
+    bool transposed = false;
+    const int32_t *offsets = nullptr, *order = nullptr;
+};
+hipError_t launch_list_product(const ListProduct &p, int type, hipStream_t stream);
+
+// out [nlist][n][d]: per list, the sum over its rows p of grad[p] (outer) x[order[p] / k].
+struct ListGradient {
+    const void *grad = nullptr, *x = nullptr;
+    void *out = nullptr, *ws = nullptr;
+    int64_t arows = 0, rows = 0;
+    int d = 0, n = 0, nlist = 0, k = 1;
+    const int32_t *offsets = nullptr, *order = nullptr;
+};
+size_t list_gradient_bytes(int64_t rows, int n, int d, int nlist);
+hipError_t launch_list_gradient(const ListGradient &p, int type, int out_type, hipStream_t stream);
+
+// out [t][n] = x w^T, plus for a row of list a scales[a] up[a] (down[a] x).
+struct AdapterProduct {
+    const void *x = nullptr, *w = nullptr, *down = nullptr, *up = nullptr;
+    const float *scales = nullptr;
+    void *out = nullptr, *ws = nullptr;
+    int64_t t = 0;
+    int d = 0, n = 0, nlist = 0, r = 0;
+    const int32_t *offsets = nullptr, *order = nullptr, *pos = nullptr;
+};
+size_t adapter_bytes(int64_t t, int r);
+hipError_t launch_adapter(const AdapterProduct &p, int type, hipStream_t stream);
+
+// out [n][d] = scale times row ids[i] of table [rows][d].
+hipError_t launch_table_lookup(const void *table, int type, int64_t rows, int d, const int32_t *ids,
+                               int64_t n, float scale, void *out, hipStream_t stream);
+
+// out [nlist][d]: scale times the sum of the rows order[p] / k of grad over a list's p.
+size_t table_grad_bytes(int64_t n, int d);
+hipError_t launch_table_grad(const void *grad, int type, int64_t nvec, int d,
+                             const int32_t *offsets, const int32_t *order, int k, int nlist,
+                             float scale, int out_type, void *out, void *ws, hipStream_t stream);
 
 } // namespace ivfpq

@@ -519,6 +519,100 @@ ivfpq_status ivfpq_route_combine_grad_ex(const void *grad_dev, const void *rows_
                                          void *grad_rows_dev, float *grad_weights_dev,
                                          void *stream);
 
+/* ---- products per list, adapters, table rows -----------------------------
+ *
+ * What rows sorted by ivfpq_route_sort_ex are multiplied and summed with, in
+ * float32, bfloat16 or binary16.  All calls are asynchronous on `stream` of the
+ * current device, allocate nothing and may be captured in a graph.  Rows and
+ * matrices are row-major and contiguous, aligned to their type (16-byte aligned
+ * ones whose rows are multiples of 16 bytes are read faster); an output or workspace
+ * overlaps no input.  Two calls that may run at the same time need a workspace
+ * each.  Sums are float32, rounded once to the output's type.  float32 products
+ * are formed from three bfloat16 parts of each factor, exact to 2^-26 of every
+ * product; an infinite factor gives NaN there, in 16-bit types what float32 sums
+ * of its products give. */
+
+/* Rows sorted by list, each times its list's own matrix: matrices_dev holds nlist
+ * matrices [n][d] (transposed 0) or [d][n] (not 0), offsets_dev [nlist + 1]
+ * int32 the lists' first rows (ascending; read on the device, values outside [0,
+ * rows] count as the nearer end).  Output row p of list e is matrix e (transposed:
+ * its transpose) times row order[p] / k of rows_dev [arows][d], or row p when
+ * order_dev is NULL (then arows >= rows).  Rows of no list are zero; an entry of
+ * order outside the rows stands for a row of zeros.  out_dev [rows][n] of `type`.
+ * rows = 0 is a no-op.  The gradient of the sorted rows is the same call on the
+ * outputs' gradient with the other `transposed`, n and d exchanged (then
+ * ivfpq_route_combine_ex takes it to the vectors).  Errors: IVFPQ_E_INVALID_ARG (a
+ * bad type, rows or arows outside [0, 2^31), d or n outside [1, 2^20], nlist
+ * outside [1, 2^16], k < 1, too few rows, a NULL or misaligned pointer),
+ * IVFPQ_E_DEVICE. */
+ivfpq_status ivfpq_list_product_ex(const void *rows_dev, int type, int64_t arows, int d,
+                                   const void *matrices_dev, int transposed, int nlist, int n,
+                                   const int32_t *offsets_dev, const int32_t *order_dev, int k,
+                                   int64_t rows, void *out_dev, void *stream);
+
+/* Bytes of device workspace for ivfpq_list_product_grad_ex; 0 where none is
+ * needed and for arguments that it rejects. */
+size_t ivfpq_list_product_grad_bytes(int64_t rows, int n, int d, int nlist);
+
+/* The gradient of the matrices: out_dev [nlist][n][d] of out_type (`type` or
+ * IVFPQ_F32) receives, per list, the sum over its rows p of grad[p] times row
+ * order[p] / k of rows_dev (or row p), grad_dev [rows][n] the gradient of the
+ * product's output; zero for an empty list.  For transposed matrices exchange
+ * the two: they are read alike when order_dev is NULL.  The result does not depend
+ * on the run.  Errors as above, and IVFPQ_E_INVALID_ARG for a bad out_type or a
+ * workspace below ivfpq_list_product_grad_bytes or not 16-byte aligned. */
+ivfpq_status ivfpq_list_product_grad_ex(const void *grad_dev, const void *rows_dev, int type,
+                                        int64_t arows, int d, int nlist, int n,
+                                        const int32_t *offsets_dev, const int32_t *order_dev, int k,
+                                        int64_t rows, int out_type, void *workspace_dev,
+                                        size_t workspace_bytes, void *out_dev, void *stream);
+
+/* Bytes of device workspace for ivfpq_adapter_product_ex. */
+size_t ivfpq_adapter_product_bytes(int64_t t, int r);
+
+/* Rows through one shared matrix, each with a low-rank product of its own beside it
+ * (the adapter of the request that the row belongs to): out_dev [t][n], row i is
+ * W x + scales[a] U_a (D_a x) for x row i of rows_dev [t][d], W matrix_dev [n][d],
+ * a the row's list, D_a of down_dev [nlist][r][d], U_a of up_dev [nlist][n][r],
+ * scales_dev [nlist] float32 (NULL: 1).  offsets_dev, order_dev [t] and pos_dev [t]
+ * are those of one ivfpq_route_sort_ex of the rows' lists (k = 1), made once for
+ * all products of the same rows; a row whose list is masked gets W x.  D_a x times
+ * the scale is held in float32, for 16-bit types in two parts (binary16: below
+ * 65504).  t = 0 is a no-op.  Its gradients come from ivfpq_list_product_ex and
+ * ivfpq_list_product_grad_ex of the sorted rows.  Errors as above, with r in [1,
+ * 2^12]. */
+ivfpq_status ivfpq_adapter_product_ex(const void *rows_dev, int type, int64_t t, int d,
+                                      const void *matrix_dev, int n, const void *down_dev,
+                                      const void *up_dev, int nlist, int r, const float *scales_dev,
+                                      const int32_t *offsets_dev, const int32_t *order_dev,
+                                      const int32_t *pos_dev, void *workspace_dev,
+                                      size_t workspace_bytes, void *out_dev, void *stream);
+
+/* out_dev [n][d]: scale times row ids[i] of table_dev [rows][d], formed in
+ * float32 and rounded once; zero where the number is outside [0, rows).  n = 0 is
+ * a no-op.  Errors: IVFPQ_E_INVALID_ARG (a bad type, rows or n outside [0, 2^31),
+ * d outside [1, 2^20], a NULL or misaligned pointer), IVFPQ_E_DEVICE. */
+ivfpq_status ivfpq_table_lookup_ex(const void *table_dev, int type, int64_t rows, int d,
+                                   const int32_t *ids_dev, int64_t n, float scale, void *out_dev,
+                                   void *stream);
+
+/* Bytes of device workspace for ivfpq_table_grad_ex; 0 where none is needed. */
+size_t ivfpq_table_grad_bytes(int64_t nvec, int d, int k);
+
+/* The gradient of the table, out_dev [nlist][d] of out_type (`type` or IVFPQ_F32):
+ * row l is scale times the sum of the rows order[p] / k of grad_dev [nvec][d] over
+ * the positions p of list l, zero without any; entries of order outside [0, nvec k)
+ * add nothing.  offsets_dev and order_dev [nvec k] are those of
+ * ivfpq_route_sort_ex of the row numbers (k = 1 for the gradient of a lookup; with
+ * vectors in the place of grad these are the sums of the lists' vectors).  The
+ * result does not depend on the run.  Errors: as above, and IVFPQ_E_INVALID_ARG
+ * for nvec k >= 2^31, nlist outside [1, 2^22), a bad out_type, or a workspace below
+ * ivfpq_table_grad_bytes or not 16-byte aligned. */
+ivfpq_status ivfpq_table_grad_ex(const void *grad_dev, int type, int64_t nvec, int d,
+                                 const int32_t *offsets_dev, const int32_t *order_dev, int k,
+                                 int nlist, float scale, int out_type, void *workspace_dev,
+                                 size_t workspace_bytes, void *out_dev, void *stream);
+
 /* ---- measurement support ---------------------------------------------- */
 
 /* Reference streaming read for the bandwidth roofline (not part of the search

@@ -1,5 +1,5 @@
-"""4-bit rows, their products and the routing of vectors to lists, by
-definition, in numpy and 64-bit floats (sharing no code with the library).
+"""4-bit rows, their products, the routing of vectors to lists, and what sorted
+rows are multiplied and summed with, by definition, in numpy and 64-bit floats (sharing no code with the library).
 
 4-bit rows follow the OCP Microscaling specification (MXFP4): blocks of 32
 values, e2m1 codes and one power-of-two scale a block.
@@ -109,3 +109,48 @@ def combine_grad(grad, rows, pos, weights):
                 d_w[t, j] = grad[t] @ rows[p]
                 mag[t, j] = np.abs(grad[t]) @ np.abs(rows[p])
     return d_rows, d_w, mag
+
+
+def list_gradient(grad, x, offsets, order, k, nlist):
+    """Per list the sum of grad[p] (outer) x[order[p] // k] (or x[p]), and the sums of
+    the terms' magnitudes."""
+    out = np.zeros((nlist, grad.shape[1], x.shape[1]))
+    mag = np.zeros_like(out)
+    for e in range(nlist):
+        for p in range(offsets[e], offsets[e + 1]):
+            r = x[p if order is None else order[p] // k]
+            out[e] += np.outer(grad[p], r)
+            mag[e] += np.outer(np.abs(grad[p]), np.abs(r))
+    return out, mag
+
+
+def adapter(x, w, down, up, lists, scales=None):
+    """W x + s U (D x) for each row x with the D, U and s of its list (W x where the
+    list is masked), and the sums of the terms' magnitudes."""
+    out, mag = x @ w.T, np.abs(x) @ np.abs(w).T
+    for i, e in enumerate(lists.tolist()):
+        if 0 <= e < len(down):
+            s = 1.0 if scales is None else float(scales[e])
+            out[i] += s * (up[e] @ (down[e] @ x[i]))
+            mag[i] += abs(s) * (np.abs(up[e]) @ (np.abs(down[e]) @ np.abs(x[i])))
+    return out, mag
+
+
+def table_lookup(table, ids, scale):
+    out = np.zeros((len(ids), table.shape[1]))
+    for i, e in enumerate(ids.tolist()):
+        if 0 <= e < len(table):
+            out[i] = table[e] * scale
+    return out
+
+
+def table_gradient(grad, ids, rows, scale):
+    """Sums of the rows of grad with the same number (ids [nvec, k]), and of their
+    magnitudes."""
+    out, mag = np.zeros((rows, grad.shape[1])), np.zeros((rows, grad.shape[1]))
+    for i, row in enumerate(ids.tolist()):
+        for e in row:
+            if 0 <= e < rows:
+                out[e] += grad[i] * scale
+                mag[e] += np.abs(grad[i] * scale)
+    return out, mag

@@ -1,0 +1,156 @@
+"""Products per list and the gradient of their matrices on the GPU against the 64-bit
+definitions of oracle/rows.py.
+
+Tolerances.  Small integers: every product and partial sum is an integer below 2^24
+(2^11 and 2^8 parts of the inputs too), so results are exact, rounded once.  Real
+values: K exact products added one after the other in float32 take K - 1 additions
+that round, each by at most 2^-23 of the sum of the magnitudes however it rounds.  A
+float32 product is six part products, so there are 6 K - 1 such additions, of terms
+whose magnitudes sum to at most (1 + 2^-8 + 2^-17)^2 < 1 + 2^-6 of the products';
+the three dropped parts add 2^-26.  Storing rounds by half a step of the type, or
+2^-25 near zero for binary16 and 2^-134 for bfloat16.
+"""
+import numpy as np
+import pytest
+import torch
+
+import approximate_nearest_neighbour_amd as A
+from oracle import rows as R
+
+pytestmark = pytest.mark.gpu
+
+UNIT = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+TYPES = list(UNIT)
+
+
+def np64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def integers(rng, *shape, dtype, top=3):
+    return torch.from_numpy(rng.integers(-top, top + 1, shape).astype(np.float32)).to(dtype).cuda()
+
+
+def reals(rng, *shape, dtype):
+    return torch.from_numpy(rng.standard_normal(shape)).to(dtype).cuda()
+
+
+def ragged(rng, rows, nlist, lo=0, hi=None):
+    """Offsets of nlist lists between rows lo and hi, some of them empty."""
+    hi = rows if hi is None else hi
+    cuts = np.sort(rng.integers(lo, hi + 1, nlist - 1)) if nlist > 1 else np.empty(0, int)
+    return np.concatenate([[lo], cuts, [hi]]).astype(np.int32)
+
+
+def list_product64(x, matrices, offsets, rows, source, transposed):
+    out = np.zeros((rows, matrices.shape[1] if not transposed else matrices.shape[2]))
+    mag = np.zeros_like(out)
+    for e, w in enumerate(matrices):
+        lo, hi = max(offsets[e], 0), min(offsets[e + 1], rows)
+        if lo < hi:
+            w = w if transposed else w.T
+            out[lo:hi] = x[source[lo:hi]] @ w
+            mag[lo:hi] = np.abs(x[source[lo:hi]]) @ np.abs(w)
+    return out, mag
+
+
+def sum_error(terms, dtype):
+    """Share of the sum of magnitudes that a float32 sum of so many products is off by."""
+    if dtype == torch.float32:
+        return (6 * terms - 1) * 2.0 ** -23 * (1 + 2.0 ** -6) + 2.0 ** -26
+    return (terms - 1) * 2.0 ** -23
+
+
+def rounded(exact, dtype):
+    return np64(torch.from_numpy(exact).to(dtype))
+
+
+# rows, lists, n, d: one row and one value, tiles' edges, odd sizes, many lists of few
+# rows, lists longer than any tile
+SHAPES = [(1, 1, 1, 1), (3, 1, 5, 7), (16, 2, 16, 32), (17, 3, 33, 31), (64, 1, 64, 64),
+          (65, 4, 129, 65), (127, 2, 128, 100), (128, 1, 256, 128), (200, 7, 72, 96),
+          (300, 64, 40, 136), (31, 200, 24, 8), (1000, 3, 136, 72), (777, 16, 301, 200),
+          (700, 2, 520, 264), (2500, 5, 96, 40), (40, 1, 1024, 512), (513, 2, 257, 1032),
+          (33, 9, 1040, 2050), (1500, 1, 16, 24)]
+
+
+@pytest.mark.parametrize("rows,nlist,n,d", SHAPES)
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_product_is_exact_on_integers(rows, nlist, n, d, transposed, dtype):
+    rng = np.random.default_rng(rows + nlist + n + d)
+    x = integers(rng, rows, d, dtype=dtype)
+    w = integers(rng, nlist, *((d, n) if transposed else (n, d)), dtype=dtype)
+    offsets = ragged(rng, rows, nlist, rows // 9, rows - rows // 7)
+    y = A.ivfpq_list_product_ex(x, w, torch.from_numpy(offsets).cuda(), transposed=transposed)
+    want, _ = list_product64(np64(x), np64(w), offsets, rows, np.arange(rows), transposed)
+    assert y.dtype == dtype and np.array_equal(np64(y), rounded(want, dtype))
+
+
+@pytest.mark.parametrize("t,k,nlist,n,d", [(1, 1, 1, 8, 8), (1, 8, 64, 64, 128), (4, 8, 16, 136, 64),
+                                           (100, 3, 7, 33, 49), (333, 2, 5, 264, 72),
+                                           (600, 4, 3, 48, 200)])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_product_gathers_by_order(t, k, nlist, n, d, transposed, dtype):
+    rng = np.random.default_rng(t + n)
+    lists = rng.integers(-1, nlist, (t, k)).astype(np.int32)
+    offsets, order, _ = A.ivfpq_route_sort_ex(torch.from_numpy(lists).cuda(), nlist)
+    x = integers(rng, t, d, dtype=dtype)
+    w = integers(rng, nlist, *((d, n) if transposed else (n, d)), dtype=dtype)
+    y = A.ivfpq_list_product_ex(x, w, offsets, order=order, k=k, transposed=transposed)
+    source = np.maximum(order.cpu().numpy(), 0) // k
+    want, _ = list_product64(np64(x), np64(w), offsets.tolist(), t * k, source, transposed)
+    assert np.array_equal(np64(y), rounded(want, dtype))
+
+
+@pytest.mark.parametrize("rows,nlist,n,d", [(1, 1, 1, 1), (130, 4, 72, 1), (64, 2, 40, 4),
+                                            (150, 3, 130, 200), (90, 5, 65, 777)])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_product_of_reals(rows, nlist, n, d, transposed, dtype):
+    rng = np.random.default_rng(rows * d)
+    x = reals(rng, rows, d, dtype=dtype)
+    w = reals(rng, nlist, *((d, n) if transposed else (n, d)), dtype=dtype)
+    offsets = ragged(rng, rows, nlist)
+    y = A.ivfpq_list_product_ex(x, w, torch.from_numpy(offsets).cuda(), transposed=transposed)
+    want, mag = list_product64(np64(x), np64(w), offsets, rows, np.arange(rows), transposed)
+    sums = sum_error(d, dtype) * mag
+    assert (np.abs(np64(y) - want) <= sums + UNIT[dtype] * (np.abs(want) + sums) + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("t,k,nlist,n,d", [(1, 1, 1, 1, 1), (5, 1, 3, 8, 16), (40, 2, 4, 33, 31),
+                                           (64, 1, 1, 64, 64), (333, 3, 5, 65, 129),
+                                           (800, 2, 3, 136, 264), (100, 4, 150, 40, 24),
+                                           (3000, 1, 2, 32, 48), (500, 2, 7, 257, 520),
+                                           (6000, 1, 1, 24, 40)])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("dtype,out", [(t, o) for t in TYPES for o in {t, torch.float32}])
+def test_gradient_is_exact_on_integers(t, k, nlist, n, d, gather, dtype, out):
+    rng = np.random.default_rng(t + n + d)
+    lists = rng.integers(-1, nlist, (t, k)).astype(np.int32)
+    offsets, order, _ = A.ivfpq_route_sort_ex(torch.from_numpy(lists).cuda(), nlist)
+    rows = t * k
+    grad = integers(rng, rows, n, dtype=dtype)
+    x = integers(rng, t if gather else rows, d, dtype=dtype)
+    got = A.ivfpq_list_product_grad_ex(grad, x, offsets, order=order if gather else None, k=k,
+                                       dtype=out)
+    source = np.maximum(order.cpu().numpy(), 0) // k if gather else np.arange(rows)
+    g64, x64, bounds = np64(grad), np64(x), offsets.tolist()
+    want = np.stack([g64[lo:hi].T @ x64[source[lo:hi]] for lo, hi in zip(bounds, bounds[1:])])
+    assert got.dtype == out and np.array_equal(np64(got), rounded(want, out))
+
+
+def test_definitions_of_the_oracle():
+    """The vectorised forms above against the oracle's loops."""
+    rng = np.random.default_rng(0)
+    x, w = rng.standard_normal((6, 5)), rng.standard_normal((3, 4, 5))
+    offsets, order = [0, 2, 2, 7], rng.integers(0, 12, 8)
+    want, mag = R.list_product(x, w, offsets, order, 2, 8)
+    got, mag2 = list_product64(x, w, offsets, 8, order // 2, False)
+    assert np.allclose(got, want) and np.allclose(mag, mag2)
+    grad = rng.standard_normal((8, 4))
+    want, _ = R.list_gradient(grad, x, offsets, order, 2, 3)
+    for e in range(3):
+        part = slice(offsets[e], offsets[e + 1])
+        assert np.allclose(grad[part].T @ x[order[part] // 2], want[e])
