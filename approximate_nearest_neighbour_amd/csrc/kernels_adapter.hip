@@ -43,6 +43,9 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
     p.b = q.w;
     p.n = q.n;
     p.out = q.out;
+    if constexpr (sizeof(T) == 2)
+        if (copies_fit<kAdapter>(p))
+            return launch_copies<T, T, kAdapter, 64, 2, 4, 2, 2, 4>(p, stream);
     return launch_tiles<T, T, kAdapter, KS, 2, 2, 2, 2>(p, stream);
 }
 

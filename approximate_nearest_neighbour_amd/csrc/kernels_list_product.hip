@@ -9,6 +9,8 @@ static hipError_t rows_as(const ListJob &p, hipStream_t stream)
 {
     if constexpr (std::is_same<T, float>::value)
         return launch_tiles<T, T, FORM, 32, 2, 2, 2, 2>(p, stream);
+    else if (copies_fit<FORM>(p))
+        return launch_copies<T, T, FORM, 64, 2, 4, 2, 2, 4>(p, stream);
     else
         return launch_tiles<T, T, FORM, 64, 2, 2, 2, 2>(p, stream);
 }
@@ -43,6 +45,9 @@ hipError_t launch_list_product(const ListProduct &q, int type, hipStream_t strea
 template <typename T, typename TO>
 static hipError_t gradient_as(const ListJob &p, hipStream_t stream)
 {
+    if constexpr (sizeof(T) == 2)
+        if (copies_fit<kGradient>(p))
+            return launch_copies<T, TO, kGradient, 64, 2, 4, 2, 2, 4>(p, stream);
     return launch_tiles<T, TO, kGradient, 32, 2, 2, 2, 2>(p, stream);
 }
 

@@ -28,6 +28,7 @@
 #include "rows_internal.hpp"
 #include "tile_ops.hpp"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace ivfpq {
@@ -257,6 +258,51 @@ __device__ __forceinline__ int64_t source_row(const ListJob &p, int64_t row)
     return q < p.arows ? q : -1;
 }
 
+// The list of each row of a tile (-1: none), and these lists each once, ascending:
+// segs[0 .. segs[TM]).
+template <int TM, int THREADS>
+__device__ __forceinline__ void find_lists(const ListJob &p, const PartTile &tile, int *tile_list,
+                                           int *segs)
+{
+    const int tid = (int)threadIdx.x, lane = lane_id();
+    for (int i = tid; i < TM; i += THREADS) {
+        const int64_t row = tile.p0 + i;
+        int e = -1;
+        if (row < tile.p1 && (uint32_t)p.pos[row] < (uint64_t)p.rows) {
+            e = p.row_list[row];
+            e = e < p.nlist ? e : -1;
+        }
+        tile_list[i] = e;
+    }
+    lds_barrier();
+    if (tid < 64) {
+        int last = -1, found = 0;
+        for (;;) { // at most TM times
+            uint32_t next = 0xFFFFFFFFu;
+#pragma unroll
+            for (int i = 0; i < (TM + 63) / 64; ++i) {
+                const int e = i * 64 + lane < TM ? tile_list[i * 64 + lane] : -1;
+                next = e > last ? min(next, (uint32_t)e) : next;
+            }
+            next = min(next, xor_lane<1>(next));
+            next = min(next, xor_lane<2>(next));
+            next = min(next, xor_lane<4>(next));
+            next = min(next, xor_lane<8>(next));
+            next = min(next, xor_lane<16>(next));
+            next = min(next, xor_lane<32>(next));
+            if (next == 0xFFFFFFFFu)
+                break;
+            last = (int)next;
+            if (lane == 0)
+                segs[found] = last;
+            ++found;
+        }
+        if (lane == 0)
+            segs[TM] = found;
+    }
+    lds_barrier();
+}
+
 template <typename T, typename TO, int FORM, int KS, int WM, int WN, int MW, int NW>
 __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
 {
@@ -306,43 +352,7 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
     const int64_t main_chunks = chunks;
     const int per_seg = FORM == kAdapter ? (p.width + KS - 1) / KS : 1;
     if constexpr (FORM == kAdapter) {
-        // the lists of the tile's rows, each once
-        for (int i = tid; i < TM; i += THREADS) {
-            const int64_t row = tile.p0 + i;
-            int e = -1;
-            if (row < tile.p1 && (uint32_t)p.pos[row] < (uint64_t)p.rows) {
-                e = p.row_list[row];
-                e = e < p.nlist ? e : -1;
-            }
-            tile_list[i] = e;
-        }
-        __syncthreads();
-        if (wave == 0) {
-            int last = -1, found = 0;
-            for (;;) { // ascending, at most TM times
-                uint32_t next = 0xFFFFFFFFu;
-#pragma unroll
-                for (int i = 0; i < (TM + 63) / 64; ++i) {
-                    const int e = i * 64 + lane < TM ? tile_list[i * 64 + lane] : -1;
-                    next = e > last ? min(next, (uint32_t)e) : next;
-                }
-                next = min(next, xor_lane<1>(next));
-                next = min(next, xor_lane<2>(next));
-                next = min(next, xor_lane<4>(next));
-                next = min(next, xor_lane<8>(next));
-                next = min(next, xor_lane<16>(next));
-                next = min(next, xor_lane<32>(next));
-                if (next == 0xFFFFFFFFu)
-                    break;
-                last = (int)next;
-                if (lane == 0)
-                    segs[found] = last;
-                ++found;
-            }
-            if (lane == 0)
-                segs[TM] = found;
-        }
-        __syncthreads();
+        find_lists<TM, THREADS>(p, tile, tile_list, segs);
         chunks += (int64_t)segs[TM] * per_seg;
     }
 
@@ -560,6 +570,440 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
                 }
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// tiles of 16-bit operands copied from memory into LDS without registers
+// ---------------------------------------------------------------------------
+
+// Offset of a copy that reads nothing: past any range (ranges are below 2^31 bytes).
+constexpr uint32_t kNowhere = 0x80000000u;
+
+// A memory range of less than 2^31 bytes from byte `from` on.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t range_of(const void *base, int64_t from,
+                                                           int64_t bytes)
+{
+    from = uniform(from);
+    const int64_t left = min(max(bytes - from, (int64_t)0), (int64_t)0x7FFFFFFF);
+    const uint8_t *p = static_cast<const uint8_t *>(base) + from;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)uniform(left),
+                                             0x00027000);
+}
+
+// Which tile a workgroup forms: groups of `high` by `wide` tiles go to the XCDs in turn
+// (every eighth workgroup runs on the same one), m first inside a group, so that the
+// tiles that an XCD's 32 CUs form together share operands in its cache, and numbers
+// that turn out empty are spread over all.
+struct TileGroups {
+    uint32_t high, wide, across; // across: groups along n
+    int64_t mt;
+    uint32_t nt;
+    __device__ __forceinline__ bool tile(int64_t block, int64_t &m, uint32_t &n) const
+    {
+        const uint32_t size = high * wide, x = (uint32_t)block & 7;
+        const int64_t i = block >> 3, turn = i / size, group = turn * 8 + x;
+        const uint32_t in = (uint32_t)(i - turn * size);
+        m = group / across * high + in % high;
+        n = (uint32_t)(group % across) * wide + in / high;
+        return m < mt && n < nt;
+    }
+};
+
+template <typename T, typename TO, int FORM, int KS, int STAGES, int WM, int WN, int MW, int NW>
+__global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, TileGroups groups)
+{
+    static_assert(sizeof(T) == 2, "float32 operands go through registers");
+    using F = FormOf<FORM>;
+    constexpr int WAVES = MW * NW, THREADS = 64 * WAVES, TM = 32 * WM * MW, TN = 32 * WN * NW;
+    constexpr bool PAIR = sizeof(TO) == 2;
+    using PA = Place<F::A_ALONG, TM, KS>;
+    using PB = Place<F::B_ALONG, TN, KS>;
+    constexpr int STAGE = PA::PLANE + PB::PLANE;
+    // objects of their own, so that the compiler knows a copy into one from a read of
+    // another
+    __shared__ __align__(16) uint8_t stage0[STAGE], stage1[STAGE];
+    __shared__ __align__(16) uint8_t stage2[STAGES > 2 ? STAGE : 16], stage3[STAGES > 3 ? STAGE : 16];
+    __shared__ int segs[FORM == kAdapter ? TM + 1 : 1];
+    __shared__ int tile_list[FORM == kAdapter ? TM : 1];
+
+    const int tid = (int)threadIdx.x, lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % MW, wn = wave / MW;
+    int64_t mt;
+    uint32_t nt;
+    if (!groups.tile(p.block0 + blockIdx.x, mt, nt))
+        return;
+    const int n0 = (int)nt * TN;
+
+    PartTile tile;
+    int m0 = 0;
+    if constexpr (FORM == kGradient) {
+        const int e = (int)(mt / p.mt);
+        m0 = (int)(mt - (int64_t)e * p.mt) * TM;
+        tile = {e, part_begin(p.offsets, p.nlist, p.rows, e + 1),
+                part_begin(p.offsets, p.nlist, p.rows, e + 2)};
+    } else if constexpr (FORM == kAdapter) {
+        tile = {0, mt * TM, min(mt * TM + TM, p.rows)};
+    } else {
+        tile = find_part(p.offsets, p.nlist, p.rows, mt, TM, p.by_row);
+        if (tile.p0 >= tile.p1)
+            return;
+    }
+    tile.p0 = uniform(tile.p0);
+    tile.p1 = uniform(tile.p1);
+    tile.e = __builtin_amdgcn_readfirstlane(tile.e);
+    const bool listed = FORM == kAdapter || (tile.e >= 0 && tile.e < p.nlist);
+    const int64_t kdim = !listed ? 0 : FORM == kGradient ? max(tile.p1 - tile.p0, (int64_t)0)
+                                                         : (int64_t)p.kdim;
+    int chunks = (int)((kdim + KS - 1) / KS); // a list has fewer than 2^31 rows
+    const int main_chunks = chunks;
+    const int per_seg = FORM == kAdapter ? (p.width + KS - 1) / KS : 1;
+
+    // copies: instruction j of a wave brings 1 KB of consecutive LDS lines, a lane 16 bytes
+    constexpr int CA = PA::PLANE / 1024 / WAVES, CB = PB::PLANE / 1024 / WAVES;
+    static_assert(CA * 1024 * WAVES == PA::PLANE && CB * 1024 * WAVES == PB::PLANE, "whole copies");
+    constexpr int LA = 64 / PA::BLOCKS, LB = 64 / PB::BLOCKS; // lines of a copy
+    auto line_a = [&](int j) { return (wave * CA + j) * LA + lane / PA::BLOCKS; };
+    auto line_b = [&](int j) { return (wave * CB + j) * LB + lane / PB::BLOCKS; };
+    // the block of its line that a lane brings
+    auto block_a = [&](int j) { return (lane % PA::BLOCKS) ^ PA::swizzle(line_a(j)); };
+    auto block_b = [&](int j) { return (lane % PB::BLOCKS) ^ PB::swizzle(line_b(j)); };
+    uint32_t offa[CA], offb[CB]; // bytes from the start of the chunk's range
+    const int64_t lda = F::A_ALONG ? p.kdim : p.m, ldb = F::B_ALONG ? p.kdim : p.n;
+    const bool gather_a = F::PER_LIST_ROWS && p.order;
+#pragma unroll
+    for (int j = 0; j < CA; ++j) {
+        if constexpr (F::A_ALONG) {
+            const int64_t row = tile.p0 + line_a(j);
+            int64_t from = -1;
+            if (row < tile.p1)
+                from = F::PER_LIST_ROWS ? source_row(p, row) : row;
+            const int64_t first = gather_a ? 0 : tile.p0;
+            offa[j] = from < 0 ? kNowhere : (uint32_t)((from - first) * lda * 2) + block_a(j) * 16;
+        } else {
+            offa[j] = (uint32_t)(line_a(j) * lda * 2) + block_a(j) * 16;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < CB; ++j)
+        offb[j] = FORM == kGradient && p.order ? block_b(j) * 16
+                                               : (uint32_t)(line_b(j) * ldb * 2) + block_b(j) * 16;
+    const int64_t abytes = (FORM == kGradient ? p.rows : p.arows) * lda * 2;
+    const int64_t bmats = FORM == kAdapter ? 1 : p.nlist;
+    const int64_t bbytes = FORM == kGradient ? p.arows * ldb * 2 : bmats * p.n * (int64_t)p.kdim * 2;
+    const __amdgpu_buffer_rsrc_t arange =
+        range_of(p.a, F::A_ALONG && !gather_a ? tile.p0 * lda * 2 : 0, abytes);
+    const __amdgpu_buffer_rsrc_t brange = range_of(
+        p.b, F::B_ALONG ? ((FORM == kAdapter ? 0 : (int64_t)max(tile.e, 0) * p.n) + n0) * ldb * 2 : 0,
+        bbytes);
+    typedef const __attribute__((address_space(4))) int32_t *ConstInts;
+
+    // Copy q of chunk c (A's copies, then B's) into the chunk's LDS place.  Past the last
+    // chunk nothing is read, and the place cleared: so the number of copies under way
+    // is known.
+    auto fetch = [&](int c, uint8_t *to, int q) {
+        const bool of_a = q < CA;
+        const int j = of_a ? q : q - CA;
+        to += of_a ? (wave * CA + j) * 1024 : PA::PLANE + (wave * CB + j) * 1024;
+        if constexpr (FORM == kAdapter) {
+            if (c >= main_chunks && c < chunks) {
+                const int x = c - main_chunks, nth = x / per_seg;
+                const int seg = __builtin_amdgcn_readfirstlane(segs[nth]);
+                const int k0 = (x - nth * per_seg) * KS;
+                if (of_a) {
+                    const int at = k0 + block_a(j) * 8;
+                    const bool mine = tile_list[line_a(j)] == seg && at < p.width;
+                    copy16_to_lds(
+                        range_of(p.hidden, tile.p0 * p.width * 2, p.rows * p.width * 2),
+                        mine ? (line_a(j) * p.width + at) * 2 : kNowhere, 0, to);
+                } else { // the low parts meet the same values
+                    const int at = k0 + block_b(j) * 8, col = at < p.rp ? at : at - p.rp;
+                    copy16_to_lds(range_of(p.up, ((int64_t)seg * p.n + n0) * p.r * 2,
+                                           (int64_t)p.nlist * p.n * p.r * 2),
+                                  at < p.width ? (line_b(j) * p.r + col) * 2 : kNowhere, 0, to);
+                }
+                return;
+            }
+        }
+        const int64_t k0 = (int64_t)c * KS;
+        const int left = (int)min(kdim - k0, (int64_t)KS); // values in the chunk
+        // The range check of a copy subtracts the scalar offset from the range's bytes, so
+        // it may not pass them: inside a row, and a range holds at least one.
+        const int along = left > 0 ? c * KS * 2 : 0;
+        if (of_a) {
+            if constexpr (F::A_ALONG)
+                copy16_to_lds(arange, block_a(j) * 8 < left ? offa[j] : kNowhere, along, to);
+            else
+                copy16_to_lds(range_of(p.a, ((tile.p0 + k0) * lda + m0) * 2, abytes),
+                              line_a(j) < left ? offa[j] : kNowhere, 0, to);
+        } else if constexpr (F::B_ALONG) {
+            copy16_to_lds(brange, block_b(j) * 8 < left ? offb[j] : kNowhere, along, to);
+        } else if (FORM == kGradient && p.order) {
+            // a wave's lines follow each other, so their slots are scalar loads, whose
+            // wait does not hold the copies under way
+            const ConstInts slots = (ConstInts)(uintptr_t)(p.order);
+            uint32_t at = kNowhere;
+#pragma unroll
+            for (int l = 0; l < LB; ++l) {
+                const int line = (wave * CB + j) * LB + l;
+                const int32_t slot = line < left ? slots[tile.p0 + k0 + line] : -1;
+                const uint32_t row = slot >= 0 ? p.k.div((uint32_t)slot) : 0x7FFFFFFFu;
+                const uint32_t byte =
+                    row < (uint64_t)p.arows ? row * (uint32_t)(ldb * 2) : kNowhere;
+                at = lane / PB::BLOCKS == l ? byte : at;
+            }
+            copy16_to_lds(range_of(p.b, (int64_t)n0 * 2, bbytes),
+                          at == kNowhere ? at : at + offb[j], 0, to);
+        } else {
+            const int64_t row = FORM == kGradient ? tile.p0 + k0
+                                                  : (int64_t)max(tile.e, 0) * p.kdim + k0;
+            copy16_to_lds(range_of(p.b, (row * ldb + n0) * 2, bbytes),
+                          line_b(j) < left ? offb[j] : kNowhere, 0, to);
+        }
+    };
+    auto place = [&](auto i) -> uint8_t * {
+        constexpr int I = decltype(i)::value % STAGES;
+        if constexpr (I == 0)
+            return stage0;
+        else if constexpr (I == 1)
+            return stage1;
+        else if constexpr (I == 2)
+            return stage2;
+        else
+            return stage3;
+    };
+    constexpr std::integral_constant<int, 0> i0{};
+    constexpr std::integral_constant<int, 1> i1{};
+    constexpr std::integral_constant<int, 2> i2{};
+    constexpr std::integral_constant<int, 3> i3{};
+
+    if constexpr (FORM == kAdapter) {
+        find_lists<TM, THREADS>(p, tile, tile_list, segs);
+        chunks += segs[TM] * per_seg;
+    }
+#pragma unroll
+    for (int q = 0; q < CA + CB; ++q)
+        fetch(0, place(i0), q);
+    if constexpr (STAGES > 2)
+#pragma unroll
+        for (int q = 0; q < CA + CB; ++q)
+            fetch(1, place(i1), q);
+    if constexpr (STAGES > 3)
+#pragma unroll
+        for (int q = 0; q < CA + CB; ++q)
+            fetch(2, place(i2), q);
+
+    f32x16 acc[WM][WN];
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                acc[i][j][q] = 0.f;
+    Reader<F::A_ALONG, TM, KS, WM, false> reada;
+    Reader<F::B_ALONG, TN, KS, WN, PAIR> readb;
+    reada.init(wm * WM * 32);
+    readb.init(wn * WN * 32);
+    struct Operands {
+        s16x8 a[WM], b[WN];
+    } o[2];
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+        o[1].a[i] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < WN; ++j)
+        o[1].b[j] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+    // operand number q of step s: a[0], then b, then the rest of a, as the products take them
+    auto read = [&](const uint8_t *from, int s, Operands &to, int q) {
+        if (q == 0)
+            to.a[0] = reada.read(from, 0, s);
+        else if (q <= WN)
+            to.b[q - 1] = readb.read(from + PA::PLANE, q - 1, s);
+        else
+            to.a[q - WN] = reada.read(from, q - WN, s);
+    };
+    constexpr int STEPS = KS / 16, PRODUCTS = WM * WN, READS = WM + WN, COPIES = CA + CB;
+    static_assert(STEPS % 2 == 0, "the last step's operands lie in o[1]");
+    constexpr int PARTS = STAGES == 2 ? STEPS / 2 : STEPS; // steps that issue copies
+    // how many of `count` things are issued before product m
+    auto before = [](int count, int m) { return (count * m + PRODUCTS - 1) / PRODUCTS; };
+    // Chunk c in stage i: a step's products, the last chunk's last step first, with the
+    // reads of the next step's operands and the copies of the chunk STAGES - 1 ahead
+    // (to where the chunk before lay) issued between them: issued together they would
+    // keep a wave from its products while the others issue theirs.
+    auto chunk = [&](auto i, int c) {
+        constexpr int I = decltype(i)::value;
+        const uint8_t *now = place(i);
+        uint8_t *ahead = place(std::integral_constant<int, I + STAGES - 1>{});
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const Operands &x = o[(s + 1) & 1];
+            const int c0 = COPIES * min(s, PARTS) / PARTS, c1 = COPIES * min(s + 1, PARTS) / PARTS;
+#pragma unroll
+            for (int m = 0; m < PRODUCTS; ++m) {
+                const int bi = m / WN, bj = m % WN;
+                acc[bi][bj] = PAIR ? mfma16<T>(x.b[bj], x.a[bi], acc[bi][bj])
+                                   : mfma16<T>(x.a[bi], x.b[bj], acc[bi][bj]);
+#pragma unroll
+                for (int q = before(READS, m); q < before(READS, m + 1); ++q)
+                    read(now, s, o[s & 1], q);
+#pragma unroll
+                for (int q = c0 + before(c1 - c0, m); q < c0 + before(c1 - c0, m + 1); ++q)
+                    fetch(c + STAGES - 1, ahead, q);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        wait_vm<(STAGES - 2) * (CA + CB)>(); // the next chunk
+        lds_barrier(); // every wave's part of it is here, and this one's last reads done
+    };
+    if (chunks > 0) {
+        wait_vm<(STAGES - 2) * (CA + CB)>();
+        lds_barrier();
+        for (int c = 0; c < chunks; c += STAGES) {
+            chunk(i0, c);
+            chunk(i1, c + 1);
+            if constexpr (STAGES > 2)
+                chunk(i2, c + 2);
+            if constexpr (STAGES > 3)
+                chunk(i3, c + 3);
+        }
+#pragma unroll
+        for (int m = 0; m < PRODUCTS; ++m) {
+            const int bi = m / WN, bj = m % WN;
+            acc[bi][bj] = PAIR ? mfma16<T>(o[1].b[bj], o[1].a[bi], acc[bi][bj])
+                               : mfma16<T>(o[1].a[bi], o[1].b[bj], acc[bi][bj]);
+        }
+    }
+    wait_vm<0>(); // no copy is under way to where results may go, or past the end
+
+    const int r = lane & 31, half = lane >> 5;
+    const int64_t row_base = FORM == kGradient ? (int64_t)tile.e * p.m + m0 : tile.p0;
+    const int64_t row_end = FORM == kGradient ? (int64_t)(tile.e + 1) * p.m : tile.p1;
+    TO *out = static_cast<TO *>(p.out);
+    if constexpr (PAIR) {
+        // Through LDS, a wave's own part of a stage, so that a store covers whole rows of
+        // its columns.
+        typedef TO T8 __attribute__((ext_vector_type(8)));
+        typedef TO T8U __attribute__((ext_vector_type(8), aligned(sizeof(TO))));
+        constexpr int BR = WN * 4, ROWB = BR * 16, PART = STAGE / WAVES / 16 * 16;
+        constexpr int SLAB = PART / (32 * ROWB) < WM ? PART / (32 * ROWB) : WM;
+        static_assert(SLAB >= 1 && WM % SLAB == 0, "rows through LDS");
+        lds_barrier();
+        uint8_t *mine = stage0 + wave * PART;
+#pragma unroll
+        for (int b0 = 0; b0 < WM; b0 += SLAB) {
+#pragma unroll
+            for (int i = 0; i < SLAB; ++i)
+#pragma unroll
+                for (int j = 0; j < WN; ++j)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        T8 v;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = (TO)acc[b0 + i][j][q * 8 + e];
+                        const int b = (j * 4 + q * 2 + half) ^ (r & (BR - 1));
+                        *reinterpret_cast<T8 *>(mine + (i * 32 + r) * ROWB + b * 16) = v;
+                    }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int k = 0; k < SLAB * 32 * BR / 64; ++k) {
+                const int line = (k * 64 + lane) / BR, b = lane % BR;
+                const T8 v = *reinterpret_cast<const T8 *>(mine + line * ROWB +
+                                                           (b ^ (line & (BR - 1))) * 16);
+                const int64_t row = row_base + (wm * WM + b0) * 32 + line;
+                const int n = n0 + wn * WN * 32 + b * 8;
+                if (row >= row_end || n >= p.n)
+                    continue;
+                TO *to = out + row * p.n + n;
+                if (n + 8 <= p.n) {
+                    *reinterpret_cast<T8U *>(to) = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (n + e < p.n)
+                            to[e] = v[e];
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < WN; ++j) {
+            const int n = n0 + (wn * WN + j) * 32 + r;
+            if (n >= p.n)
+                continue;
+#pragma unroll
+            for (int i = 0; i < WM; ++i)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const int64_t row =
+                        row_base + (wm * WM + i) * 32 + (q >> 2) * 8 + half * 4 + (q & 3);
+                    if (row < row_end)
+                        out[row * p.n + n] = (TO)acc[i][j][q];
+                }
+        }
+    }
+}
+
+// Whether the copies can read a product's operands: 16-byte blocks of rows that are
+// multiples of 16 bytes, ranges of less than 2^31 bytes.
+template <int FORM>
+bool copies_fit(const ListJob &p)
+{
+    auto whole = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+    const int64_t lda = FormOf<FORM>::A_ALONG ? p.kdim : p.m;
+    const int64_t ldb = FormOf<FORM>::B_ALONG ? p.kdim : p.n;
+    const int64_t most = (int64_t)0x7FFFFFFF - (1 << 22);
+    const bool gathers = FORM != kAdapter && p.order;
+    const int64_t gathered = gathers ? p.arows * (FORM == kGradient ? ldb : lda) * 2 : 0;
+    return whole(p.a) && whole(p.b) && lda % 8 == 0 && ldb % 8 == 0 &&
+           std::max(lda, ldb) * 2 * 256 < most && gathered < most &&
+           (FORM != kAdapter || (whole(p.up) && p.r % 8 == 0));
+}
+
+template <typename T, typename TO, int FORM, int KS, int STAGES, int WM, int WN, int MW, int NW>
+hipError_t launch_copies(ListJob p, hipStream_t stream)
+{
+    constexpr int TM = 32 * WM * MW, TN = 32 * WN * NW, THREADS = 64 * MW * NW;
+    p.nt = (uint32_t)((p.n + TN - 1) / TN);
+    int64_t mt;
+    if (FORM == kGradient) {
+        p.mt = (uint32_t)((p.m + TM - 1) / TM);
+        mt = (int64_t)p.mt * p.nlist;
+    } else if (FORM == kAdapter) {
+        mt = (p.rows + TM - 1) / TM;
+    } else {
+        p.by_row = slots_by_row(p.rows, p.nlist, TM);
+        mt = tile_slots(p.rows, p.nlist, TM);
+    }
+    TileGroups g;
+    g.mt = mt;
+    g.nt = p.nt;
+    // 32 tiles a group, more if there are enough groups (8192 x 8192 x 8192: 4 x 16 tiles
+    // a group 1027 us, 2 rows of 32 tiles 1135; 8 or 16 rows of tiles are no better)
+    g.high = 4;
+    g.wide = 8;
+    auto count = [&](int64_t high, int64_t wide) {
+        return (mt + high - 1) / high * ((p.nt + wide - 1) / wide);
+    };
+    while (g.high > 1 && count(g.high, g.wide) < 8)
+        g.high /= 2;
+    while (g.wide > 1 && count(g.high, g.wide) < 8)
+        g.wide /= 2;
+    while (g.wide < p.nt && count(g.high, 2 * g.wide) >= 64)
+        g.wide *= 2;
+    g.across = (p.nt + g.wide - 1) / g.wide;
+    const int64_t blocks = (count(g.high, g.wide) + 7) / 8 * 8 * g.high * g.wide;
+    const int64_t most = most_blocks(THREADS);
+    for (int64_t b = 0; b < blocks; b += most) {
+        p.block0 = b;
+        hipLaunchKernelGGL((list_copy_kernel<T, TO, FORM, KS, STAGES, WM, WN, MW, NW>),
+                           dim3((unsigned)(blocks - b < most ? blocks - b : most)), dim3(THREADS),
+                           0, stream, p, g);
+    }
+    return hipGetLastError();
 }
 
 template <typename T, typename TO, int FORM, int KS, int WM, int WN, int MW, int NW>
