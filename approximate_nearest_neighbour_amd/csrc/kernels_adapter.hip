@@ -11,6 +11,7 @@
 // and multiplied with the same up matrix twice: rounded once more to 16 bits they
 // would add an error as large as the result's own rounding.  float32 hidden
 // rows are float32.
+#include "list_direct.hpp"
 #include "list_tiles.hpp"
 
 namespace ivfpq {
@@ -20,7 +21,7 @@ static int hidden_part(int r) { return (r + 7) / 8 * 8; }
 template <typename T>
 static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
 {
-    constexpr int KS = std::is_same<T, float>::value ? 32 : 64;
+    constexpr int KS = std::is_same<T, float>::value ? 16 : 32;
     ListJob p;
     p.a = q.x;
     p.rows = p.arows = q.t;
@@ -38,11 +39,22 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
     p.row_list = reinterpret_cast<int32_t *>(static_cast<T *>(q.ws) + q.t * p.width);
     p.b = q.down;
     p.n = q.r;
-    if (hipError_t e = launch_tiles<T, float, kHidden, KS, 2, 1, 2, 2>(p, stream))
+    const bool tiny = p.arows * p.kdim < 8 || (int64_t)p.nlist * p.r * p.kdim < 8;
+    if (hipError_t e = tiny ? launch_tiles<T, float, kHidden, 32, 2, 1, 2, 2>(p, stream)
+                            : launch_direct<T, kHidden, 2, 8>(p, stream))
         return e;
     p.b = q.w;
     p.n = q.n;
     p.out = q.out;
+    if (p.rows <= 64 && !(p.arows * p.kdim < 8 || (int64_t)p.n * p.kdim < 8 ||
+                          (int64_t)p.nlist * p.n * p.r < 8)) {
+        if (p.rows <= 16)
+            return launch_direct<T, kAdapter, 1, 8>(p, stream);
+        if (p.rows <= 32 || sizeof(T) == 4)
+            return launch_direct<T, kAdapter, 2, 8>(p, stream);
+        if constexpr (sizeof(T) == 2)
+            return launch_direct<T, kAdapter, 4, 4>(p, stream);
+    }
     if constexpr (sizeof(T) == 2)
         if (copies_fit<kAdapter>(p))
             return launch_copies<T, T, kAdapter, 64, 2, 4, 2, 2, 4>(p, stream);

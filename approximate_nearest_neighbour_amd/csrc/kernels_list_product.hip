@@ -1,5 +1,6 @@
 // Products of rows sorted by list with their list's own matrix, and the gradient of
 // the matrices.
+#include "list_direct.hpp"
 #include "list_tiles.hpp"
 
 namespace ivfpq {
@@ -7,12 +8,19 @@ namespace ivfpq {
 template <typename T, int FORM>
 static hipError_t rows_as(const ListJob &p, hipStream_t stream)
 {
+    if constexpr (FORM == kRowsAlong) {
+        if (p.rows <= 16 * p.nlist && !(p.arows * p.kdim < 8 || (int64_t)p.nlist * p.n * p.kdim < 8)) {
+            if (p.rows <= 8 * p.nlist)
+                return launch_direct<T, kRowsAlong, 1, 4>(p, stream);
+            return launch_direct<T, kRowsAlong, 2, 4>(p, stream);
+        }
+    }
     if constexpr (std::is_same<T, float>::value)
-        return launch_tiles<T, T, FORM, 32, 2, 2, 2, 2>(p, stream);
+        return launch_tiles<T, T, FORM, 16, 2, 2, 2, 2>(p, stream);
     else if (copies_fit<FORM>(p))
         return launch_copies<T, T, FORM, 64, 2, 4, 2, 2, 4>(p, stream);
     else
-        return launch_tiles<T, T, FORM, 64, 2, 2, 2, 2>(p, stream);
+        return launch_tiles<T, T, FORM, 32, 2, 2, 2, 2>(p, stream);
 }
 
 template <typename T>
@@ -48,7 +56,8 @@ static hipError_t gradient_as(const ListJob &p, hipStream_t stream)
     if constexpr (sizeof(T) == 2)
         if (copies_fit<kGradient>(p))
             return launch_copies<T, TO, kGradient, 64, 2, 4, 2, 2, 4>(p, stream);
-    return launch_tiles<T, TO, kGradient, 32, 2, 2, 2, 2>(p, stream);
+    constexpr int KS = std::is_same<T, float>::value ? 16 : 32;
+    return launch_tiles<T, TO, kGradient, KS, 2, 2, 2, 2>(p, stream);
 }
 
 template <typename T>

@@ -224,6 +224,103 @@ __global__ __launch_bounds__(64 * WAVES) void route_scatter_kernel(SortPass s)
     }
 }
 
+// The same sort of up to kSoloSlots slots of any number of lists: one workgroup, as many
+// passes of 8 bits as the lists' numbers have, keys and slots in LDS between them.
+// 1000 slots of 5003 lists: SOLOFIG.
+constexpr int kDigitBins = 256;
+
+__global__ __launch_bounds__(1024) void route_solo_kernel(SortPass s)
+{
+    constexpr int WAVES = 16, ROUNDS = kSoloSlots / (64 * WAVES);
+    __shared__ uint32_t keys[kSoloSlots];
+    __shared__ uint16_t slots[kSoloSlots];
+    __shared__ uint32_t at[WAVES][kDigitBins];
+    __shared__ uint32_t sums[kDigitBins / 64];
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t part = (s.n + WAVES - 1) / WAVES;
+    const uint32_t first = min(wave * part, s.n), end = min(first + part, s.n);
+    const int rounds = (int)((end - first + 63) / 64);
+    uint32_t key[ROUNDS], slot[ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        slot[r] = first + r * 64 + lane;
+        key[r] = slot[r] < end ? list_key(s.lists, slot[r], s.nlist) : 0;
+    }
+    for (uint32_t shift = 0; s.nlist >> shift; shift += 8) {
+        for (uint32_t b = threadIdx.x; b < WAVES * kDigitBins; b += 1024)
+            (&at[0][0])[b] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+            if (first + r * 64 + lane < end)
+                atomicAdd(&at[wave][(key[r] >> shift) & (kDigitBins - 1)], 1u);
+        __syncthreads();
+        // a thread a digit: exclusive sums over the digits, then over the waves
+        uint32_t mine = 0, upto = 0;
+        if (threadIdx.x < kDigitBins) {
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w)
+                mine += at[w][threadIdx.x];
+            upto = wave_inclusive_sum(mine);
+            if (lane == 63)
+                sums[wave] = upto;
+        }
+        __syncthreads();
+        if (threadIdx.x < kDigitBins) {
+            uint32_t p = upto - mine;
+            for (int w = 0; w < wave; ++w)
+                p += sums[w];
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) {
+                const uint32_t c = at[w][threadIdx.x];
+                at[w][threadIdx.x] = p;
+                p += c;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            if (r < rounds) {
+                const bool live = first + r * 64 + lane < end;
+                const uint32_t bin = (key[r] >> shift) & (kDigitBins - 1);
+                uint64_t same = __ballot(live);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const uint64_t m = __ballot((bin >> q) & 1);
+                    same &= (bin >> q) & 1 ? m : ~m;
+                }
+                if (live) {
+                    const uint32_t p =
+                        at[wave][bin] + (uint32_t)__popcll(same & ((1ull << lane) - 1));
+                    keys[p] = key[r];
+                    slots[p] = (uint16_t)slot[r];
+                    if ((same >> lane) == 1)
+                        at[wave][bin] = p + 1;
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); // the cursors
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            const uint32_t i = first + r * 64 + lane;
+            key[r] = i < end ? keys[i] : 0;
+            slot[r] = i < end ? slots[i] : 0;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const uint32_t p = first + r * 64 + lane;
+        if (p < end) {
+            const bool kept = key[r] < s.nlist;
+            s.key_out[p] = key[r];
+            s.order[p] = kept ? (int32_t)slot[r] : -1;
+            s.pos[slot[r]] = kept ? (int32_t)p : -1;
+        }
+    }
+}
+
 // List starts of a sort of more than one pass: offsets[l] = keys below l.
 __global__ __launch_bounds__(256) void route_bounds_kernel(const uint32_t *__restrict__ keys,
                                                            uint32_t n, uint32_t nlist,
@@ -257,7 +354,7 @@ size_t route_sort_bytes(int64_t n, int nlist)
     const size_t blocks = sort_blocks(n);
     const size_t bins = nlist < kSortBins ? (size_t)nlist + 1 : (size_t)kSortBins;
     size_t b = (bins * blocks + bins) * 4;
-    if (nlist >= kSortBins)
+    if (nlist >= kSortBins || n <= kSoloSlots)
         b += (size_t)n * 4 * 3; // keys and slots after the first pass, keys after the second
     return b;
 }
@@ -286,6 +383,15 @@ hipError_t launch_route_sort(const int32_t *lists, int64_t n, int nlist, void *w
         s.offsets = offsets;
         hipLaunchKernelGGL((route_scatter_kernel<16, kSoloBins, true>), dim3(1), dim3(1024), 0,
                            stream, s);
+        return hipGetLastError();
+    }
+    if (n <= kSoloSlots) { // more lists than the one-launch sort has counters for
+        s.order = order;
+        s.pos = pos;
+        s.key_out = sorted;
+        hipLaunchKernelGGL(route_solo_kernel, dim3(1), dim3(1024), 0, stream, s);
+        hipLaunchKernelGGL(route_bounds_kernel, dim3((unsigned)nlist / 256 + 1), dim3(256), 0,
+                           stream, sorted, (uint32_t)n, (uint32_t)nlist, offsets);
         return hipGetLastError();
     }
     for (int pass = 0; pass < (two ? 2 : 1); ++pass) {

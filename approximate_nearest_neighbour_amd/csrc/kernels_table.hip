@@ -89,45 +89,119 @@ hipError_t launch_table_lookup(const void *table, int type, int64_t rows, int d,
 // gradient of the table
 // ---------------------------------------------------------------------------
 
-// The sum of sorted rows [lo, hi), eight values of columns c on a lane, in ascending
-// order in float32; kSumRows of them under way together.
+// Eight columns of a row of d: four from c[0] on and four from c[1] on, where the lanes
+// that share a row have the first fours side by side, then the second ones, so that
+// loads and stores of either type are of whole lines.
+struct Columns {
+    int c[2];
+    __device__ __forceinline__ Columns(int first, int lane, int lanes)
+        : c{first + lane * 4, first + (lanes + lane) * 4}
+    {
+    }
+};
+
+// Sums of rows.  Several rows are loaded together, and no load has a branch of its own
+// (row 0 or a column inside stands for what is not there, and is dropped), or each
+// would be waited for before the next.
 constexpr int kSumRows = 8;
 
 template <typename T>
 struct RowSum {
-    static constexpr int N = Piece<T>::N, Q = 8 / N;
-    float v[8];
+    typedef T V __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+    float v[2][4];
+
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = 0.f;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[h][e] = 0.f;
     }
-    __device__ __forceinline__ void add_rows(const T *grad, int64_t nvec, FastDiv k, int d, int c,
-                                             const int32_t *order, int64_t lo, int64_t hi)
+    struct Batch {
+        T x[kSumRows][2][4];
+        bool live[kSumRows];
+    };
+    // rows t[i] of grad [nvec][d], -1: none
+    __device__ __forceinline__ static void load(Batch &b, const T *grad, int64_t nvec, int d,
+                                                Columns at, const int (&t)[kSumRows])
+    {
+        const T *from[kSumRows];
+#pragma unroll
+        for (int i = 0; i < kSumRows; ++i) {
+            b.live[i] = (uint32_t)t[i] < (uint64_t)nvec;
+            from[i] = grad + (int64_t)(b.live[i] ? t[i] : 0) * d;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (at.c[h] + 4 <= d) {
+#pragma unroll
+                for (int i = 0; i < kSumRows; ++i) {
+                    const V w = *reinterpret_cast<const V *>(from[i] + at.c[h]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        b.x[i][h][e] = w[e];
+                }
+            } else { // the row's end: values past it are not stored
+#pragma unroll
+                for (int i = 0; i < kSumRows; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        b.x[i][h][e] = from[i][min(at.c[h] + e, d - 1)];
+            }
+        }
+    }
+    __device__ __forceinline__ void add(const Batch &b, int i)
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[h][e] = b.live[i] ? v[h][e] + (float)b.x[i][h][e] : v[h][e];
+    }
+    // sorted rows [lo, hi), ascending in float32
+    __device__ __forceinline__ void add_rows(const T *grad, int64_t nvec, FastDiv k, int d,
+                                             Columns at, const int32_t *order, int64_t lo,
+                                             int64_t hi)
     {
         for (int64_t p = lo; p < hi; p += kSumRows) {
-            int64_t t[kSumRows];
+            int t[kSumRows];
 #pragma unroll
-            for (int i = 0; i < kSumRows; ++i) {
-                const int32_t u = p + i < hi ? order[p + i] : -1;
-                t[i] = u >= 0 ? (int64_t)k.div((uint32_t)u) : -1;
+            for (int i = 0; i < kSumRows; ++i)
+                t[i] = order[min(p + i, hi - 1)];
+#pragma unroll
+            for (int i = 0; i < kSumRows; ++i)
+                t[i] = p + i < hi && t[i] >= 0 ? (int)k.div((uint32_t)t[i]) : -1;
+            Batch b;
+            load(b, grad, nvec, d, at, t);
+#pragma unroll
+            for (int i = 0; i < kSumRows; ++i)
+                add(b, i);
+        }
+    }
+    // times scale to a row of d values
+    // NT: past the caches, for rows that nothing reads soon
+    template <bool NT = false, typename TO>
+    __device__ __forceinline__ void store(TO *row, int d, Columns at, float scale) const
+    {
+        typedef TO W __attribute__((ext_vector_type(4), aligned(sizeof(TO))));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (at.c[h] + 4 <= d) {
+                W w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = (TO)(v[h][e] * scale);
+                if constexpr (NT)
+                    __builtin_nontemporal_store(w, reinterpret_cast<W *>(row + at.c[h]));
+                else
+                    *reinterpret_cast<W *>(row + at.c[h]) = w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (at.c[h] + e < d)
+                        row[at.c[h] + e] = (TO)(v[h][e] * scale);
             }
-            Piece<T> r[kSumRows][Q];
-#pragma unroll
-            for (int i = 0; i < kSumRows; ++i)
-#pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    if ((uint64_t)t[i] < (uint64_t)nvec)
-                        r[i][q].load(grad + t[i] * d + c + q * N, d - c - q * N);
-                    else
-                        r[i][q].zero();
-                }
-#pragma unroll
-            for (int i = 0; i < kSumRows; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] += r[i][e / N].v[e % N];
         }
     }
 };
@@ -160,79 +234,177 @@ __global__ __launch_bounds__(256) void table_span_kernel(TableGrad g, int64_t wa
         return;
     const int strips = (g.d + 511) / 512;
     const int64_t which = id / strips;
-    const int c = (int)(id % strips) * 512 + lane * 8;
+    const Columns at((int)(id % strips) * 512, lane, 64);
     const int64_t from = which / 2 * g.span, to = min(from + g.span, g.n);
-    const int64_t at = which & 1 ? to - 1 : from;
-    // the list of slot `at`: the last that begins at or before it
+    const int64_t slot = which & 1 ? to - 1 : from;
+    // the list of `slot`: the last that begins at or before it
     auto begin = [&](int64_t e) { return part_begin(g.offsets, g.nlist, g.n, (int)e + 1); };
     int64_t first = 0, count = g.nlist;
     while (count > 1) {
         const int64_t step = (count + 63) / 64, i = first + lane * step;
-        const uint64_t m = __ballot(i < first + count && begin(i) <= at);
+        const uint64_t m = __ballot(i < first + count && begin(i) <= slot);
         const int who = m ? 63 - __builtin_clzll(m) : 0;
         first += who * step;
         count = min(count - who * step, step);
     }
     const int64_t lo = begin(first), hi = begin(first + 1);
-    if (at < lo || at >= hi || hi - lo <= g.span || (which & 1 && lo <= from))
+    if (slot < lo || slot >= hi || hi - lo <= g.span || (which & 1 && lo <= from))
         return; // of no list, of a short one, or of the list that the first slot has
-    if (c >= g.d)
-        return;
+    const T *grad = static_cast<const T *>(g.grad);
+    const int64_t p0 = max(lo, from), p1 = min(hi, to);
     RowSum<T> s;
     s.clear();
-    s.add_rows(static_cast<const T *>(g.grad), g.nvec, g.k, g.d, c, g.order, max(lo, from),
-               min(hi, to));
-    float *part = g.part + which * g.d + c;
+    for (int64_t base = p0; base < p1; base += 64) { // 64 slots a load
+        const int n = (int)min(p1 - base, (int64_t)64);
+        const int mine = lane < n ? g.order[base + lane] : -1;
+        const int row = mine >= 0 ? (int)g.k.div((uint32_t)mine) : -1;
+        for (int first = 0; first < n; first += kSumRows) {
+            int t[kSumRows];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (c + e < g.d)
-            part[e] = s.v[e];
+            for (int i = 0; i < kSumRows; ++i)
+                t[i] = __builtin_amdgcn_readlane(row, first + i);
+            typename RowSum<T>::Batch b;
+            RowSum<T>::load(b, grad, g.nvec, g.d, at, t);
+#pragma unroll
+            for (int i = 0; i < kSumRows; ++i)
+                s.add(b, i);
+        }
+    }
+    s.store(g.part + which * g.d, g.d, at, 1.f);
+}
+
+// The joined sums of a long list's spans, ascending, added to s.
+template <typename T>
+__device__ __forceinline__ void add_spans(RowSum<T> &s, const TableGrad &g, int64_t lo, int64_t hi,
+                                          Columns at)
+{
+    // the first span may be the one whose last slot's list this is
+    const int64_t i0 = lo / g.span, i1 = (hi + g.span - 1) / g.span;
+    for (int64_t i = i0; i < i1; i += kSumRows) {
+        int t[kSumRows];
+#pragma unroll
+        for (int j = 0; j < kSumRows; ++j)
+            t[j] = i + j < i1 ? (int)(2 * (i + j) + (lo > (i + j) * g.span ? 1 : 0)) : -1;
+        typename RowSum<float>::Batch b;
+        RowSum<float>::load(b, g.part, 2 * i1, g.d, at, t);
+#pragma unroll
+        for (int j = 0; j < kSumRows; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s.v[h][e] = b.live[j] ? s.v[h][e] + b.x[j][h][e] : s.v[h][e];
+    }
 }
 
 // Row l of the table's gradient: zero for an empty list, the sum of a short one's rows,
-// the joined sums of a long one, ascending.  A group of lanes a row and strip.
+// the joined sums of a long one.  A group of lanes a row: for rows of at most 256
+// values.
 template <typename T, typename TO>
 __global__ __launch_bounds__(256) void table_grad_kernel(TableGrad g, int64_t groups, int64_t group0)
 {
-    const int64_t id = group0 + (int64_t)blockIdx.x * (256 / g.lanes) + threadIdx.x / g.lanes;
-    if (id >= groups)
+    const int64_t l = group0 + (int64_t)blockIdx.x * (256 / g.lanes) + threadIdx.x / g.lanes;
+    if (l >= groups)
         return;
-    const int64_t l = id / g.strips;
-    const int c = ((int)(id % g.strips) * g.lanes + (threadIdx.x & (g.lanes - 1))) * 8;
-    if (c >= g.d)
-        return;
+    const Columns at(0, threadIdx.x & (g.lanes - 1), g.lanes);
     const int64_t lo = part_begin(g.offsets, g.nlist, g.n, (int)l + 1);
     const int64_t hi = part_begin(g.offsets, g.nlist, g.n, (int)l + 2);
     RowSum<T> s;
     s.clear();
-    if (hi - lo <= g.span) {
-        s.add_rows(static_cast<const T *>(g.grad), g.nvec, g.k, g.d, c, g.order, lo, hi);
-    } else {
-        for (int64_t i = lo / g.span; i * g.span < hi; ++i) {
-            const float *part = g.part + (2 * i + (lo > i * g.span ? 1 : 0)) * g.d + c;
+    if (hi - lo <= g.span)
+        s.add_rows(static_cast<const T *>(g.grad), g.nvec, g.k, g.d, at, g.order, lo, hi);
+    else
+        add_spans(s, g, lo, hi, at);
+    s.store(static_cast<TO *>(g.out) + l * g.d, g.d, at, g.scale);
+}
+
+// The same for longer rows: a wave has 512 columns of kTableRows lists in a row.
+// Their offsets are one load, their slots come 64 a load, and the rows eight at a
+// time, whichever lists they belong to, so that short lists wait for memory together;
+// most rows of a large table are empty and only stored.
+constexpr int kTableRows = 16;
+
+template <typename T, typename TO, bool NT>
+__global__ __launch_bounds__(256) void table_grad_wave_kernel(TableGrad g, int64_t waves,
+                                                              int64_t wave0)
+{
+    const int lane = lane_id();
+    const int64_t id = wave0 + (int64_t)blockIdx.x * 4 +
+                       __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if (id >= waves)
+        return;
+    const int64_t l0 = id / g.strips * kTableRows;
+    const Columns cols((int)(id % g.strips) * 512, lane, 64);
+    const int count = (int)min((int64_t)g.nlist - l0, (int64_t)kTableRows);
+    const T *grad = static_cast<const T *>(g.grad);
+    // positions fit 32 bits; lane i: where list l0 + i begins
+    const int begins = (int)part_begin(g.offsets, g.nlist, g.n, (int)(l0 + min(lane, count)) + 1);
+    auto begin_of = [&](int i) { return __builtin_amdgcn_readlane(begins, i); };
+    RowSum<T> s;
+    s.clear();
+    int at = 0; // list that is being summed, its next position and its end
+    int p = 0, end = 0;
+    auto put = [&](int list) {
+        s.template store<NT>(static_cast<TO *>(g.out) + (l0 + list) * g.d, g.d, cols, g.scale);
+        s.clear();
+    };
+    // On to the first list from `at` on that has positions to sum; empty ones are stored,
+    // the positions of long ones passed (those are joined at the end).
+    auto advance = [&] {
+        for (; at < count; ++at) {
+            p = begin_of(at);
+            end = begin_of(at + 1);
+            if (end > p && end - p <= g.span)
+                return;
+            if (end <= p)
+                put(at);
+        }
+    };
+    advance();
+    while (at < count) {
+        // the slots of the next 64 positions, of which eight at a time are taken
+        const int base = p, last = begin_of(count);
+        const int mine = base + lane < last ? g.order[base + lane] : -1;
+        const int row = mine >= 0 ? (int)g.k.div((uint32_t)mine) : -1;
+        while (at < count && p - base < 64 && p >= base) {
+            // p is before the end of its list (and that past `last` only if the offsets do
+            // not ascend), so a turn takes at least one position
+            const int first = p - base, n = min(min(64 - first, kSumRows), max(last, end) - p);
+            int t[kSumRows];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                s.v[e] += c + e < g.d ? part[e] : 0.f;
+            for (int i = 0; i < kSumRows; ++i)
+                t[i] = i < n ? __builtin_amdgcn_readlane(row, min(first + i, 63)) : -1;
+            typename RowSum<T>::Batch b;
+            RowSum<T>::load(b, grad, g.nvec, g.d, cols, t);
+            const int from = p;
+#pragma unroll
+            for (int i = 0; i < kSumRows; ++i) {
+                if (i < n && p == from + i && at < count) { // not past a long list
+                    s.add(b, i);
+                    ++p;
+                    if (p == end) {
+                        put(at++);
+                        advance();
+                    }
+                }
+            }
         }
     }
-    TO *out = static_cast<TO *>(g.out) + l * g.d + c;
-    constexpr int N = Piece<TO>::N;
-#pragma unroll
-    for (int q = 0; q < 8 / N; ++q) {
-        Piece<TO> o;
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            o.v[e] = s.v[q * N + e] * g.scale;
-        o.store(out + q * N, g.d - c - q * N);
+    for (at = 0; at < count; ++at) {
+        const int lo = begin_of(at), hi = begin_of(at + 1);
+        if (hi - lo > g.span) {
+            add_spans(s, g, lo, hi, cols);
+            put(at);
+        }
     }
 }
 
-// Slots of a span: near the square root of all, so that a long list has about as
-// many spans to join as a span has rows.
+// Slots of a span: a quarter of the square root of all: the spans of a long list are summed side by
+// side, their sums one after the other, so a span is the longer wait.
 static int64_t span_of(int64_t n)
 {
-    int64_t s = 32;
-    while (s < 4096 && s * s < n)
+    int64_t s = 64;
+    while (s < 4096 && 16 * s * s < n)
         s *= 2;
     return s;
 }
@@ -256,13 +428,25 @@ static hipError_t table_grad_as(TableGrad g, hipStream_t stream)
                                0, stream, g, waves, b * 4);
     }
     g.lanes = piece_lanes((g.d + 7) / 8);
-    g.strips = (g.d + g.lanes * 8 - 1) / (g.lanes * 8);
-    const int64_t groups = (int64_t)g.nlist * g.strips, per = 256 / g.lanes;
-    const int64_t blocks = (groups + per - 1) / per;
+    g.strips = (g.d + 511) / 512;
+    if (g.lanes == 64) {
+        const int64_t waves = ((int64_t)g.nlist + kTableRows - 1) / kTableRows * g.strips;
+        const int64_t blocks = (waves + 3) / 4;
+        // gradients of half of the last-level cache (256 MB) and more go past it
+        const bool past = (int64_t)g.nlist * g.d * (int64_t)sizeof(TO) >= (int64_t)128 << 20;
+        const auto kernel = past ? table_grad_wave_kernel<T, TO, true>
+                                 : table_grad_wave_kernel<T, TO, false>;
+        for (int64_t b = 0; b < blocks; b += most)
+            hipLaunchKernelGGL(kernel,
+                               dim3((unsigned)(blocks - b < most ? blocks - b : most)), dim3(256),
+                               0, stream, g, waves, b * 4);
+        return hipGetLastError();
+    }
+    const int64_t per = 256 / g.lanes, blocks = (g.nlist + per - 1) / per;
     for (int64_t b = 0; b < blocks; b += most)
         hipLaunchKernelGGL((table_grad_kernel<T, TO>),
                            dim3((unsigned)(blocks - b < most ? blocks - b : most)), dim3(256), 0,
-                           stream, g, groups, b * per);
+                           stream, g, (int64_t)g.nlist, b * per);
     return hipGetLastError();
 }
 

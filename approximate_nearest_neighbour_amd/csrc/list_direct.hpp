@@ -1,0 +1,281 @@
+// Products of few rows: bound by the matrices' bytes, which go from memory straight to
+// registers.
+//
+// A wave forms 16 RT rows by 16 columns with 16 x 16 x 32 matrix instructions; KW of a
+// workgroup's eight waves share the contraction of the same columns out between them
+// and join their sums through LDS, in the waves' order.  The contraction comes in
+// units of 64 values, of which lane group g (16 lanes) has values 16 g to 16 g + 15 of
+// its row: whole lines of memory for 16-bit rows.  Two turns of two units are under
+// way, one of them while the other is multiplied.  Rows may begin at any address.
+//
+// An adapter's hidden rows are multiplied with the up matrices after the shared ones:
+// the lists of the tile's rows are dealt to the KW waves.
+#pragma once
+
+#include "list_tiles.hpp"
+
+namespace ivfpq {
+
+template <typename E>
+__device__ __forceinline__ f32x4 mfma16_small(s16x8 a, s16x8 b, f32x4 c)
+{
+    typedef E V __attribute__((ext_vector_type(8)));
+    if constexpr (std::is_same<E, __bf16>::value)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V, a),
+                                                       __builtin_bit_cast(V, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(V, a),
+                                                      __builtin_bit_cast(V, b), c, 0, 0, 0);
+}
+
+// Operands of the matrix instructions from eight values: the values, or their parts.
+template <typename T>
+__device__ __forceinline__ void operands_of(const Eight<T> &x, s16x8 (&out)[Parts<T>::N])
+{
+    if constexpr (sizeof(T) == 2) {
+        out[0] = __builtin_bit_cast(s16x8, x.v);
+    } else {
+        typename Eight<T>::E8 parts[3];
+        x.split(parts);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+            out[p] = __builtin_bit_cast(s16x8, parts[p]);
+    }
+}
+
+template <typename T, int FORM, int RT, int KW>
+__global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
+{
+    static_assert(FormOf<FORM>::B_ALONG, "rows along the contraction");
+    using E = typename Parts<T>::E;
+    constexpr int NP = Parts<T>::N, TM = 16 * RT, GROUPS = 8 / KW, UNIT = 64, TURN = 2;
+    __shared__ f32x4 part[KW > 1 ? 8 : 1][RT][64];
+    __shared__ int segs[FORM == kAdapter ? TM + 1 : 1];
+    __shared__ int tile_list[FORM == kAdapter ? TM : 1];
+
+    const int lane = lane_id(), r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int64_t block = p.block0 + blockIdx.x;
+    const int64_t mt = block / p.nt;
+    const int cols = FORM == kHidden ? p.r : p.n;
+    const int n0 = ((int)(block - mt * p.nt) * GROUPS + wave / KW) * 16;
+    PartTile tile{0, mt * TM, min(mt * TM + TM, p.rows)};
+    if constexpr (FORM != kAdapter)
+        tile = find_part(p.offsets, p.nlist, p.rows, mt, TM, p.by_row);
+    if (tile.p0 >= tile.p1)
+        return;
+    tile.p0 = uniform(tile.p0);
+    tile.p1 = uniform(tile.p1);
+    const bool listed = FORM == kAdapter || (tile.e >= 0 && tile.e < p.nlist);
+    if (FORM == kHidden && !listed)
+        return;
+
+    f32x4 acc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+        acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int64_t arow[RT]; // rows past the tile's end repeat its last one; they are not stored
+    bool there[RT];
+    if (listed) {
+        const T *a = static_cast<const T *>(p.a), *b = static_cast<const T *>(p.b);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int64_t row = min(tile.p0 + i * 16 + r, tile.p1 - 1);
+            const int64_t from = FORM == kAdapter ? row : source_row(p, row);
+            there[i] = from >= 0;
+            arow[i] = max(from, (int64_t)0) * p.kdim;
+        }
+        const int64_t list = FORM == kAdapter ? 0 : tile.e;
+        const int64_t brow = (list * cols + min(n0 + r, cols - 1)) * p.kdim;
+        struct Turn {
+            Eight<T> a[TURN][2][RT], b[TURN][2];
+        };
+        const int units = (p.kdim + UNIT - 1) / UNIT, whole = p.kdim / UNIT;
+        auto load = [&](Turn &t, int u0) { // units u0 and u0 + KW, whole ones
+#pragma unroll
+            for (int u = 0; u < TURN; ++u) {
+                const int64_t at = (int64_t)min(u0 + u * KW, whole - 1) * UNIT + g * 16;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    t.b[u][h].read(b + brow + at + h * 8);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+                        t.a[u][h][i].read(a + arow[i] + at + h * 8);
+                }
+            }
+        };
+        auto product = [&](const Eight<T> &xa, const Eight<T> &xb, f32x4 &c) {
+            s16x8 oa[NP], ob[NP];
+            operands_of(xa, oa);
+            operands_of(xb, ob);
+#pragma unroll
+            for (int sum = NP - 1; sum >= 0; --sum)
+#pragma unroll
+                for (int q = 0; q <= sum; ++q)
+                    c = mfma16_small<E>(ob[sum - q], oa[q], c);
+        };
+        auto multiply = [&](const Turn &t, int u0) {
+#pragma unroll
+            for (int u = 0; u < TURN; ++u) {
+                if (u0 + u * KW >= whole)
+                    break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+                        product(t.a[u][h][i], t.b[u][h], acc[i]);
+            }
+        };
+        const int first = wave % KW, step = TURN * KW;
+        if (whole > 0) {
+            Turn x, y;
+            load(x, first);
+            for (int u = first; u < whole; u += 2 * step) {
+                load(y, u + step);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(x, u);
+                load(x, u + 2 * step);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(y, u + step);
+            }
+        }
+        if (units > whole && whole % KW == first) { // the rows' end
+            const int64_t all_a = p.arows * p.kdim;
+            const int64_t all_b = (FORM == kAdapter ? 1 : (int64_t)p.nlist) * cols * p.kdim;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int at = whole * UNIT + g * 16 + h * 8;
+                Eight<T> xb, xa[RT];
+                xb.template read_near<false>(b, brow + at, all_b);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    xa[i].template read_near<false>(a, arow[i] + at, all_a);
+                xb.template settle<false>(brow + at, all_b, p.kdim - at);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    xa[i].template settle<false>(arow[i] + at, all_a, p.kdim - at);
+                    product(xa[i], xb, acc[i]);
+                }
+            }
+        }
+        if constexpr (FORM == kAdapter) {
+            find_lists<TM, 512>(p, tile, tile_list, segs);
+            const T *hidden = static_cast<const T *>(p.hidden), *up = static_cast<const T *>(p.up);
+            const int64_t all_up = (int64_t)p.nlist * p.n * p.r;
+            const int count = segs[TM];
+            for (int at0 = 0; at0 < p.width; at0 += 32) { // 32 values a matrix instruction
+                const int at = at0 + g * 8, col = at < p.rp ? at : at - p.rp;
+                for (int s0 = first; s0 < count; s0 += 4 * KW) { // four lists under way
+                    Eight<T> xb[4], xa[4][RT];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const int seg = segs[min(s0 + s * KW, count - 1)];
+                        xb[s].template read_near<false>(
+                            up, ((int64_t)seg * p.n + min(n0 + r, p.n - 1)) * p.r + col, all_up);
+#pragma unroll
+                        for (int i = 0; i < RT; ++i) {
+                            const int64_t row = min(tile.p0 + i * 16 + r, tile.p1 - 1);
+                            xa[s][i].read(hidden + row * p.width + min(at, p.width - 8));
+                        }
+                    }
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        if (s0 + s * KW >= count)
+                            break;
+                        const int seg = segs[s0 + s * KW];
+                        xb[s].template settle<false>(
+                            ((int64_t)seg * p.n + min(n0 + r, p.n - 1)) * p.r + col, all_up,
+                            at < p.width ? p.r - col : 0);
+#pragma unroll
+                        for (int i = 0; i < RT; ++i) {
+                            const bool mine = tile_list[i * 16 + r] == seg && at < p.width;
+                            xa[s][i].template settle<false>(0, 8, mine ? 8 : 0);
+                            product(xa[s][i], xb[s], acc[i]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if constexpr (KW > 1) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+            part[wave][i][lane] = acc[i];
+        __syncthreads();
+        if (wave % KW != 0)
+            return;
+#pragma unroll
+        for (int w = 1; w < KW; ++w)
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                acc[i] += part[wave + w][i][lane];
+    }
+    // result q of a lane: column 4 g + q, row r
+    const int n = n0 + 4 * g;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int64_t row = tile.p0 + i * 16 + r;
+        if (row >= tile.p1)
+            continue;
+        if (listed && !there[i])
+            acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (FORM == kHidden) {
+            const int64_t t = source_row(p, row);
+            if (t < 0)
+                continue;
+            if (n0 == 0 && g == 0)
+                p.row_list[t] = tile.e;
+            const float scale = p.scales ? p.scales[tile.e] : 1.f;
+            T *to = static_cast<T *>(p.hidden) + t * p.width + n;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (n + q >= p.rp)
+                    continue;
+                const float h = n + q < p.r ? acc[i][q] * scale : 0.f;
+                to[q] = (T)h;
+                if constexpr (NP == 1)
+                    to[p.rp + q] = (T)(h - (float)to[q]);
+            }
+        } else {
+            typedef T V __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+            T *out = static_cast<T *>(p.out) + row * p.n + n;
+            if (n + 4 <= p.n) {
+                V v;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    v[q] = (T)acc[i][q];
+                *reinterpret_cast<V *>(out) = v;
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (n + q < p.n)
+                        out[q] = (T)acc[i][q];
+            }
+        }
+    }
+}
+
+template <typename T, int FORM, int RT, int KW>
+hipError_t launch_direct(ListJob p, hipStream_t stream)
+{
+    constexpr int TM = 16 * RT, TN = 16 * 8 / KW;
+    const int cols = FORM == kHidden ? p.rp : p.n;
+    p.nt = (uint32_t)((cols + TN - 1) / TN);
+    int64_t mt;
+    if (FORM == kAdapter) {
+        mt = (p.rows + TM - 1) / TM;
+    } else {
+        p.by_row = slots_by_row(p.rows, p.nlist, TM);
+        mt = tile_slots(p.rows, p.nlist, TM);
+    }
+    const int64_t blocks = mt * p.nt, most = most_blocks(512);
+    for (int64_t b = 0; b < blocks; b += most) {
+        p.block0 = b;
+        hipLaunchKernelGGL((list_direct_kernel<T, FORM, RT, KW>),
+                           dim3((unsigned)(blocks - b < most ? blocks - b : most)), dim3(512), 0,
+                           stream, p);
+    }
+    return hipGetLastError();
+}
+
+} // namespace ivfpq

@@ -177,49 +177,106 @@ struct Reader {
 template <typename T>
 struct Eight {
     static constexpr int Q = sizeof(T) / 2; // 16-byte pieces
-    T v[8];
-    // those past `valid` are zero
-    __device__ __forceinline__ void load(const T *p, int64_t valid)
+    typedef T V __attribute__((ext_vector_type(8 / Q), aligned(sizeof(T))));
+    typedef uint32_t Words __attribute__((ext_vector_type(4 * Q)));
+    Words v;
+
+    __device__ __forceinline__ void read(const T *p)
     {
-        typedef T V __attribute__((ext_vector_type(8 / Q), aligned(sizeof(T))));
-        if (valid >= 8) {
 #pragma unroll
-            for (int h = 0; h < Q; ++h) {
-                const V w = reinterpret_cast<const V *>(p)[h];
+        for (int h = 0; h < Q; ++h) {
+            const u32x4 w = __builtin_bit_cast(u32x4, reinterpret_cast<const V *>(p)[h]);
 #pragma unroll
-                for (int i = 0; i < 8 / Q; ++i)
-                    v[h * (8 / Q) + i] = w[i];
-            }
+            for (int i = 0; i < 4; ++i)
+                v[h * 4 + i] = w[i];
+        }
+    }
+    // The eight values from number `at` of an array of `all` on, in two steps, so that
+    // loads are under way together and no branch waits for one.  Near the array's end
+    // its last eight are read, and moved down when they are stored.  TINY: the array may
+    // have fewer than eight.
+    template <bool TINY>
+    __device__ __forceinline__ void read_near(const T *array, int64_t at, int64_t all)
+    {
+        if constexpr (!TINY) {
+            read(array + min(at, all - 8));
         } else {
+            T x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = i < valid ? p[i] : (T)0.f;
+                x[i] = array[min(at + i, all - 1)];
+#pragma unroll
+            for (int i = 0; i < 4 * Q; ++i) {
+                if constexpr (Q == 1)
+                    v[i] = (uint32_t)__builtin_bit_cast(uint16_t, x[2 * i]) |
+                           (uint32_t)__builtin_bit_cast(uint16_t, x[2 * i + 1]) << 16;
+                else
+                    v[i] = __builtin_bit_cast(uint32_t, x[i]);
+            }
+        }
+    }
+    // ... of which the first `count` are kept, the others zero.
+    template <bool TINY>
+    __device__ __forceinline__ void settle(int64_t at, int64_t all, int count)
+    {
+        if constexpr (!TINY) {
+            const int past = (int)min(at - min(at, all - 8), (int64_t)8);
+            if (__any(past > 0)) {
+#pragma unroll
+                for (int b = 8; b >= 1; b >>= 1) {
+                    const bool move = past & b;
+                    if constexpr (Q == 1) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t up = b == 1 ? (v[i] >> 16 | (i < 3 ? v[(i + 1) & 3] << 16 : 0))
+                                                : i + b / 2 < 4 ? v[(i + b / 2) & 3] : 0u;
+                            v[i] = move ? up : v[i];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[i] = move ? (i + b < 8 ? v[(i + b) & 7] : 0u) : v[i];
+                    }
+                }
+            }
+        }
+        const int n = min(max(count, 0), 8);
+#pragma unroll
+        for (int i = 0; i < 4 * Q; ++i) {
+            if constexpr (Q == 1)
+                v[i] &= n >= 2 * i + 2 ? ~0u : n == 2 * i + 1 ? 0xFFFFu : 0u;
+            else
+                v[i] = i < n ? v[i] : 0u;
+        }
+    }
+    typedef __bf16 E8 __attribute__((ext_vector_type(8)));
+    // float32 values to their three parts
+    __device__ __forceinline__ void split(E8 (&out)[3]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // the largest finite values stay finite in bfloat16
+            const float x = __uint_as_float(v[i]);
+            const __bf16 hi = (__bf16)__builtin_amdgcn_fmed3f(x, -0x1.FEp127f, 0x1.FEp127f);
+            const float r1 = x - (float)hi;
+            const __bf16 mid = (__bf16)r1;
+            out[0][i] = hi;
+            out[1][i] = mid;
+            out[2][i] = (__bf16)(r1 - (float)mid);
         }
     }
     // to the planes at `to`, `plane` bytes apart
     __device__ __forceinline__ void store(uint8_t *to, int plane) const
     {
-        using E = typename Parts<T>::E;
-        typedef E V __attribute__((ext_vector_type(8)));
-        V out[Parts<T>::N];
+        if constexpr (Q == 1) {
+            *reinterpret_cast<Words *>(to) = v;
+        } else {
+            E8 out[3];
+            split(out);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (std::is_same<T, float>::value) {
-                // the largest finite values stay finite in bfloat16
-                const float x = v[i];
-                const E hi = (E)__builtin_amdgcn_fmed3f(x, -0x1.FEp127f, 0x1.FEp127f);
-                const float r1 = x - (float)hi;
-                const E mid = (E)r1;
-                out[0][i] = hi;
-                out[1][i] = mid;
-                out[2][i] = (E)(r1 - (float)mid);
-            } else {
-                out[0][i] = v[i];
-            }
+            for (int p = 0; p < 3; ++p)
+                *reinterpret_cast<E8 *>(to + p * plane) = out[p];
         }
-#pragma unroll
-        for (int p = 0; p < Parts<T>::N; ++p)
-            *reinterpret_cast<V *>(to + p * plane) = out[p];
     }
 };
 
@@ -303,7 +360,7 @@ __device__ __forceinline__ void find_lists(const ListJob &p, const PartTile &til
     lds_barrier();
 }
 
-template <typename T, typename TO, int FORM, int KS, int WM, int WN, int MW, int NW>
+template <typename T, typename TO, int FORM, int KS, int WM, int WN, int MW, int NW, bool TINY>
 __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
 {
     using F = FormOf<FORM>;
@@ -314,7 +371,7 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
     using PA = Place<F::A_ALONG, TM, KS>;
     using PB = Place<F::B_ALONG, TN, KS>;
     constexpr int STAGE = NP * (PA::PLANE + PB::PLANE);
-    __shared__ __align__(16) uint8_t stage[2][STAGE];
+    __shared__ __align__(16) uint8_t stage0[STAGE], stage1[STAGE];
     __shared__ int segs[FORM == kAdapter ? TM + 1 : 1]; // lists of the tile's rows, their number
     __shared__ int tile_list[FORM == kAdapter ? TM : 1];
 
@@ -370,7 +427,6 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
     static_assert(QA * THREADS == PA::LINES * PA::BLOCKS && QB * THREADS == PB::LINES * PB::BLOCKS,
                   "whole pieces a thread");
     const T *a = static_cast<const T *>(p.a), *b = static_cast<const T *>(p.b);
-    Eight<T> ra[QA], rb[QB];
     int64_t arow[F::A_ALONG ? QA : 1];
     if constexpr (F::A_ALONG) {
 #pragma unroll
@@ -379,78 +435,177 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
             arow[j] = row >= tile.p1 ? -1 : F::PER_LIST_ROWS ? source_row(p, row) : row;
         }
     }
-    auto load = [&](int64_t c) {
-        const bool extra = FORM == kAdapter && c >= main_chunks;
-        if (extra) {
-            const int x = (int)(c - main_chunks), seg = segs[x / per_seg];
-            const int k0 = x % per_seg * KS;
-            const T *hidden = static_cast<const T *>(p.hidden);
-            const T *up = static_cast<const T *>(p.up) + (int64_t)seg * p.n * p.r;
-#pragma unroll
-            for (int j = 0; j < QA; ++j) {
-                const int piece = j * THREADS + tid, row = piece / PA::BLOCKS;
-                const int at = k0 + piece % PA::BLOCKS * 8;
-                const bool mine = tile_list[row] == seg;
-                ra[j].load(hidden + (tile.p0 + (mine ? row : 0)) * p.width + at,
-                           mine ? p.width - at : 0);
-            }
+    // kGradient: the slots of the next chunk's rows, a chunk ahead of the rows themselves
+    int32_t slots[FORM == kGradient ? QB : 1];
+    auto load_slots = [&](int64_t c) {
+        if constexpr (FORM == kGradient) {
 #pragma unroll
             for (int j = 0; j < QB; ++j) {
-                const int piece = j * THREADS + tid, row = n0 + piece / PB::BLOCKS;
-                const int at = k0 + piece % PB::BLOCKS * 8;
-                const int col = at < p.rp ? at : at - p.rp; // the low parts meet the same values
-                const bool inside = row < p.n && at < p.width;
-                rb[j].load(up + (int64_t)(inside ? row : 0) * p.r + (inside ? col : 0),
-                           inside ? p.r - col : 0);
-            }
-            return;
-        }
-        const int64_t k0 = c * KS;
-#pragma unroll
-        for (int j = 0; j < QA; ++j) {
-            const int piece = j * THREADS + tid, line = piece / PA::BLOCKS;
-            const int value = piece % PA::BLOCKS * 8;
-            if constexpr (F::A_ALONG) {
-                const bool live = arow[j] >= 0;
-                ra[j].load(a + (live ? arow[j] : 0) * p.kdim + k0 + value,
-                           live ? kdim - k0 - value : 0);
-            } else {
-                const bool live = k0 + line < kdim;
-                ra[j].load(a + (tile.p0 + (live ? k0 + line : 0)) * p.m + m0 + value,
-                           live ? p.m - m0 - value : 0);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < QB; ++j) {
-            const int piece = j * THREADS + tid, line = piece / PB::BLOCKS;
-            const int value = piece % PB::BLOCKS * 8;
-            if constexpr (F::B_ALONG) {
-                const int64_t base = F::PER_LIST_ROWS ? (int64_t)tile.e * p.n : 0;
-                const bool live = n0 + line < p.n;
-                rb[j].load(b + (base + (live ? n0 + line : 0)) * p.kdim + k0 + value,
-                           live ? kdim - k0 - value : 0);
-            } else {
-                int64_t row = k0 + line < kdim ? k0 + line : -1;
-                if constexpr (FORM == kGradient)
-                    row = row >= 0 ? source_row(p, tile.p0 + row) : -1;
-                else
-                    row = row >= 0 ? (int64_t)tile.e * p.kdim + row : -1;
-                rb[j].load(b + (row >= 0 ? row : 0) * p.n + n0 + value,
-                           row >= 0 ? p.n - n0 - value : 0);
+                const int64_t row = tile.p0 + min(c * KS + (j * THREADS + tid) / PB::BLOCKS, kdim - 1);
+                slots[j] = p.order ? p.order[row] : (int32_t)row;
             }
         }
     };
-    auto store = [&](uint8_t *to) {
+    // Whether a chunk has a line's end or a line that is not there (a gather may find no
+    // row); the others are read as they stand.
+    const bool edge_a = F::A_ALONG ? tile.p1 - tile.p0 < TM || (F::PER_LIST_ROWS && p.order)
+                                   : m0 + TM > p.m;
+    const bool edge_b = FORM == kGradient || n0 + TN > p.n;
+
+    // A chunk on its way: read at once, settled (ends, missing lines) when it goes to LDS.
+    struct Chunk {
+        Eight<T> a[QA], b[QB];
+        int64_t at[FORM == kGradient ? QB : 1]; // kGradient: where b's pieces come from
+        int count[FORM == kGradient ? QB : 1];
+    };
+    // of an adapter's chunk: its list and where it begins
+    auto extra_of = [&](int64_t c, int &seg, int &k0) {
+        const int x = (int)(c - main_chunks);
+        seg = segs[x / per_seg];
+        k0 = x % per_seg * KS;
+    };
+    // Where a piece of a chunk begins in its array, and how many of its values there are:
+    // the first chunk's place, and the same step for all pieces.
+    struct Part {
+        int64_t at;
+        int count;
+    };
+    int64_t first_a[QA], first_b[QB];
+#pragma unroll
+    for (int j = 0; j < QA; ++j) {
+        const int piece = j * THREADS + tid, line = piece / PA::BLOCKS;
+        const int value = piece % PA::BLOCKS * 8;
+        if constexpr (F::A_ALONG)
+            first_a[j] = max(arow[j], (int64_t)0) * p.kdim + value;
+        else
+            first_a[j] = (tile.p0 + line) * p.m + m0 + value;
+    }
+#pragma unroll
+    for (int j = 0; j < QB; ++j) {
+        const int piece = j * THREADS + tid, line = piece / PB::BLOCKS;
+        const int value = piece % PB::BLOCKS * 8;
+        const int64_t list = F::PER_LIST_ROWS ? max(tile.e, 0) : 0;
+        if constexpr (F::B_ALONG)
+            first_b[j] = (list * p.n + min(n0 + line, p.n - 1)) * p.kdim + value;
+        else
+            first_b[j] = (list * p.kdim + line) * p.n + n0 + value;
+    }
+    const int64_t step_a = F::A_ALONG ? KS : (int64_t)KS * p.m;
+    const int64_t step_b = F::B_ALONG ? KS : (int64_t)KS * p.n;
+    auto part_a = [&](int64_t c, int j) -> Part {
+        const int piece = j * THREADS + tid, line = piece / PA::BLOCKS;
+        const int left = (int)(kdim - c * KS), value = piece % PA::BLOCKS * 8;
+        if constexpr (F::A_ALONG)
+            return {first_a[j] + c * step_a, arow[j] >= 0 ? left - value : 0};
+        else
+            return {first_a[j] + c * step_a, line < left ? p.m - m0 - value : 0};
+    };
+    auto part_b = [&](int64_t c, int j) -> Part { // all but kGradient
+        const int piece = j * THREADS + tid, line = piece / PB::BLOCKS;
+        const int left = (int)(kdim - c * KS), value = piece % PB::BLOCKS * 8;
+        if constexpr (F::B_ALONG)
+            return {first_b[j] + c * step_b, n0 + line < p.n ? left - value : 0};
+        else
+            return {first_b[j] + c * step_b, line < left ? p.n - n0 - value : 0};
+    };
+    auto extra_a = [&](int seg, int k0, int j) -> Part {
+        const int piece = j * THREADS + tid, row = piece / PA::BLOCKS;
+        const int at = k0 + piece % PA::BLOCKS * 8;
+        const bool mine = tile_list[row] == seg;
+        return {(tile.p0 + (mine ? row : 0)) * p.width + at, mine ? p.width - at : 0};
+    };
+    auto extra_b = [&](int seg, int k0, int j) -> Part {
+        const int piece = j * THREADS + tid, row = n0 + piece / PB::BLOCKS;
+        const int at = k0 + piece % PB::BLOCKS * 8;
+        const int col = at < p.rp ? at : at - p.rp; // the low parts meet the same values
+        return {((int64_t)seg * p.n + min(row, p.n - 1)) * p.r + col,
+                row < p.n && at < p.width ? p.r - col : 0};
+    };
+    const int64_t all_a = F::A_ALONG ? p.arows * p.kdim : p.rows * p.m;
+    const int64_t all_b = FORM == kGradient ? p.arows * p.n
+                                            : (FORM == kAdapter ? 1 : (int64_t)p.nlist) * p.n * p.kdim;
+    const int64_t all_hidden = p.rows * p.width, all_up = (int64_t)p.nlist * p.n * p.r;
+    auto load = [&](Chunk &to, int64_t c) {
+        if (FORM == kAdapter && c >= main_chunks) {
+            int seg, k0;
+            extra_of(c, seg, k0);
+#pragma unroll
+            for (int j = 0; j < QA; ++j)
+                to.a[j].template read_near<TINY>(static_cast<const T *>(p.hidden),
+                                                 extra_a(seg, k0, j).at, all_hidden);
+#pragma unroll
+            for (int j = 0; j < QB; ++j)
+                to.b[j].template read_near<TINY>(static_cast<const T *>(p.up),
+                                                 extra_b(seg, k0, j).at, all_up);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < QA; ++j)
+            to.a[j].template read_near<TINY>(a, part_a(c, j).at, all_a);
+        if constexpr (FORM == kGradient) {
+#pragma unroll
+            for (int j = 0; j < QB; ++j) {
+                const int piece = j * THREADS + tid;
+                const uint32_t q = !p.order ? (uint32_t)slots[j]
+                                   : slots[j] >= 0 ? p.k.div((uint32_t)slots[j]) : ~0u;
+                const bool there =
+                    q < (uint64_t)p.arows && c * KS + piece / PB::BLOCKS < kdim;
+                to.at[j] = (there ? (int64_t)q : 0) * p.n + n0 + piece % PB::BLOCKS * 8;
+                to.count[j] = there ? p.n - n0 - piece % PB::BLOCKS * 8 : 0;
+                to.b[j].template read_near<TINY>(b, to.at[j], all_b);
+            }
+            load_slots(min(c + 1, main_chunks - 1));
+        } else {
+#pragma unroll
+            for (int j = 0; j < QB; ++j)
+                to.b[j].template read_near<TINY>(b, part_b(c, j).at, all_b);
+        }
+    };
+    auto store = [&](Chunk &from, int64_t c, uint8_t *to) {
+        const bool none = c >= chunks, last = (c + 1) * KS > kdim;
+        if (FORM == kAdapter && c >= main_chunks && !none) {
+            int seg, k0;
+            extra_of(c, seg, k0);
+#pragma unroll
+            for (int j = 0; j < QA; ++j) {
+                const Part q = extra_a(seg, k0, j);
+                from.a[j].template settle<TINY>(q.at, all_hidden, q.count);
+            }
+#pragma unroll
+            for (int j = 0; j < QB; ++j) {
+                const Part q = extra_b(seg, k0, j);
+                from.b[j].template settle<TINY>(q.at, all_up, q.count);
+            }
+        } else {
+            if (last || edge_a || TINY) {
+#pragma unroll
+                for (int j = 0; j < QA; ++j) {
+                    const Part q = part_a(c, j);
+                    from.a[j].template settle<TINY>(q.at, all_a, q.count);
+                }
+            }
+            if (last || edge_b || TINY) {
+#pragma unroll
+                for (int j = 0; j < QB; ++j) {
+                    Part q;
+                    if constexpr (FORM == kGradient)
+                        q = {from.at[j], none ? 0 : from.count[j]};
+                    else
+                        q = part_b(c, j);
+                    from.b[j].template settle<TINY>(q.at, all_b, q.count);
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < QA; ++j) {
             const int piece = j * THREADS + tid;
-            ra[j].store(to + PA::at(piece / PA::BLOCKS, piece % PA::BLOCKS), PA::PLANE);
+            from.a[j].store(to + PA::at(piece / PA::BLOCKS, piece % PA::BLOCKS), PA::PLANE);
         }
 #pragma unroll
         for (int j = 0; j < QB; ++j) {
             const int piece = j * THREADS + tid;
-            rb[j].store(to + NP * PA::PLANE + PB::at(piece / PB::BLOCKS, piece % PB::BLOCKS),
-                        PB::PLANE);
+            from.b[j].store(to + NP * PA::PLANE + PB::at(piece / PB::BLOCKS, piece % PB::BLOCKS),
+                            PB::PLANE);
         }
     };
     Reader<F::A_ALONG, TM, KS, WM, false> reada;
@@ -458,19 +613,7 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
     reada.init(wm * WM * 32);
     readb.init(wn * WN * 32);
 
-    if (chunks > 0) {
-        load(0);
-        store(stage[0]);
-    }
-    if (chunks > 1)
-        load(1);
-    lds_barrier();
-    for (int64_t c = 0; c < chunks; ++c) {
-        const uint8_t *now = stage[c & 1];
-        if (c + 1 < chunks)
-            store(stage[(c + 1) & 1]);
-        if (c + 2 < chunks)
-            load(c + 2);
+    auto multiply = [&](const uint8_t *now) {
 #pragma unroll
         for (int s = 0; s < KS / 16; ++s) {
             s16x8 oa[NP][WM], ob[NP][WN];
@@ -495,7 +638,35 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
                             acc[i][j] = PAIR ? mfma16<E>(ob[sum - q][j], oa[q][i], acc[i][j])
                                              : mfma16<E>(oa[q][i], ob[sum - q][j], acc[i][j]);
         }
-        lds_barrier(); // the next chunk is here, and the last reads of this one are done
+    };
+    // Chunk c lies in LDS, c + 1 and c + 2 are on their way in registers: a load has two
+    // chunks' time.  At the end the last chunk is loaded again and stored as zeros, so
+    // that the loads under way are known, and waited for one by one, and so that the
+    // loop has one end (with two the sums would take their registers twice).
+    if (chunks > 0) {
+        const int64_t end = chunks - 1;
+        Chunk x, y;
+        load_slots(0);
+        load(x, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        load(y, min((int64_t)1, end));
+        __builtin_amdgcn_sched_barrier(0);
+        store(x, 0, stage0);
+        load(x, min((int64_t)2, end));
+        __builtin_amdgcn_sched_barrier(0);
+        lds_barrier();
+        for (int64_t c = 0; c <= end; c += 2) {
+            store(y, c + 1, stage1);
+            load(y, min(c + 3, end));
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(stage0);
+            lds_barrier(); // the next chunk is here, and the last reads of this one are done
+            store(x, c + 2, stage0);
+            load(x, min(c + 4, end));
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(stage1);
+            lds_barrier();
+        }
     }
 
     const int r = lane & 31, half = lane >> 5;
@@ -1023,9 +1194,16 @@ hipError_t launch_tiles(ListJob p, hipStream_t stream)
         mt = tile_slots(p.rows, p.nlist, TM);
     }
     const int64_t blocks = mt * p.nt, most = most_blocks(THREADS);
+    // an array of fewer than eight values is read value by value
+    const int64_t all_b = FORM == kGradient ? p.arows * p.n
+                                            : (FORM == kAdapter ? 1 : (int64_t)p.nlist) * p.n * p.kdim;
+    const bool tiny = (FORM == kGradient ? p.rows * p.m : p.arows * p.kdim) < 8 || all_b < 8 ||
+                      (FORM == kAdapter && (int64_t)p.nlist * p.n * p.r < 8);
+    const auto kernel = tiny ? list_tile_kernel<T, TO, FORM, KS, WM, WN, MW, NW, true>
+                             : list_tile_kernel<T, TO, FORM, KS, WM, WN, MW, NW, false>;
     for (int64_t b = 0; b < blocks; b += most) {
         p.block0 = b;
-        hipLaunchKernelGGL((list_tile_kernel<T, TO, FORM, KS, WM, WN, MW, NW>),
+        hipLaunchKernelGGL(kernel,
                            dim3((unsigned)(blocks - b < most ? blocks - b : most)), dim3(THREADS),
                            0, stream, p);
     }
