@@ -18,6 +18,26 @@ namespace ivfpq {
 
 static int hidden_part(int r) { return (r + 7) / 8 * 8; }
 
+// Hidden rows are short and their contraction long, so they take the kernel of few rows,
+// of as many columns at once as they have.
+template <typename T>
+static hipError_t hidden_as(const ListJob &p, hipStream_t stream)
+{
+    if (any_tiny<kHidden>(p))
+        return launch_tiles<T, float, kHidden, 32, 2, 1, 2, 2>(p, stream);
+    const bool few = p.rows <= 16 * p.nlist;
+    if constexpr (sizeof(T) == 4) {
+        return few ? launch_direct<T, kHidden, 1, 1, 8, 2>(p, stream)
+                   : launch_direct<T, kHidden, 2, 2, 8, 1>(p, stream);
+    } else {
+        if (few)
+            return p.r <= 16 ? launch_direct<T, kHidden, 1, 1, 8, 2>(p, stream)
+                             : launch_direct<T, kHidden, 1, 4, 8, 1>(p, stream);
+        return p.r <= 16 ? launch_direct<T, kHidden, 4, 1, 8, 1>(p, stream)
+                         : launch_direct<T, kHidden, 2, 4, 8, 1>(p, stream);
+    }
+}
+
 template <typename T>
 static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
 {
@@ -39,21 +59,17 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
     p.row_list = reinterpret_cast<int32_t *>(static_cast<T *>(q.ws) + q.t * p.width);
     p.b = q.down;
     p.n = q.r;
-    const bool tiny = p.arows * p.kdim < 8 || (int64_t)p.nlist * p.r * p.kdim < 8;
-    if (hipError_t e = tiny ? launch_tiles<T, float, kHidden, 32, 2, 1, 2, 2>(p, stream)
-                            : launch_direct<T, kHidden, 2, 8>(p, stream))
+    if (hipError_t e = hidden_as<T>(p, stream))
         return e;
     p.b = q.w;
     p.n = q.n;
     p.out = q.out;
-    if (p.rows <= 64 && !(p.arows * p.kdim < 8 || (int64_t)p.n * p.kdim < 8 ||
-                          (int64_t)p.nlist * p.n * p.r < 8)) {
+    if (p.rows <= 320 && !any_tiny<kAdapter>(p)) {
         if (p.rows <= 16)
-            return launch_direct<T, kAdapter, 1, 8>(p, stream);
-        if (p.rows <= 32 || sizeof(T) == 4)
-            return launch_direct<T, kAdapter, 2, 8>(p, stream);
-        if constexpr (sizeof(T) == 2)
-            return launch_direct<T, kAdapter, 4, 4>(p, stream);
+            return launch_direct<T, kAdapter, 1, 1, 8, 2>(p, stream);
+        if (p.rows <= 32)
+            return launch_direct<T, kAdapter, 2, 1, 8, 2>(p, stream);
+        return launch_direct<T, kAdapter, 2, 2, 8, 1>(p, stream);
     }
     if constexpr (sizeof(T) == 2)
         if (copies_fit<kAdapter>(p))

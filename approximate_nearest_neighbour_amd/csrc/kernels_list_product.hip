@@ -5,22 +5,27 @@
 
 namespace ivfpq {
 
+static bool small_tiles(const ListJob &p)
+{
+    const int64_t mt = (p.rows + 127) / 128 + (p.rows < p.nlist ? p.rows : p.nlist) / 2;
+    return mt * ((p.n + 127) / 128) <= 512;
+}
+
 template <typename T, int FORM>
 static hipError_t rows_as(const ListJob &p, hipStream_t stream)
 {
     if constexpr (FORM == kRowsAlong) {
-        if (p.rows <= 16 * p.nlist && !(p.arows * p.kdim < 8 || (int64_t)p.nlist * p.n * p.kdim < 8)) {
-            if (p.rows <= 8 * p.nlist)
-                return launch_direct<T, kRowsAlong, 1, 4>(p, stream);
-            return launch_direct<T, kRowsAlong, 2, 4>(p, stream);
-        }
+        if (p.rows <= 4 * p.nlist && !any_tiny<FORM>(p))
+            return launch_direct<T, kRowsAlong, 1, 1, 4, 2>(p, stream);
     }
     if constexpr (std::is_same<T, float>::value)
-        return launch_tiles<T, T, FORM, 16, 2, 2, 2, 2>(p, stream);
+        return small_tiles(p) ? launch_tiles<T, T, FORM, 32, 1, 1, 2, 2>(p, stream)
+                              : launch_tiles<T, T, FORM, 16, 2, 2, 2, 2>(p, stream);
     else if (copies_fit<FORM>(p))
         return launch_copies<T, T, FORM, 64, 2, 4, 2, 2, 4>(p, stream);
     else
-        return launch_tiles<T, T, FORM, 32, 2, 2, 2, 2>(p, stream);
+        return small_tiles(p) ? launch_tiles<T, T, FORM, 64, 1, 1, 2, 2>(p, stream)
+                              : launch_tiles<T, T, FORM, 32, 2, 2, 2, 2>(p, stream);
 }
 
 template <typename T>
@@ -57,6 +62,8 @@ static hipError_t gradient_as(const ListJob &p, hipStream_t stream)
         if (copies_fit<kGradient>(p))
             return launch_copies<T, TO, kGradient, 64, 2, 4, 2, 2, 4>(p, stream);
     constexpr int KS = std::is_same<T, float>::value ? 16 : 32;
+    if ((int64_t)p.nlist * ((p.n + 127) / 128) * ((p.m + 127) / 128) <= 512)
+        return launch_tiles<T, TO, kGradient, 32, 1, 1, 2, 2>(p, stream);
     return launch_tiles<T, TO, kGradient, KS, 2, 2, 2, 2>(p, stream);
 }
 

@@ -1,11 +1,11 @@
 // Products of few rows: bound by the matrices' bytes, which go from memory straight to
 // registers.
 //
-// A wave forms 16 RT rows by 16 columns with 16 x 16 x 32 matrix instructions; KW of a
+// A wave forms 16 RT rows by 16 CT columns with 16 x 16 x 32 matrix instructions; KW of a
 // workgroup's eight waves share the contraction of the same columns out between them
 // and join their sums through LDS, in the waves' order.  The contraction comes in
 // units of 64 values, of which lane group g (16 lanes) has values 16 g to 16 g + 15 of
-// its row: whole lines of memory for 16-bit rows.  Two turns of two units are under
+// its row: whole lines of memory for 16-bit rows.  Two turns of TURN units are under
 // way, one of them while the other is multiplied.  Rows may begin at any address.
 //
 // An adapter's hidden rows are multiplied with the up matrices after the shared ones:
@@ -29,13 +29,13 @@ __device__ __forceinline__ f32x4 mfma16_small(s16x8 a, s16x8 b, f32x4 c)
 }
 
 // Operands of the matrix instructions from eight values: the values, or their parts.
-template <typename T>
-__device__ __forceinline__ void operands_of(const Eight<T> &x, s16x8 (&out)[Parts<T>::N])
+template <typename T, bool ODD>
+__device__ __forceinline__ void operands_of(const Eight<T, ODD> &x, s16x8 (&out)[Parts<T>::N])
 {
     if constexpr (sizeof(T) == 2) {
         out[0] = __builtin_bit_cast(s16x8, x.v);
     } else {
-        typename Eight<T>::E8 parts[3];
+        typename Eight<T, ODD>::E8 parts[3];
         x.split(parts);
 #pragma unroll
         for (int p = 0; p < 3; ++p)
@@ -43,13 +43,13 @@ __device__ __forceinline__ void operands_of(const Eight<T> &x, s16x8 (&out)[Part
     }
 }
 
-template <typename T, int FORM, int RT, int KW>
+template <typename T, bool ODD, int FORM, int RT, int CT, int KW, int TURN>
 __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
 {
     static_assert(FormOf<FORM>::B_ALONG, "rows along the contraction");
     using E = typename Parts<T>::E;
-    constexpr int NP = Parts<T>::N, TM = 16 * RT, GROUPS = 8 / KW, UNIT = 64, TURN = 2;
-    __shared__ f32x4 part[KW > 1 ? 8 : 1][RT][64];
+    constexpr int NP = Parts<T>::N, TM = 16 * RT, GROUPS = 8 / KW, UNIT = 64;
+    __shared__ f32x4 part[KW > 1 ? 8 : 1][RT * CT][64];
     __shared__ int segs[FORM == kAdapter ? TM + 1 : 1];
     __shared__ int tile_list[FORM == kAdapter ? TM : 1];
 
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
     const int64_t block = p.block0 + blockIdx.x;
     const int64_t mt = block / p.nt;
     const int cols = FORM == kHidden ? p.r : p.n;
-    const int n0 = ((int)(block - mt * p.nt) * GROUPS + wave / KW) * 16;
+    const int n0 = ((int)(block - mt * p.nt) * GROUPS + wave / KW) * 16 * CT;
     PartTile tile{0, mt * TM, min(mt * TM + TM, p.rows)};
     if constexpr (FORM != kAdapter)
         tile = find_part(p.offsets, p.nlist, p.rows, mt, TM, p.by_row);
@@ -70,10 +70,12 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
     if (FORM == kHidden && !listed)
         return;
 
-    f32x4 acc[RT];
+    f32x4 acc[RT][CT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
-        acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     int64_t arow[RT]; // rows past the tile's end repeat its last one; they are not stored
     bool there[RT];
     if (listed) {
@@ -86,9 +88,13 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
             arow[i] = max(from, (int64_t)0) * p.kdim;
         }
         const int64_t list = FORM == kAdapter ? 0 : tile.e;
-        const int64_t brow = (list * cols + min(n0 + r, cols - 1)) * p.kdim;
+        int64_t brow[CT]; // columns past the last repeat it; they are not stored
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+            brow[j] = (list * cols + min(n0 + j * 16 + r, cols - 1)) * p.kdim;
+        using Values = Eight<T, ODD>;
         struct Turn {
-            Eight<T> a[TURN][2][RT], b[TURN][2];
+            Values a[TURN][2][RT], b[TURN][2][CT];
         };
         const int units = (p.kdim + UNIT - 1) / UNIT, whole = p.kdim / UNIT;
         auto load = [&](Turn &t, int u0) { // units u0 and u0 + KW, whole ones
@@ -97,33 +103,52 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
                 const int64_t at = (int64_t)min(u0 + u * KW, whole - 1) * UNIT + g * 16;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    t.b[u][h].read(b + brow + at + h * 8);
+#pragma unroll
+                    for (int j = 0; j < CT; ++j)
+                        t.b[u][h][j].read(b + brow[j] + at + h * 8);
 #pragma unroll
                     for (int i = 0; i < RT; ++i)
                         t.a[u][h][i].read(a + arow[i] + at + h * 8);
                 }
             }
         };
-        auto product = [&](const Eight<T> &xa, const Eight<T> &xb, f32x4 &c) {
-            s16x8 oa[NP], ob[NP];
-            operands_of(xa, oa);
-            operands_of(xb, ob);
+        auto product = [&](const s16x8 (&oa)[NP], const s16x8 (&ob)[NP], f32x4 &c) {
 #pragma unroll
             for (int sum = NP - 1; sum >= 0; --sum)
 #pragma unroll
                 for (int q = 0; q <= sum; ++q)
                     c = mfma16_small<E>(ob[sum - q], oa[q], c);
         };
-        auto multiply = [&](const Turn &t, int u0) {
+        auto products = [&](const Values (&xa)[RT], const Values (&xb)[CT]) {
+            s16x8 ob[CT][NP];
+#pragma unroll
+            for (int j = 0; j < CT; ++j)
+                operands_of(xb[j], ob[j]);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                s16x8 oa[NP];
+                operands_of(xa[i], oa);
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+                    product(oa, ob[j], acc[i][j]);
+            }
+        };
+        auto all_ready = [](auto &x) {
+#pragma unroll
+            for (auto &v : x)
+                v.ready();
+        };
+        auto multiply = [&](Turn &t, int u0) {
 #pragma unroll
             for (int u = 0; u < TURN; ++u) {
                 if (u0 + u * KW >= whole)
                     break;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < RT; ++i)
-                        product(t.a[u][h][i], t.b[u][h], acc[i]);
+                for (int h = 0; h < 2; ++h) {
+                    all_ready(t.a[u][h]);
+                    all_ready(t.b[u][h]);
+                    products(t.a[u][h], t.b[u][h]);
+                }
             }
         };
         const int first = wave % KW, step = TURN * KW;
@@ -145,17 +170,22 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int at = whole * UNIT + g * 16 + h * 8;
-                Eight<T> xb, xa[RT];
-                xb.template read_near<false>(b, brow + at, all_b);
+                Values xb[CT], xa[RT];
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+                    xb[j].template read_near<false>(b, brow[j] + at, all_b);
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
                     xa[i].template read_near<false>(a, arow[i] + at, all_a);
-                xb.template settle<false>(brow + at, all_b, p.kdim - at);
+                all_ready(xa);
+                all_ready(xb);
 #pragma unroll
-                for (int i = 0; i < RT; ++i) {
+                for (int j = 0; j < CT; ++j)
+                    xb[j].template settle<false>(brow[j] + at, all_b, p.kdim - at);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
                     xa[i].template settle<false>(arow[i] + at, all_a, p.kdim - at);
-                    product(xa[i], xb, acc[i]);
-                }
+                products(xa, xb);
             }
         }
         if constexpr (FORM == kAdapter) {
@@ -163,15 +193,20 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
             const T *hidden = static_cast<const T *>(p.hidden), *up = static_cast<const T *>(p.up);
             const int64_t all_up = (int64_t)p.nlist * p.n * p.r;
             const int count = segs[TM];
+            constexpr int AHEAD = RT + CT <= 3 ? 4 : 2; // lists under way
             for (int at0 = 0; at0 < p.width; at0 += 32) { // 32 values a matrix instruction
                 const int at = at0 + g * 8, col = at < p.rp ? at : at - p.rp;
-                for (int s0 = first; s0 < count; s0 += 4 * KW) { // four lists under way
-                    Eight<T> xb[4], xa[4][RT];
+                for (int s0 = first; s0 < count; s0 += AHEAD * KW) {
+                    Values xb[AHEAD][CT], xa[AHEAD][RT];
+                    auto up_at = [&](int seg, int j) {
+                        return ((int64_t)seg * p.n + min(n0 + j * 16 + r, p.n - 1)) * p.r + col;
+                    };
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
+                    for (int s = 0; s < AHEAD; ++s) {
                         const int seg = segs[min(s0 + s * KW, count - 1)];
-                        xb[s].template read_near<false>(
-                            up, ((int64_t)seg * p.n + min(n0 + r, p.n - 1)) * p.r + col, all_up);
+#pragma unroll
+                        for (int j = 0; j < CT; ++j)
+                            xb[s][j].template read_near<false>(up, up_at(seg, j), all_up);
 #pragma unroll
                         for (int i = 0; i < RT; ++i) {
                             const int64_t row = min(tile.p0 + i * 16 + r, tile.p1 - 1);
@@ -179,19 +214,22 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
                         }
                     }
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
+                    for (int s = 0; s < AHEAD; ++s) {
                         if (s0 + s * KW >= count)
                             break;
                         const int seg = segs[s0 + s * KW];
-                        xb[s].template settle<false>(
-                            ((int64_t)seg * p.n + min(n0 + r, p.n - 1)) * p.r + col, all_up,
-                            at < p.width ? p.r - col : 0);
+                        all_ready(xa[s]);
+                        all_ready(xb[s]);
+#pragma unroll
+                        for (int j = 0; j < CT; ++j)
+                            xb[s][j].template settle<false>(up_at(seg, j), all_up,
+                                                            at < p.width ? p.r - col : 0);
 #pragma unroll
                         for (int i = 0; i < RT; ++i) {
                             const bool mine = tile_list[i * 16 + r] == seg && at < p.width;
                             xa[s][i].template settle<false>(0, 8, mine ? 8 : 0);
-                            product(xa[s][i], xb[s], acc[i]);
                         }
+                        products(xa[s], xb[s]);
                     }
                 }
             }
@@ -200,7 +238,9 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
     if constexpr (KW > 1) {
 #pragma unroll
         for (int i = 0; i < RT; ++i)
-            part[wave][i][lane] = acc[i];
+#pragma unroll
+            for (int j = 0; j < CT; ++j)
+                part[wave][i * CT + j][lane] = acc[i][j];
         __syncthreads();
         if (wave % KW != 0)
             return;
@@ -208,57 +248,67 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
         for (int w = 1; w < KW; ++w)
 #pragma unroll
             for (int i = 0; i < RT; ++i)
-                acc[i] += part[wave + w][i][lane];
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+                    acc[i][j] += part[wave + w][i * CT + j][lane];
     }
     // result q of a lane: column 4 g + q, row r
-    const int n = n0 + 4 * g;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         const int64_t row = tile.p0 + i * 16 + r;
         if (row >= tile.p1)
             continue;
-        if (listed && !there[i])
-            acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        int64_t t = -1;
+        float scale = 1.f;
         if constexpr (FORM == kHidden) {
-            const int64_t t = source_row(p, row);
+            t = source_row(p, row);
             if (t < 0)
                 continue;
             if (n0 == 0 && g == 0)
                 p.row_list[t] = tile.e;
-            const float scale = p.scales ? p.scales[tile.e] : 1.f;
-            T *to = static_cast<T *>(p.hidden) + t * p.width + n;
+            scale = p.scales ? p.scales[tile.e] : 1.f;
+        }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (n + q >= p.rp)
-                    continue;
-                const float h = n + q < p.r ? acc[i][q] * scale : 0.f;
-                to[q] = (T)h;
-                if constexpr (NP == 1)
-                    to[p.rp + q] = (T)(h - (float)to[q]);
-            }
-        } else {
-            typedef T V __attribute__((ext_vector_type(4), aligned(sizeof(T))));
-            T *out = static_cast<T *>(p.out) + row * p.n + n;
-            if (n + 4 <= p.n) {
-                V v;
+        for (int j = 0; j < CT; ++j) {
+            const int n = n0 + j * 16 + 4 * g;
+            f32x4 v = acc[i][j];
+            if (listed && !there[i])
+                v = f32x4{0.f, 0.f, 0.f, 0.f};
+            if constexpr (FORM == kHidden) {
+                T *to = static_cast<T *>(p.hidden) + t * p.width + n;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    v[q] = (T)acc[i][q];
-                *reinterpret_cast<V *>(out) = v;
+                for (int q = 0; q < 4; ++q) {
+                    if (n + q >= p.rp)
+                        continue;
+                    const float h = n + q < p.r ? v[q] * scale : 0.f;
+                    to[q] = (T)h;
+                    if constexpr (NP == 1)
+                        to[p.rp + q] = (T)(h - (float)to[q]);
+                }
             } else {
+                typedef T V __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+                T *out = static_cast<T *>(p.out) + row * p.n + n;
+                if (n + 4 <= p.n) {
+                    V w;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (n + q < p.n)
-                        out[q] = (T)acc[i][q];
+                    for (int q = 0; q < 4; ++q)
+                        w[q] = (T)v[q];
+                    *reinterpret_cast<V *>(out) = w;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (n + q < p.n)
+                            out[q] = (T)v[q];
+                }
             }
         }
     }
 }
 
-template <typename T, int FORM, int RT, int KW>
+template <typename T, int FORM, int RT, int CT, int KW, int TURN>
 hipError_t launch_direct(ListJob p, hipStream_t stream)
 {
-    constexpr int TM = 16 * RT, TN = 16 * 8 / KW;
+    constexpr int TM = 16 * RT, TN = 16 * CT * 8 / KW;
     const int cols = FORM == kHidden ? p.rp : p.n;
     p.nt = (uint32_t)((cols + TN - 1) / TN);
     int64_t mt;
@@ -269,11 +319,17 @@ hipError_t launch_direct(ListJob p, hipStream_t stream)
         mt = tile_slots(p.rows, p.nlist, TM);
     }
     const int64_t blocks = mt * p.nt, most = most_blocks(512);
+    auto odd = [&](const void *q, int64_t width) {
+        return sizeof(T) == 2 && ((reinterpret_cast<uintptr_t>(q) & 2) || width % 2);
+    };
+    auto kernel = list_direct_kernel<T, false, FORM, RT, CT, KW, TURN>;
+    if constexpr (sizeof(T) == 2)
+        if (odd(p.a, p.kdim) || odd(p.b, p.kdim) || (FORM == kAdapter && odd(p.up, p.r)))
+            kernel = list_direct_kernel<T, true, FORM, RT, CT, KW, TURN>;
     for (int64_t b = 0; b < blocks; b += most) {
         p.block0 = b;
-        hipLaunchKernelGGL((list_direct_kernel<T, FORM, RT, KW>),
-                           dim3((unsigned)(blocks - b < most ? blocks - b : most)), dim3(512), 0,
-                           stream, p);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks - b < most ? blocks - b : most)),
+                           dim3(512), 0, stream, p);
     }
     return hipGetLastError();
 }

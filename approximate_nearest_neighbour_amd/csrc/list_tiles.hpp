@@ -173,22 +173,46 @@ struct Reader {
     }
 };
 
-// Eight values of a line in registers, on their way to LDS.
-template <typename T>
+// Eight values of a line in registers.  ODD: 16-bit values whose place may not be a
+// multiple of four bytes, where loads of 16 bytes take twice as long: the aligned four
+// bytes that hold them are read (which end in the same four bytes as the values do)
+// and shifted together when they have arrived (`ready`).  301 rows by 1001 x 777, rank 7:
+// ODDFIG.
+template <typename T, bool ODD = false>
 struct Eight {
+    static_assert(!ODD || sizeof(T) == 2, "four-byte values are aligned");
     static constexpr int Q = sizeof(T) / 2; // 16-byte pieces
     typedef T V __attribute__((ext_vector_type(8 / Q), aligned(sizeof(T))));
     typedef uint32_t Words __attribute__((ext_vector_type(4 * Q)));
     Words v;
+    uint32_t last, shift; // ODD
 
     __device__ __forceinline__ void read(const T *p)
     {
+        if constexpr (ODD) {
+            typedef uint32_t W4 __attribute__((ext_vector_type(4), aligned(4)));
+            const uint32_t half = (uint32_t)(uintptr_t)p & 2;
+            const uint8_t *from = reinterpret_cast<const uint8_t *>(p) - half;
+            v = *reinterpret_cast<const W4 *>(from);
+            last = *reinterpret_cast<const uint32_t *>(from + 12 + 2 * half);
+            shift = 8 * half;
+        } else {
 #pragma unroll
-        for (int h = 0; h < Q; ++h) {
-            const u32x4 w = __builtin_bit_cast(u32x4, reinterpret_cast<const V *>(p)[h]);
+            for (int h = 0; h < Q; ++h) {
+                const u32x4 w = __builtin_bit_cast(u32x4, reinterpret_cast<const V *>(p)[h]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[h * 4 + i] = w[i];
+            }
+        }
+    }
+    // once after read, before anything else
+    __device__ __forceinline__ void ready()
+    {
+        if constexpr (ODD) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[h * 4 + i] = w[i];
+                v[i] = __builtin_amdgcn_alignbit(i < 3 ? v[(i + 1) & 3] : last, v[i], shift);
         }
     }
     // The eight values from number `at` of an array of `all` on, in two steps, so that
@@ -213,6 +237,8 @@ struct Eight {
                 else
                     v[i] = __builtin_bit_cast(uint32_t, x[i]);
             }
+            last = v[3];
+            shift = 0;
         }
     }
     // ... of which the first `count` are kept, the others zero.
@@ -453,8 +479,9 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
     const bool edge_b = FORM == kGradient || n0 + TN > p.n;
 
     // A chunk on its way: read at once, settled (ends, missing lines) when it goes to LDS.
+    constexpr bool ODD = sizeof(T) == 2; // aligned 16-bit operands take the copies below
     struct Chunk {
-        Eight<T> a[QA], b[QB];
+        Eight<T, ODD> a[QA], b[QB];
         int64_t at[FORM == kGradient ? QB : 1]; // kGradient: where b's pieces come from
         int count[FORM == kGradient ? QB : 1];
     };
@@ -563,6 +590,12 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
     };
     auto store = [&](Chunk &from, int64_t c, uint8_t *to) {
         const bool none = c >= chunks, last = (c + 1) * KS > kdim;
+#pragma unroll
+        for (int j = 0; j < QA; ++j)
+            from.a[j].ready();
+#pragma unroll
+        for (int j = 0; j < QB; ++j)
+            from.b[j].ready();
         if (FORM == kAdapter && c >= main_chunks && !none) {
             int seg, k0;
             extra_of(c, seg, k0);
@@ -1177,6 +1210,16 @@ hipError_t launch_copies(ListJob p, hipStream_t stream)
     return hipGetLastError();
 }
 
+// Whether an operand has fewer than eight values in all, and so is read value by value.
+template <int FORM>
+bool any_tiny(const ListJob &p)
+{
+    const int64_t a = FORM == kGradient ? p.rows * p.m : p.arows * p.kdim;
+    const int64_t b = FORM == kGradient ? p.arows * p.n
+                                        : (FORM == kAdapter ? 1 : (int64_t)p.nlist) * p.n * p.kdim;
+    return a < 8 || b < 8 || (FORM == kAdapter && (int64_t)p.nlist * p.n * p.r < 8);
+}
+
 template <typename T, typename TO, int FORM, int KS, int WM, int WN, int MW, int NW>
 hipError_t launch_tiles(ListJob p, hipStream_t stream)
 {
@@ -1194,11 +1237,7 @@ hipError_t launch_tiles(ListJob p, hipStream_t stream)
         mt = tile_slots(p.rows, p.nlist, TM);
     }
     const int64_t blocks = mt * p.nt, most = most_blocks(THREADS);
-    // an array of fewer than eight values is read value by value
-    const int64_t all_b = FORM == kGradient ? p.arows * p.n
-                                            : (FORM == kAdapter ? 1 : (int64_t)p.nlist) * p.n * p.kdim;
-    const bool tiny = (FORM == kGradient ? p.rows * p.m : p.arows * p.kdim) < 8 || all_b < 8 ||
-                      (FORM == kAdapter && (int64_t)p.nlist * p.n * p.r < 8);
+    const bool tiny = any_tiny<FORM>(p);
     const auto kernel = tiny ? list_tile_kernel<T, TO, FORM, KS, WM, WN, MW, NW, true>
                              : list_tile_kernel<T, TO, FORM, KS, WM, WN, MW, NW, false>;
     for (int64_t b = 0; b < blocks; b += most) {
