@@ -64,17 +64,31 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
     p.b = q.w;
     p.n = q.n;
     p.out = q.out;
-    if (p.rows <= 320 && !any_tiny<kAdapter>(p)) {
+    // Few rows, or rows that the copies cannot read and too few tiles for all CUs.
+    const bool copies = sizeof(T) == 2 && copies_fit<kAdapter>(p);
+    const int64_t middle = count_tiles<kAdapter>(p, 128, 128);
+    if (!any_tiny<kAdapter>(p) && (p.rows <= 128 || (!copies && middle <= 64))) {
         if (p.rows <= 16)
             return launch_direct<T, kAdapter, 1, 1, 8, 2>(p, stream);
         if (p.rows <= 32)
             return launch_direct<T, kAdapter, 2, 1, 8, 2>(p, stream);
         return launch_direct<T, kAdapter, 2, 2, 8, 1>(p, stream);
     }
-    if constexpr (sizeof(T) == 2)
-        if (copies_fit<kAdapter>(p))
-            return launch_copies<T, T, kAdapter, 64, 2, 4, 2, 2, 4>(p, stream);
-    return launch_tiles<T, T, kAdapter, KS, 2, 2, 2, 2>(p, stream);
+    if constexpr (sizeof(T) == 2) {
+        if (copies) {
+            if (middle <= 64)
+                return launch_copies<T, T, kAdapter, 64, 4, 1, 1, 1, 4>(p, stream);
+            if (middle <= 128)
+                return launch_copies<T, T, kAdapter, 64, 4, 1, 2, 2, 2>(p, stream);
+            if (middle <= 256)
+                return launch_copies<T, T, kAdapter, 64, 2, 1, 2, 2, 2>(p, stream);
+            if (3 * ((count_tiles<kAdapter>(p, 256, 256) + 255) / 256) <= (middle + 255) / 256)
+                return launch_copies<T, T, kAdapter, 64, 2, 4, 2, 2, 4>(p, stream);
+            return launch_copies<T, T, kAdapter, 64, 2, 2, 2, 2, 2>(p, stream);
+        }
+    }
+    return middle <= 512 ? launch_tiles<T, T, kAdapter, 2 * KS, 1, 1, 2, 2>(p, stream)
+                         : launch_tiles<T, T, kAdapter, KS, 2, 2, 2, 2>(p, stream);
 }
 
 size_t adapter_bytes(int64_t t, int r)

@@ -5,27 +5,32 @@
 
 namespace ivfpq {
 
-static bool small_tiles(const ListJob &p)
-{
-    const int64_t mt = (p.rows + 127) / 128 + (p.rows < p.nlist ? p.rows : p.nlist) / 2;
-    return mt * ((p.n + 127) / 128) <= 512;
-}
-
 template <typename T, int FORM>
 static hipError_t rows_as(const ListJob &p, hipStream_t stream)
 {
+    const int64_t middle = count_tiles<FORM>(p, 128, 128);
+    if constexpr (sizeof(T) == 2) {
+        if (copies_fit<FORM>(p)) {
+            const int64_t large = count_tiles<FORM>(p, 256, 256);
+            if (p.rows <= 16 * p.nlist)
+                return launch_copies<T, T, FORM, 64, 4, 1, 1, 1, 4>(p, stream);
+            if (p.rows > 256 * p.nlist && 3 * ((large + 255) / 256) <= (middle + 255) / 256)
+                return launch_copies<T, T, FORM, 64, 2, 4, 2, 2, 4>(p, stream);
+            if (p.rows <= 32 * p.nlist)
+                return launch_copies<T, T, FORM, 64, 2, 1, 2, 2, 2>(p, stream);
+            if (middle <= 192)
+                return launch_copies<T, T, FORM, 64, 4, 2, 2, 2, 2>(p, stream);
+            return launch_copies<T, T, FORM, 64, 2, 2, 2, 2, 2>(p, stream);
+        }
+    }
     if constexpr (FORM == kRowsAlong) {
         if (p.rows <= 4 * p.nlist && !any_tiny<FORM>(p))
             return launch_direct<T, kRowsAlong, 1, 1, 4, 2>(p, stream);
     }
-    if constexpr (std::is_same<T, float>::value)
-        return small_tiles(p) ? launch_tiles<T, T, FORM, 32, 1, 1, 2, 2>(p, stream)
-                              : launch_tiles<T, T, FORM, 16, 2, 2, 2, 2>(p, stream);
-    else if (copies_fit<FORM>(p))
-        return launch_copies<T, T, FORM, 64, 2, 4, 2, 2, 4>(p, stream);
-    else
-        return small_tiles(p) ? launch_tiles<T, T, FORM, 64, 1, 1, 2, 2>(p, stream)
-                              : launch_tiles<T, T, FORM, 32, 2, 2, 2, 2>(p, stream);
+    constexpr int KS = sizeof(T) == 4 ? 16 : 32;
+    return p.rows <= 32 * p.nlist || middle <= 512
+               ? launch_tiles<T, T, FORM, 2 * KS, 1, 1, 2, 2>(p, stream)
+               : launch_tiles<T, T, FORM, KS, 2, 2, 2, 2>(p, stream);
 }
 
 template <typename T>
@@ -58,11 +63,15 @@ hipError_t launch_list_product(const ListProduct &q, int type, hipStream_t strea
 template <typename T, typename TO>
 static hipError_t gradient_as(const ListJob &p, hipStream_t stream)
 {
-    if constexpr (sizeof(T) == 2)
-        if (copies_fit<kGradient>(p))
-            return launch_copies<T, TO, kGradient, 64, 2, 4, 2, 2, 4>(p, stream);
-    constexpr int KS = std::is_same<T, float>::value ? 16 : 32;
-    if ((int64_t)p.nlist * ((p.n + 127) / 128) * ((p.m + 127) / 128) <= 512)
+    if constexpr (sizeof(T) == 2) {
+        if (copies_fit<kGradient>(p)) {
+            if (count_tiles<kGradient>(p, 256, 256) > 96)
+                return launch_copies<T, TO, kGradient, 64, 2, 4, 2, 2, 4>(p, stream);
+            return launch_copies<T, TO, kGradient, 64, 2, 2, 2, 2, 2>(p, stream);
+        }
+    }
+    constexpr int KS = sizeof(T) == 4 ? 16 : 32;
+    if (count_tiles<kGradient>(p, 128, 128) <= 512)
         return launch_tiles<T, TO, kGradient, 32, 1, 1, 2, 2>(p, stream);
     return launch_tiles<T, TO, kGradient, KS, 2, 2, 2, 2>(p, stream);
 }
@@ -73,7 +82,56 @@ static hipError_t gradient_to(const ListJob &p, int out_type, hipStream_t stream
     return out_type == kF32 ? gradient_as<T, float>(p, stream) : gradient_as<T, T>(p, stream);
 }
 
-size_t list_gradient_bytes(int64_t, int, int, int) { return 0; }
+// The lists in descending order of length, by eighths of a power of two, so that no long
+// one is left for the end.
+__global__ __launch_bounds__(1024) void list_size_kernel(const int32_t *offsets, int nlist,
+                                                         int64_t rows, int32_t *order)
+{
+    constexpr int CLASSES = 256;
+    __shared__ int at[CLASSES];
+    auto class_of = [&](int e) {
+        const int64_t n = part_begin(offsets, nlist, rows, e + 2) -
+                          part_begin(offsets, nlist, rows, e + 1);
+        const uint32_t v = n > 0 ? (uint32_t)n : 0u;
+        if (v < 8)
+            return CLASSES - 1 - (int)v;
+        const int top = 31 - __builtin_clz(v);
+        return CLASSES - 1 - ((top - 2) * 8 + (int)(v >> (top - 3) & 7));
+    };
+    for (int c = threadIdx.x; c < CLASSES; c += 1024)
+        at[c] = 0;
+    __syncthreads();
+    for (int e = threadIdx.x; e < nlist; e += 1024)
+        atomicAdd(&at[class_of(e)], 1);
+    __syncthreads();
+    if (threadIdx.x < 64) { // exclusive sums, four classes a lane
+        int c[4], sum = 0;
+        for (int i = 0; i < 4; ++i) {
+            c[i] = at[threadIdx.x * 4 + i];
+            sum += c[i];
+        }
+        int before = (int)wave_inclusive_sum((uint32_t)sum) - sum;
+        for (int i = 0; i < 4; ++i) {
+            at[threadIdx.x * 4 + i] = before;
+            before += c[i];
+        }
+    }
+    __syncthreads();
+    // which list of a class comes first depends on the run; no result does
+    for (int e = threadIdx.x; e < nlist; e += 1024)
+        order[atomicAdd(&at[class_of(e)], 1)] = e;
+}
+
+// Worth a launch (LPTFIG)
+static bool by_size(int64_t rows, int n, int d, int nlist)
+{
+    return nlist > 1 && rows * n >= ((int64_t)1 << 33) / d;
+}
+
+size_t list_gradient_bytes(int64_t rows, int n, int d, int nlist)
+{
+    return by_size(rows, n, d, nlist) ? (size_t)nlist * 4 : 0;
+}
 
 hipError_t launch_list_gradient(const ListGradient &q, int type, int out_type, hipStream_t stream)
 {
@@ -89,6 +147,12 @@ hipError_t launch_list_gradient(const ListGradient &q, int type, int out_type, h
     p.k = FastDiv((uint32_t)q.k);
     p.rows = q.rows;
     p.out = q.out;
+    if (by_size(q.rows, q.n, q.d, q.nlist)) {
+        int32_t *order = static_cast<int32_t *>(q.ws);
+        hipLaunchKernelGGL(list_size_kernel, dim3(1), dim3(1024), 0, stream, q.offsets, q.nlist,
+                           q.rows, order);
+        p.by_size = order;
+    }
     switch (type) {
     case kF32: return gradient_as<float, float>(p, stream);
     case kBF16: return gradient_to<__bf16>(p, out_type, stream);

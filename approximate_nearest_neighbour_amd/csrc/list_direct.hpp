@@ -35,7 +35,7 @@ __device__ __forceinline__ void operands_of(const Eight<T, ODD> &x, s16x8 (&out)
     if constexpr (sizeof(T) == 2) {
         out[0] = __builtin_bit_cast(s16x8, x.v);
     } else {
-        typename Eight<T, ODD>::E8 parts[3];
+        u32x4 parts[3];
         x.split(parts);
 #pragma unroll
         for (int p = 0; p < 3; ++p)
@@ -152,9 +152,12 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
             }
         };
         const int first = wave % KW, step = TURN * KW;
-        if (whole > 0) {
-            Turn x, y;
+        Turn x, y;
+        if (whole > 0)
             load(x, first);
+        if constexpr (FORM == kAdapter) // while the first operands are under way
+            find_lists<TM, 512>(p, tile, tile_list, segs);
+        if (whole > 0) {
             for (int u = first; u < whole; u += 2 * step) {
                 load(y, u + step);
                 __builtin_amdgcn_sched_barrier(0);
@@ -189,7 +192,6 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
             }
         }
         if constexpr (FORM == kAdapter) {
-            find_lists<TM, 512>(p, tile, tile_list, segs);
             const T *hidden = static_cast<const T *>(p.hidden), *up = static_cast<const T *>(p.up);
             const int64_t all_up = (int64_t)p.nlist * p.n * p.r;
             const int count = segs[TM];

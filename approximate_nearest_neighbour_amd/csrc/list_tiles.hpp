@@ -16,11 +16,14 @@
 // line's number, so that lanes that read together touch every bank equally.
 //
 // float32 values are split into three bfloat16 parts, x = hi + mid + lo, each the
-// nearest to what the parts before leave: |mid| <= 2^-9 |x|, |lo| <= 2^-18 |x|,
-// and what three parts leave is below 2^-27 |x|.  A product is the sum of six of
-// the nine part products, the smallest first; the three dropped are below 2^-26 of
-// it together, less than float32's own half step.  Six bfloat16 instructions take
-// 6 / 16 of the time of the float32 one.  An infinity becomes a NaN this way.
+// nearest to what the parts before leave: |mid| <= 2^-8 |x|, |lo| <= 2^-16 |x|, and
+// the three hold all 24 bits.  A product is the sum of six of the nine part products,
+// the smallest first; the three dropped, mid lo, lo mid and lo lo, are below 2^-23 of
+// it together (2^-25 on average), so that a sum of products is as near as float32's
+// own: 512 x 512 results of 2048 random products are off by 7.0e-7 of their norm, the
+// library's float32 product by 8.1e-7.  Six bfloat16 instructions take 6 / 16 of the
+// time of the float32 one.  What rounds to an infinity in bfloat16 (magnitudes from
+// 255.5 2^120 on) becomes a NaN this way.
 #pragma once
 
 #include "list_plan.hpp"
@@ -275,20 +278,23 @@ struct Eight {
                 v[i] = i < n ? v[i] : 0u;
         }
     }
-    typedef __bf16 E8 __attribute__((ext_vector_type(8)));
-    // float32 values to their three parts
-    __device__ __forceinline__ void split(E8 (&out)[3]) const
+    // float32 values to their three parts, two at a time: a conversion rounds two values, and
+    // the rounded ones are the upper halves of float32 numbers
+    __device__ __forceinline__ void split(u32x4 (&out)[3]) const
     {
+        typedef float F2 __attribute__((ext_vector_type(2)));
+        typedef __bf16 B2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // the largest finite values stay finite in bfloat16
-            const float x = __uint_as_float(v[i]);
-            const __bf16 hi = (__bf16)__builtin_amdgcn_fmed3f(x, -0x1.FEp127f, 0x1.FEp127f);
-            const float r1 = x - (float)hi;
-            const __bf16 mid = (__bf16)r1;
-            out[0][i] = hi;
-            out[1][i] = mid;
-            out[2][i] = (__bf16)(r1 - (float)mid);
+        for (int i = 0; i < 4; ++i) {
+            F2 x = {__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])};
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                const uint32_t near =
+                    __builtin_bit_cast(uint32_t, __builtin_convertvector(x, B2));
+                out[p][i] = near;
+                x[0] -= __uint_as_float(near << 16);
+                x[1] -= __uint_as_float(near & 0xFFFF0000u);
+            }
         }
     }
     // to the planes at `to`, `plane` bytes apart
@@ -297,11 +303,11 @@ struct Eight {
         if constexpr (Q == 1) {
             *reinterpret_cast<Words *>(to) = v;
         } else {
-            E8 out[3];
+            u32x4 out[3];
             split(out);
 #pragma unroll
             for (int p = 0; p < 3; ++p)
-                *reinterpret_cast<E8 *>(to + p * plane) = out[p];
+                *reinterpret_cast<u32x4 *>(to + p * plane) = out[p];
         }
     }
 };
@@ -320,7 +326,8 @@ struct ListJob {
     int nlist = 0;
     uint32_t mt = 0, nt = 0; // tiles along both sides (kGradient: mt of one list)
     bool by_row = false;
-    int64_t block0 = 0;
+    const int32_t *by_size = nullptr; // kGradient: the lists, the longest first (nullptr: as they are)
+    int64_t block0 = 0; // the launch's first workgroup
     // adapters: hidden rows [t][width] (16-bit: high parts, then low parts, rp each),
     // the list of each row, up matrices [nlist][n][r], scales [nlist] or nullptr
     void *hidden = nullptr;
@@ -412,8 +419,9 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
     PartTile tile;
     int m0 = 0;
     if constexpr (FORM == kGradient) {
-        const int e = (int)(mt / p.mt);
-        m0 = (int)(mt - (int64_t)e * p.mt) * TM;
+        const int nth = (int)(mt / p.mt);
+        const int e = p.by_size ? p.by_size[nth] : nth;
+        m0 = (int)(mt - (int64_t)nth * p.mt) * TM;
         tile = {e, part_begin(p.offsets, p.nlist, p.rows, e + 1),
                 part_begin(p.offsets, p.nlist, p.rows, e + 2)};
     } else if constexpr (FORM == kAdapter) {
@@ -842,8 +850,9 @@ __global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, Tile
     PartTile tile;
     int m0 = 0;
     if constexpr (FORM == kGradient) {
-        const int e = (int)(mt / p.mt);
-        m0 = (int)(mt - (int64_t)e * p.mt) * TM;
+        const int nth = (int)(mt / p.mt);
+        const int e = p.by_size ? p.by_size[nth] : nth;
+        m0 = (int)(mt - (int64_t)nth * p.mt) * TM;
         tile = {e, part_begin(p.offsets, p.nlist, p.rows, e + 1),
                 part_begin(p.offsets, p.nlist, p.rows, e + 2)};
     } else if constexpr (FORM == kAdapter) {
@@ -1090,48 +1099,52 @@ __global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, Tile
         // its columns.
         typedef TO T8 __attribute__((ext_vector_type(8)));
         typedef TO T8U __attribute__((ext_vector_type(8), aligned(sizeof(TO))));
-        constexpr int BR = WN * 4, ROWB = BR * 16, PART = STAGE / WAVES / 16 * 16;
+        constexpr int PART = STAGE / WAVES / 16 * 16;
+        constexpr int JS = 32 * WN * 64 <= PART ? WN : WN / 2; // blocks of columns at a time
+        constexpr int BR = JS * 4, ROWB = BR * 16;
         constexpr int SLAB = PART / (32 * ROWB) < WM ? PART / (32 * ROWB) : WM;
         static_assert(SLAB >= 1 && WM % SLAB == 0, "rows through LDS");
         lds_barrier();
         uint8_t *mine = stage0 + wave * PART;
 #pragma unroll
-        for (int b0 = 0; b0 < WM; b0 += SLAB) {
+        for (int b0 = 0; b0 < WM; b0 += SLAB)
 #pragma unroll
-            for (int i = 0; i < SLAB; ++i)
+            for (int j0 = 0; j0 < WN; j0 += JS) {
 #pragma unroll
-                for (int j = 0; j < WN; ++j)
+                for (int i = 0; i < SLAB; ++i)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        T8 v;
+                    for (int j = 0; j < JS; ++j)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            T8 v;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                v[e] = (TO)acc[b0 + i][j0 + j][q * 8 + e];
+                            const int b = (j * 4 + q * 2 + half) ^ (r & (BR - 1));
+                            *reinterpret_cast<T8 *>(mine + (i * 32 + r) * ROWB + b * 16) = v;
+                        }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+                for (int k = 0; k < SLAB * 32 * BR / 64; ++k) {
+                    const int line = (k * 64 + lane) / BR, b = lane % BR;
+                    const T8 v = *reinterpret_cast<const T8 *>(mine + line * ROWB +
+                                                               (b ^ (line & (BR - 1))) * 16);
+                    const int64_t row = row_base + (wm * WM + b0) * 32 + line;
+                    const int n = n0 + (wn * WN + j0) * 32 + b * 8;
+                    if (row >= row_end || n >= p.n)
+                        continue;
+                    TO *to = out + row * p.n + n;
+                    if (n + 8 <= p.n) {
+                        *reinterpret_cast<T8U *>(to) = v;
+                    } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            v[e] = (TO)acc[b0 + i][j][q * 8 + e];
-                        const int b = (j * 4 + q * 2 + half) ^ (r & (BR - 1));
-                        *reinterpret_cast<T8 *>(mine + (i * 32 + r) * ROWB + b * 16) = v;
+                            if (n + e < p.n)
+                                to[e] = v[e];
                     }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-            for (int k = 0; k < SLAB * 32 * BR / 64; ++k) {
-                const int line = (k * 64 + lane) / BR, b = lane % BR;
-                const T8 v = *reinterpret_cast<const T8 *>(mine + line * ROWB +
-                                                           (b ^ (line & (BR - 1))) * 16);
-                const int64_t row = row_base + (wm * WM + b0) * 32 + line;
-                const int n = n0 + wn * WN * 32 + b * 8;
-                if (row >= row_end || n >= p.n)
-                    continue;
-                TO *to = out + row * p.n + n;
-                if (n + 8 <= p.n) {
-                    *reinterpret_cast<T8U *>(to) = v;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (n + e < p.n)
-                            to[e] = v[e];
                 }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        }
     } else {
 #pragma unroll
         for (int j = 0; j < WN; ++j) {
@@ -1167,6 +1180,17 @@ bool copies_fit(const ListJob &p)
            (FORM != kAdapter || (whole(p.up) && p.r % 8 == 0));
 }
 
+// Tiles of `high` by `wide` results that a product has; half of the lists end inside one.
+template <int FORM>
+int64_t count_tiles(const ListJob &p, int high, int wide)
+{
+    const int64_t nt = (p.n + wide - 1) / wide;
+    if (FORM == kGradient)
+        return p.nlist * ((p.m + high - 1) / high) * nt;
+    const int64_t ends = FORM == kAdapter ? 0 : (p.rows < p.nlist ? p.rows : p.nlist) / 2;
+    return ((p.rows + high - 1) / high + ends) * nt;
+}
+
 template <typename T, typename TO, int FORM, int KS, int STAGES, int WM, int WN, int MW, int NW>
 hipError_t launch_copies(ListJob p, hipStream_t stream)
 {
@@ -1196,8 +1220,12 @@ hipError_t launch_copies(ListJob p, hipStream_t stream)
         g.high /= 2;
     while (g.wide > 1 && count(g.high, g.wide) < 8)
         g.wide /= 2;
-    while (g.wide < p.nt && count(g.high, 2 * g.wide) >= 64)
+    while (FORM != kGradient && g.wide < p.nt && count(g.high, 2 * g.wide) >= 64)
         g.wide *= 2;
+    // a list's tiles on all XCDs alike, as lists differ in length
+    while (FORM == kGradient && p.nlist > 1 && g.wide > 1 &&
+           (int64_t)p.mt * p.nt < 8 * g.high * g.wide)
+        g.wide /= 2;
     g.across = (p.nt + g.wide - 1) / g.wide;
     const int64_t blocks = (count(g.high, g.wide) + 7) / 8 * 8 * g.high * g.wide;
     const int64_t most = most_blocks(THREADS);

@@ -528,9 +528,10 @@ ivfpq_status ivfpq_route_combine_grad_ex(const void *grad_dev, const void *rows_
  * ones whose rows are multiples of 16 bytes are read faster); an output or workspace
  * overlaps no input.  Two calls that may run at the same time need a workspace
  * each.  Sums are float32, rounded once to the output's type.  float32 products
- * are formed from three bfloat16 parts of each factor, exact to 2^-26 of every
- * product; an infinite factor gives NaN there, in 16-bit types what float32 sums
- * of its products give. */
+ * are formed from three bfloat16 parts of each factor, every one within 2^-23 of
+ * itself; a factor whose magnitude is 255.5 2^120 or more, an infinity among them,
+ * gives NaN there, in 16-bit types an infinity gives what float32 sums of its
+ * products give. */
 
 /* Rows sorted by list, each times its list's own matrix: matrices_dev holds nlist
  * matrices [n][d] (transposed 0) or [d][n] (not 0), offsets_dev [nlist + 1]

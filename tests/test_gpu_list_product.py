@@ -6,8 +6,8 @@ Tolerances.  Small integers: every product and partial sum is an integer below 2
 values: K exact products added one after the other in float32 take K - 1 additions
 that round, each by at most 2^-23 of the sum of the magnitudes however it rounds.  A
 float32 product is six part products, so there are 6 K - 1 such additions, of terms
-whose magnitudes sum to at most (1 + 2^-8 + 2^-17)^2 < 1 + 2^-6 of the products';
-the three dropped parts add 2^-26.  Storing rounds by half a step of the type, or
+whose magnitudes sum to at most (1 + 2^-8 + 2^-16)^2 < 1 + 2^-6 of the products';
+the three dropped parts add 2^-23.  Storing rounds by half a step of the type, or
 2^-25 near zero for binary16 and 2^-134 for bfloat16.
 """
 import numpy as np
@@ -57,7 +57,7 @@ def list_product64(x, matrices, offsets, rows, source, transposed):
 def sum_error(terms, dtype):
     """Share of the sum of magnitudes that a float32 sum of so many products is off by."""
     if dtype == torch.float32:
-        return (6 * terms - 1) * 2.0 ** -23 * (1 + 2.0 ** -6) + 2.0 ** -26
+        return (6 * terms - 1) * 2.0 ** -23 * (1 + 2.0 ** -6) + 2.0 ** -23
     return (terms - 1) * 2.0 ** -23
 
 
