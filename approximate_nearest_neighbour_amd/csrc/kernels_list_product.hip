@@ -60,26 +60,91 @@ hipError_t launch_list_product(const ListProduct &q, int type, hipStream_t strea
     }
 }
 
-template <typename T, typename TO>
-static hipError_t gradient_as(const ListJob &p, hipStream_t stream)
+// Tiles of the gradient: 256 x 256 results, 128 x 128 where those would leave CUs
+// empty or the operands go through registers, 64 x 64 of the latter (GRADFIG).
+struct GradientTiles {
+    bool copies;
+    int size;
+};
+static GradientTiles gradient_tiles(const ListJob &p, int type)
 {
+    const bool copies = type != kF32 && copies_fit<kGradient>(p);
+    if (copies)
+        return {true, count_tiles<kGradient>(p, 256, 256) > 96 ? 256 : 128};
+    return {false, count_tiles<kGradient>(p, 128, 128) > 512 ? 128 : 64};
+}
+
+template <typename T, typename TO>
+static hipError_t gradient_as(const ListJob &p, GradientTiles tiles, hipStream_t stream)
+{
+    constexpr int KS = sizeof(T) == 4 ? 16 : 32;
     if constexpr (sizeof(T) == 2) {
-        if (copies_fit<kGradient>(p)) {
-            if (count_tiles<kGradient>(p, 256, 256) > 96)
-                return launch_copies<T, TO, kGradient, 64, 2, 4, 2, 2, 4>(p, stream);
-            return launch_copies<T, TO, kGradient, 64, 2, 2, 2, 2, 2>(p, stream);
+        if (tiles.copies)
+            return tiles.size == 256 ? launch_copies<T, TO, kGradient, 64, 2, 4, 2, 2, 4>(p, stream)
+                                     : launch_copies<T, TO, kGradient, 64, 2, 2, 2, 2, 2>(p, stream);
+    }
+    return tiles.size == 64 ? launch_tiles<T, TO, kGradient, 32, 1, 1, 2, 2>(p, stream)
+                            : launch_tiles<T, TO, kGradient, KS, 2, 2, 2, 2>(p, stream);
+}
+
+// The parts' sums, in their order, to the output's type; a thread four of them.
+template <typename TO>
+__global__ __launch_bounds__(256) void list_join_kernel(const float *__restrict__ parts,
+                                                        int64_t count, int splits,
+                                                        TO *__restrict__ out, int64_t block0)
+{
+    typedef float F4 __attribute__((ext_vector_type(4), aligned(4)));
+    typedef TO V4 __attribute__((ext_vector_type(4), aligned(sizeof(TO))));
+    const int64_t at = ((block0 + blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (at >= count)
+        return;
+    if (at + 4 <= count) {
+        F4 sum = *reinterpret_cast<const F4 *>(parts + at);
+        for (int s = 1; s < splits; ++s)
+            sum += *reinterpret_cast<const F4 *>(parts + s * count + at);
+        V4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = (TO)sum[i];
+        *reinterpret_cast<V4 *>(out + at) = v;
+    } else {
+        for (int64_t i = at; i < count; ++i) {
+            float sum = parts[i];
+            for (int s = 1; s < splits; ++s)
+                sum += parts[s * count + i];
+            out[i] = (TO)sum;
         }
     }
-    constexpr int KS = sizeof(T) == 4 ? 16 : 32;
-    if (count_tiles<kGradient>(p, 128, 128) <= 512)
-        return launch_tiles<T, TO, kGradient, 32, 1, 1, 2, 2>(p, stream);
-    return launch_tiles<T, TO, kGradient, KS, 2, 2, 2, 2>(p, stream);
+}
+
+template <typename TO>
+static hipError_t join_parts(const float *parts, int64_t count, int splits, void *out,
+                             hipStream_t stream)
+{
+    const int64_t blocks = (count + 1023) / 1024, most = most_blocks(256);
+    for (int64_t b = 0; b < blocks; b += most)
+        hipLaunchKernelGGL(list_join_kernel<TO>,
+                           dim3((unsigned)(blocks - b < most ? blocks - b : most)), dim3(256), 0,
+                           stream, parts, count, splits, static_cast<TO *>(out), b);
+    return hipGetLastError();
 }
 
 template <typename T>
-static hipError_t gradient_to(const ListJob &p, int out_type, hipStream_t stream)
+static hipError_t gradient_to(ListJob p, int type, int out_type, void *ws, hipStream_t stream)
 {
-    return out_type == kF32 ? gradient_as<T, float>(p, stream) : gradient_as<T, T>(p, stream);
+    const GradientTiles tiles = gradient_tiles(p, type);
+    if (p.splits > 1) {
+        void *out = p.out;
+        p.out = ws;
+        if (hipError_t e = gradient_as<T, float>(p, tiles, stream))
+            return e;
+        const int64_t count = (int64_t)p.nlist * p.m * p.n;
+        return out_type == kF32
+                   ? join_parts<float>(static_cast<float *>(ws), count, p.splits, out, stream)
+                   : join_parts<T>(static_cast<float *>(ws), count, p.splits, out, stream);
+    }
+    return out_type == kF32 ? gradient_as<T, float>(p, tiles, stream)
+                            : gradient_as<T, T>(p, tiles, stream);
 }
 
 // The lists in descending order of length, by eighths of a power of two, so that no long
@@ -122,14 +187,25 @@ __global__ __launch_bounds__(1024) void list_size_kernel(const int32_t *offsets,
         order[atomicAdd(&at[class_of(e)], 1)] = e;
 }
 
-// Worth a launch (LPTFIG)
+// Whether sorting the lists by length is worth a launch (64 lists, 32,768 rows, 2048 x
+// 2048, lengths as 1 / i: 524 us, the lists by length 370).
 static bool by_size(int64_t rows, int n, int d, int nlist)
 {
     return nlist > 1 && rows * n >= ((int64_t)1 << 33) / d;
 }
 
+// Workgroups that share a list, by the larger tiles: what is read by copies or not is not
+// known from the sizes alone, and the workspace is.
+static int splits_of(int64_t rows, int n, int d, int nlist)
+{
+    return gradient_splits(rows, nlist, (int64_t)nlist * ((n + 127) / 128) * ((d + 127) / 128));
+}
+
 size_t list_gradient_bytes(int64_t rows, int n, int d, int nlist)
 {
+    const int splits = splits_of(rows, n, d, nlist);
+    if (splits > 1)
+        return (size_t)splits * nlist * n * d * 4;
     return by_size(rows, n, d, nlist) ? (size_t)nlist * 4 : 0;
 }
 
@@ -147,16 +223,17 @@ hipError_t launch_list_gradient(const ListGradient &q, int type, int out_type, h
     p.k = FastDiv((uint32_t)q.k);
     p.rows = q.rows;
     p.out = q.out;
-    if (by_size(q.rows, q.n, q.d, q.nlist)) {
+    p.splits = splits_of(q.rows, q.n, q.d, q.nlist);
+    if (p.splits == 1 && by_size(q.rows, q.n, q.d, q.nlist)) {
         int32_t *order = static_cast<int32_t *>(q.ws);
         hipLaunchKernelGGL(list_size_kernel, dim3(1), dim3(1024), 0, stream, q.offsets, q.nlist,
                            q.rows, order);
         p.by_size = order;
     }
     switch (type) {
-    case kF32: return gradient_as<float, float>(p, stream);
-    case kBF16: return gradient_to<__bf16>(p, out_type, stream);
-    default: return gradient_to<_Float16>(p, out_type, stream);
+    case kF32: return gradient_to<float>(p, type, out_type, q.ws, stream);
+    case kBF16: return gradient_to<__bf16>(p, type, out_type, q.ws, stream);
+    default: return gradient_to<_Float16>(p, type, out_type, q.ws, stream);
     }
 }
 

@@ -53,4 +53,25 @@ __host__ __device__ inline int64_t slot_row(int64_t slot, int64_t begin, int64_t
     return row < end ? row : end;
 }
 
+// Part s of the rows [p0, p1) of a list that `splits` workgroups share: whole chunks of
+// 64 rows but for the last part, the same number of them for all that have any.
+__host__ __device__ inline void split_rows(int64_t &p0, int64_t &p1, int s, int splits)
+{
+    const int64_t chunks = (p1 - p0 + 63) / 64, per = (chunks + splits - 1) / splits * 64;
+    const int64_t end = p1;
+    p0 = p0 + s * per < end ? p0 + s * per : end;
+    p1 = p0 + per < end ? p0 + per : end;
+}
+
+// Workgroups that share the rows of a list's gradient where its tiles are few: enough
+// for two a CU, with at least eight chunks of an even list's rows each.  `tiles` of
+// all lists.
+inline int gradient_splits(int64_t rows, int nlist, int64_t tiles)
+{
+    int splits = 1;
+    while (splits < 64 && 2 * splits * tiles <= 512 && rows / nlist >= 2 * splits * 512)
+        splits *= 2;
+    return splits;
+}
+
 } // namespace ivfpq

@@ -327,6 +327,7 @@ struct ListJob {
     uint32_t mt = 0, nt = 0; // tiles along both sides (kGradient: mt of one list)
     bool by_row = false;
     const int32_t *by_size = nullptr; // kGradient: the lists, the longest first (nullptr: as they are)
+    int splits = 1; // kGradient: workgroups that share a list's rows, a result each
     int64_t block0 = 0; // the launch's first workgroup
     // adapters: hidden rows [t][width] (16-bit: high parts, then low parts, rp each),
     // the list of each row, up matrices [nlist][n][r], scales [nlist] or nullptr
@@ -417,13 +418,15 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
     const int n0 = (int)nt * TN;
 
     PartTile tile;
-    int m0 = 0;
+    int m0 = 0, split = 0;
     if constexpr (FORM == kGradient) {
-        const int nth = (int)(mt / p.mt);
-        const int e = p.by_size ? p.by_size[nth] : nth;
+        const int nth = (int)(mt / p.mt), list = nth / p.splits;
+        split = nth - list * p.splits;
+        const int e = p.by_size ? p.by_size[list] : list;
         m0 = (int)(mt - (int64_t)nth * p.mt) * TM;
         tile = {e, part_begin(p.offsets, p.nlist, p.rows, e + 1),
                 part_begin(p.offsets, p.nlist, p.rows, e + 2)};
+        split_rows(tile.p0, tile.p1, split, p.splits);
     } else if constexpr (FORM == kAdapter) {
         tile = {0, mt * TM, min(mt * TM + TM, p.rows)};
     } else {
@@ -711,8 +714,9 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
     }
 
     const int r = lane & 31, half = lane >> 5;
-    const int64_t row_base = FORM == kGradient ? (int64_t)tile.e * p.m + m0 : tile.p0;
-    const int64_t row_end = FORM == kGradient ? (int64_t)(tile.e + 1) * p.m : tile.p1;
+    const int64_t matrix = FORM == kGradient ? (int64_t)split * p.nlist + tile.e : 0;
+    const int64_t row_base = FORM == kGradient ? matrix * p.m + m0 : tile.p0;
+    const int64_t row_end = FORM == kGradient ? (matrix + 1) * p.m : tile.p1;
     if constexpr (FORM == kHidden) {
         // a lane has one column of sixteen rows (PAIR is false: TO is float)
         static_assert(!PAIR, "hidden rows");
@@ -848,13 +852,15 @@ __global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, Tile
     const int n0 = (int)nt * TN;
 
     PartTile tile;
-    int m0 = 0;
+    int m0 = 0, split = 0;
     if constexpr (FORM == kGradient) {
-        const int nth = (int)(mt / p.mt);
-        const int e = p.by_size ? p.by_size[nth] : nth;
+        const int nth = (int)(mt / p.mt), list = nth / p.splits;
+        split = nth - list * p.splits;
+        const int e = p.by_size ? p.by_size[list] : list;
         m0 = (int)(mt - (int64_t)nth * p.mt) * TM;
         tile = {e, part_begin(p.offsets, p.nlist, p.rows, e + 1),
                 part_begin(p.offsets, p.nlist, p.rows, e + 2)};
+        split_rows(tile.p0, tile.p1, split, p.splits);
     } else if constexpr (FORM == kAdapter) {
         tile = {0, mt * TM, min(mt * TM + TM, p.rows)};
     } else {
@@ -899,8 +905,7 @@ __global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, Tile
     }
 #pragma unroll
     for (int j = 0; j < CB; ++j)
-        offb[j] = FORM == kGradient && p.order ? block_b(j) * 16
-                                               : (uint32_t)(line_b(j) * ldb * 2) + block_b(j) * 16;
+        offb[j] = (uint32_t)(line_b(j) * ldb * 2) + block_b(j) * 16;
     const int64_t abytes = (FORM == kGradient ? p.rows : p.arows) * lda * 2;
     const int64_t bmats = FORM == kAdapter ? 1 : p.nlist;
     const int64_t bbytes = FORM == kGradient ? p.arows * ldb * 2 : bmats * p.n * (int64_t)p.kdim * 2;
@@ -909,7 +914,31 @@ __global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, Tile
     const __amdgpu_buffer_rsrc_t brange = range_of(
         p.b, F::B_ALONG ? ((FORM == kAdapter ? 0 : (int64_t)max(tile.e, 0) * p.n) + n0) * ldb * 2 : 0,
         bbytes);
-    typedef const __attribute__((address_space(4))) int32_t *ConstInts;
+    // A gathered second operand (kGradient): the slots of a lane's lines are loaded two
+    // chunks ahead, and become offsets before the chunk's copies are issued; the wait at
+    // the end of a chunk is for them too.
+    static_assert(FORM != kGradient || STAGES == 2, "slots are waited for by the next chunk");
+    const bool gather_b = FORM == kGradient && p.order;
+    int32_t slots[FORM == kGradient ? CB : 1];
+    auto load_slots = [&](int c) {
+        if constexpr (FORM == kGradient) {
+            if (gather_b && kdim > 0)
+#pragma unroll
+                for (int j = 0; j < CB; ++j)
+                    slots[j] = p.order[tile.p0 + min((int64_t)c * KS + line_b(j), kdim - 1)];
+        }
+    };
+    auto place_slots = [&](int c) { // offb of chunk c
+        if constexpr (FORM == kGradient) {
+            if (gather_b)
+#pragma unroll
+                for (int j = 0; j < CB; ++j) {
+                    const uint32_t row = slots[j] >= 0 ? p.k.div((uint32_t)slots[j]) : ~0u;
+                    const bool there = (int64_t)c * KS + line_b(j) < kdim && row < (uint64_t)p.arows;
+                    offb[j] = there ? row * (uint32_t)(ldb * 2) + block_b(j) * 16 : kNowhere;
+                }
+        }
+    };
 
     // Copy q of chunk c (A's copies, then B's) into the chunk's LDS place.  Past the last
     // chunk nothing is read, and the place cleared: so the number of copies under way
@@ -952,21 +981,7 @@ __global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, Tile
         } else if constexpr (F::B_ALONG) {
             copy16_to_lds(brange, block_b(j) * 8 < left ? offb[j] : kNowhere, along, to);
         } else if (FORM == kGradient && p.order) {
-            // a wave's lines follow each other, so their slots are scalar loads, whose
-            // wait does not hold the copies under way
-            const ConstInts slots = (ConstInts)(uintptr_t)(p.order);
-            uint32_t at = kNowhere;
-#pragma unroll
-            for (int l = 0; l < LB; ++l) {
-                const int line = (wave * CB + j) * LB + l;
-                const int32_t slot = line < left ? slots[tile.p0 + k0 + line] : -1;
-                const uint32_t row = slot >= 0 ? p.k.div((uint32_t)slot) : 0x7FFFFFFFu;
-                const uint32_t byte =
-                    row < (uint64_t)p.arows ? row * (uint32_t)(ldb * 2) : kNowhere;
-                at = lane / PB::BLOCKS == l ? byte : at;
-            }
-            copy16_to_lds(range_of(p.b, (int64_t)n0 * 2, bbytes),
-                          at == kNowhere ? at : at + offb[j], 0, to);
+            copy16_to_lds(range_of(p.b, (int64_t)n0 * 2, bbytes), offb[j], 0, to);
         } else {
             const int64_t row = FORM == kGradient ? tile.p0 + k0
                                                   : (int64_t)max(tile.e, 0) * p.kdim + k0;
@@ -994,6 +1009,9 @@ __global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, Tile
         find_lists<TM, THREADS>(p, tile, tile_list, segs);
         chunks += segs[TM] * per_seg;
     }
+    load_slots(0);
+    place_slots(0);
+    load_slots(1);
 #pragma unroll
     for (int q = 0; q < CA + CB; ++q)
         fetch(0, place(i0), q);
@@ -1049,8 +1067,11 @@ __global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, Tile
         constexpr int I = decltype(i)::value;
         const uint8_t *now = place(i);
         uint8_t *ahead = place(std::integral_constant<int, I + STAGES - 1>{});
+        place_slots(c + 1);
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
+            if (s == PARTS)
+                load_slots(c + 2);
             const Operands &x = o[(s + 1) & 1];
             const int c0 = COPIES * min(s, PARTS) / PARTS, c1 = COPIES * min(s + 1, PARTS) / PARTS;
 #pragma unroll
@@ -1091,8 +1112,9 @@ __global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, Tile
     wait_vm<0>(); // no copy is under way to where results may go, or past the end
 
     const int r = lane & 31, half = lane >> 5;
-    const int64_t row_base = FORM == kGradient ? (int64_t)tile.e * p.m + m0 : tile.p0;
-    const int64_t row_end = FORM == kGradient ? (int64_t)(tile.e + 1) * p.m : tile.p1;
+    const int64_t matrix = FORM == kGradient ? (int64_t)split * p.nlist + tile.e : 0;
+    const int64_t row_base = FORM == kGradient ? matrix * p.m + m0 : tile.p0;
+    const int64_t row_end = FORM == kGradient ? (matrix + 1) * p.m : tile.p1;
     TO *out = static_cast<TO *>(p.out);
     if constexpr (PAIR) {
         // Through LDS, a wave's own part of a stage, so that a store covers whole rows of
@@ -1199,7 +1221,7 @@ hipError_t launch_copies(ListJob p, hipStream_t stream)
     int64_t mt;
     if (FORM == kGradient) {
         p.mt = (uint32_t)((p.m + TM - 1) / TM);
-        mt = (int64_t)p.mt * p.nlist;
+        mt = (int64_t)p.mt * p.nlist * p.splits;
     } else if (FORM == kAdapter) {
         mt = (p.rows + TM - 1) / TM;
     } else {
@@ -1224,7 +1246,7 @@ hipError_t launch_copies(ListJob p, hipStream_t stream)
         g.wide *= 2;
     // a list's tiles on all XCDs alike, as lists differ in length
     while (FORM == kGradient && p.nlist > 1 && g.wide > 1 &&
-           (int64_t)p.mt * p.nt < 8 * g.high * g.wide)
+           (int64_t)p.mt * p.splits * p.nt < 8 * g.high * g.wide)
         g.wide /= 2;
     g.across = (p.nt + g.wide - 1) / g.wide;
     const int64_t blocks = (count(g.high, g.wide) + 7) / 8 * 8 * g.high * g.wide;
@@ -1257,7 +1279,7 @@ hipError_t launch_tiles(ListJob p, hipStream_t stream)
     int64_t mt;
     if (FORM == kGradient) {
         p.mt = (uint32_t)((p.m + TM - 1) / TM);
-        mt = (int64_t)p.mt * p.nlist;
+        mt = (int64_t)p.mt * p.nlist * p.splits;
     } else if (FORM == kAdapter) {
         mt = (p.rows + TM - 1) / TM;
     } else {
