@@ -60,31 +60,18 @@ hipError_t launch_list_product(const ListProduct &q, int type, hipStream_t strea
     }
 }
 
-// Tiles of the gradient: 256 x 256 results, 128 x 128 where those would leave CUs
-// empty or the operands go through registers, 64 x 64 of the latter (GRADFIG).
-struct GradientTiles {
-    bool copies;
-    int size;
-};
-static GradientTiles gradient_tiles(const ListJob &p, int type)
-{
-    const bool copies = type != kF32 && copies_fit<kGradient>(p);
-    if (copies)
-        return {true, count_tiles<kGradient>(p, 256, 256) > 96 ? 256 : 128};
-    return {false, count_tiles<kGradient>(p, 128, 128) > 512 ? 128 : 64};
-}
-
 template <typename T, typename TO>
-static hipError_t gradient_as(const ListJob &p, GradientTiles tiles, hipStream_t stream)
+static hipError_t gradient_as(const ListJob &p, int size, hipStream_t stream)
 {
     constexpr int KS = sizeof(T) == 4 ? 16 : 32;
     if constexpr (sizeof(T) == 2) {
-        if (tiles.copies)
-            return tiles.size == 256 ? launch_copies<T, TO, kGradient, 64, 2, 4, 2, 2, 4>(p, stream)
-                                     : launch_copies<T, TO, kGradient, 64, 2, 2, 2, 2, 2>(p, stream);
+        if (copies_fit<kGradient>(p))
+            return size == 256 ? launch_copies<T, TO, kGradient, 64, 2, 4, 2, 2, 4>(p, stream)
+                               : launch_copies<T, TO, kGradient, 64, 2, 2, 2, 2, 2>(p, stream);
     }
-    return tiles.size == 64 ? launch_tiles<T, TO, kGradient, 32, 1, 1, 2, 2>(p, stream)
-                            : launch_tiles<T, TO, kGradient, KS, 2, 2, 2, 2>(p, stream);
+    return count_tiles<kGradient>(p, 128, 128) * p.splits > 512
+               ? launch_tiles<T, TO, kGradient, KS, 2, 2, 2, 2>(p, stream)
+               : launch_tiles<T, TO, kGradient, 32, 1, 1, 2, 2>(p, stream);
 }
 
 // The parts' sums, in their order, to the output's type; a thread four of them.
@@ -130,21 +117,20 @@ static hipError_t join_parts(const float *parts, int64_t count, int splits, void
 }
 
 template <typename T>
-static hipError_t gradient_to(ListJob p, int type, int out_type, void *ws, hipStream_t stream)
+static hipError_t gradient_to(ListJob p, int size, int out_type, void *ws, hipStream_t stream)
 {
-    const GradientTiles tiles = gradient_tiles(p, type);
     if (p.splits > 1) {
         void *out = p.out;
         p.out = ws;
-        if (hipError_t e = gradient_as<T, float>(p, tiles, stream))
+        if (hipError_t e = gradient_as<T, float>(p, size, stream))
             return e;
         const int64_t count = (int64_t)p.nlist * p.m * p.n;
         return out_type == kF32
                    ? join_parts<float>(static_cast<float *>(ws), count, p.splits, out, stream)
                    : join_parts<T>(static_cast<float *>(ws), count, p.splits, out, stream);
     }
-    return out_type == kF32 ? gradient_as<T, float>(p, tiles, stream)
-                            : gradient_as<T, T>(p, tiles, stream);
+    return out_type == kF32 ? gradient_as<T, float>(p, size, stream)
+                            : gradient_as<T, T>(p, size, stream);
 }
 
 // The lists in descending order of length, by eighths of a power of two, so that no long
@@ -194,16 +180,9 @@ static bool by_size(int64_t rows, int n, int d, int nlist)
     return nlist > 1 && rows * n >= ((int64_t)1 << 33) / d;
 }
 
-// Workgroups that share a list, by the larger tiles: what is read by copies or not is not
-// known from the sizes alone, and the workspace is.
-static int splits_of(int64_t rows, int n, int d, int nlist)
-{
-    return gradient_splits(rows, nlist, (int64_t)nlist * ((n + 127) / 128) * ((d + 127) / 128));
-}
-
 size_t list_gradient_bytes(int64_t rows, int n, int d, int nlist)
 {
-    const int splits = splits_of(rows, n, d, nlist);
+    const int splits = gradient_share(rows, nlist, n, d).splits;
     if (splits > 1)
         return (size_t)splits * nlist * n * d * 4;
     return by_size(rows, n, d, nlist) ? (size_t)nlist * 4 : 0;
@@ -223,7 +202,8 @@ hipError_t launch_list_gradient(const ListGradient &q, int type, int out_type, h
     p.k = FastDiv((uint32_t)q.k);
     p.rows = q.rows;
     p.out = q.out;
-    p.splits = splits_of(q.rows, q.n, q.d, q.nlist);
+    const GradientShare share = gradient_share(q.rows, q.nlist, q.n, q.d);
+    p.splits = share.splits;
     if (p.splits == 1 && by_size(q.rows, q.n, q.d, q.nlist)) {
         int32_t *order = static_cast<int32_t *>(q.ws);
         hipLaunchKernelGGL(list_size_kernel, dim3(1), dim3(1024), 0, stream, q.offsets, q.nlist,
@@ -231,9 +211,9 @@ hipError_t launch_list_gradient(const ListGradient &q, int type, int out_type, h
         p.by_size = order;
     }
     switch (type) {
-    case kF32: return gradient_to<float>(p, type, out_type, q.ws, stream);
-    case kBF16: return gradient_to<__bf16>(p, type, out_type, q.ws, stream);
-    default: return gradient_to<_Float16>(p, type, out_type, q.ws, stream);
+    case kF32: return gradient_to<float>(p, share.size, out_type, q.ws, stream);
+    case kBF16: return gradient_to<__bf16>(p, share.size, out_type, q.ws, stream);
+    default: return gradient_to<_Float16>(p, share.size, out_type, q.ws, stream);
     }
 }
 

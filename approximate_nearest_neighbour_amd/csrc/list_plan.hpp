@@ -63,15 +63,23 @@ __host__ __device__ inline void split_rows(int64_t &p0, int64_t &p1, int s, int 
     p1 = p0 + per < end ? p0 + per : end;
 }
 
-// Workgroups that share the rows of a list's gradient where its tiles are few: enough
-// for two a CU, with at least eight chunks of an even list's rows each.  `tiles` of
-// all lists.
-inline int gradient_splits(int64_t rows, int nlist, int64_t tiles)
+// The gradient's tiles: 256 x 256 results if these are 32 at least, else 128 x 128; and
+// the workgroups that share a list's rows where the tiles are few: up to one a CU of the
+// larger tiles, two of the others, with at least eight chunks of an even list's rows
+// each.
+struct GradientShare {
+    int size, splits;
+};
+inline GradientShare gradient_share(int64_t rows, int nlist, int n, int d)
 {
-    int splits = 1;
-    while (splits < 64 && 2 * splits * tiles <= 512 && rows / nlist >= 2 * splits * 512)
-        splits *= 2;
-    return splits;
+    auto tiles = [&](int size) {
+        return (int64_t)nlist * ((n + size - 1) / size) * ((d + size - 1) / size);
+    };
+    GradientShare g{tiles(256) >= 32 ? 256 : 128, 1};
+    while (g.splits < 64 && 2 * g.splits * tiles(g.size) <= (g.size == 256 ? 256 : 512) &&
+           rows / nlist >= 2 * g.splits * 512)
+        g.splits *= 2;
+    return g;
 }
 
 } // namespace ivfpq

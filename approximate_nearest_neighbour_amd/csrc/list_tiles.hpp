@@ -218,6 +218,12 @@ struct Eight {
                 v[i] = __builtin_amdgcn_alignbit(i < 3 ? v[(i + 1) & 3] : last, v[i], shift);
         }
     }
+    __device__ __forceinline__ void keep(bool there) // or all zero
+    {
+#pragma unroll
+        for (int i = 0; i < 4 * Q; ++i)
+            v[i] = there ? v[i] : 0u;
+    }
     // The eight values from number `at` of an array of `all` on, in two steps, so that
     // loads are under way together and no branch waits for one.  Near the array's end
     // its last eight are read, and moved down when they are stored.  TINY: the array may
@@ -395,7 +401,7 @@ __device__ __forceinline__ void find_lists(const ListJob &p, const PartTile &til
 }
 
 template <typename T, typename TO, int FORM, int KS, int WM, int WN, int MW, int NW, bool TINY>
-__global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
+__global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
 {
     using F = FormOf<FORM>;
     constexpr int WAVES = MW * NW, THREADS = 64 * WAVES, TM = 32 * WM * MW, TN = 32 * WN * NW;
@@ -657,6 +663,40 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
     reada.init(wm * WM * 32);
     readb.init(wn * WN * 32);
 
+    // Whether chunk c has no value's end among what is read for results that are stored, nor
+    // the array's own end: then it needs no settling but for lines that a gather does not
+    // find, and its conversion, copies and the products of the chunk before are one
+    // stretch without a branch, in which the compiler lays them side by side.
+    auto plain = [&](int64_t c) {
+        const int64_t k1 = (c + 1) * KS;
+        bool fits = !TINY && c < main_chunks && k1 <= kdim;
+        if constexpr (!F::A_ALONG)
+            fits = fits && (tile.p0 + k1 - 1) * p.m + m0 + TM <= all_a;
+        if constexpr (FORM == kGradient)
+            fits = fits && n0 + TN <= p.n;
+        else if constexpr (!F::B_ALONG)
+            fits = fits && ((int64_t)tile.e * p.kdim + k1 - 1) * p.n + n0 + TN <= all_b;
+        return fits;
+    };
+    auto store_plain = [&](Chunk &from, uint8_t *to) {
+#pragma unroll
+        for (int j = 0; j < QA; ++j) {
+            const int piece = j * THREADS + tid;
+            from.a[j].ready();
+            if constexpr (F::PER_LIST_ROWS)
+                from.a[j].keep(arow[j] >= 0);
+            from.a[j].store(to + PA::at(piece / PA::BLOCKS, piece % PA::BLOCKS), PA::PLANE);
+        }
+#pragma unroll
+        for (int j = 0; j < QB; ++j) {
+            const int piece = j * THREADS + tid;
+            from.b[j].ready();
+            if constexpr (FORM == kGradient)
+                from.b[j].keep(from.count[j] > 0);
+            from.b[j].store(to + NP * PA::PLANE + PB::at(piece / PB::BLOCKS, piece % PB::BLOCKS),
+                            PB::PLANE);
+        }
+    };
     auto multiply = [&](const uint8_t *now) {
 #pragma unroll
         for (int s = 0; s < KS / 16; ++s) {
@@ -699,17 +739,27 @@ __global__ __launch_bounds__(64 * MW * NW) void list_tile_kernel(ListJob p)
         load(x, min((int64_t)2, end));
         __builtin_amdgcn_sched_barrier(0);
         lds_barrier();
-        for (int64_t c = 0; c <= end; c += 2) {
-            store(y, c + 1, stage1);
-            load(y, min(c + 3, end));
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(stage0);
+        // the products of chunk c, and chunk c + 1 to LDS, c + 3 on its way
+        auto step = [&](auto fits, Chunk &next, int64_t c, const uint8_t *now, uint8_t *to) {
+            if constexpr (fits) {
+                store_plain(next, to);
+                load(next, min(c + 3, end));
+            } else {
+                store(next, c + 1, to);
+                load(next, min(c + 3, end));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            multiply(now);
             lds_barrier(); // the next chunk is here, and the last reads of this one are done
-            store(x, c + 2, stage0);
-            load(x, min(c + 4, end));
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(stage1);
-            lds_barrier();
+        };
+        int64_t c = 0;
+        for (; plain(c + 2); c += 2) { // so c + 1 is plain too
+            step(std::true_type{}, y, c, stage0, stage1);
+            step(std::true_type{}, x, c + 1, stage1, stage0);
+        }
+        for (; c <= end; c += 2) {
+            step(std::false_type{}, y, c, stage0, stage1);
+            step(std::false_type{}, x, c + 1, stage1, stage0);
         }
     }
 
