@@ -24,7 +24,7 @@ template <typename T>
 static hipError_t hidden_as(const ListJob &p, hipStream_t stream)
 {
     if (any_tiny<kHidden>(p))
-        return launch_tiles<T, float, kHidden, 32, 2, 1, 2, 2>(p, stream);
+        return launch_tiles<T, float, kHidden, 32, 2, 1, 2, 2, true>(p, stream);
     const bool few = p.rows <= 16 * p.nlist;
     if constexpr (sizeof(T) == 4) {
         return few ? launch_direct<T, kHidden, 1, 1, 8, 2>(p, stream)

@@ -226,7 +226,7 @@ __global__ __launch_bounds__(64 * WAVES) void route_scatter_kernel(SortPass s)
 
 // The same sort of up to kSoloSlots slots of any number of lists: one workgroup, as many
 // passes of 8 bits as the lists' numbers have, keys and slots in LDS between them.
-// 1000 slots of 5003 lists: SOLOFIG.
+// 1000 slots of 5003 lists: 6.7 us and 3.6 for the offsets (seven launches: 27 us).
 constexpr int kDigitBins = 256;
 
 __global__ __launch_bounds__(1024) void route_solo_kernel(SortPass s)

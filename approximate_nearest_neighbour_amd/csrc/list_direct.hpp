@@ -9,7 +9,8 @@
 // way, one of them while the other is multiplied.  Rows may begin at any address.
 //
 // An adapter's hidden rows are multiplied with the up matrices after the shared ones:
-// the lists of the tile's rows are dealt to the KW waves.
+// the lists of the tile's rows are dealt to the KW waves.  A lane's results are of one
+// row, and keep what they were where the list is not the row's.
 #pragma once
 
 #include "list_tiles.hpp"
@@ -26,21 +27,6 @@ __device__ __forceinline__ f32x4 mfma16_small(s16x8 a, s16x8 b, f32x4 c)
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(V, a),
                                                       __builtin_bit_cast(V, b), c, 0, 0, 0);
-}
-
-// Operands of the matrix instructions from eight values: the values, or their parts.
-template <typename T, bool ODD>
-__device__ __forceinline__ void operands_of(const Eight<T, ODD> &x, s16x8 (&out)[Parts<T>::N])
-{
-    if constexpr (sizeof(T) == 2) {
-        out[0] = __builtin_bit_cast(s16x8, x.v);
-    } else {
-        u32x4 parts[3];
-        x.split(parts);
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
-            out[p] = __builtin_bit_cast(s16x8, parts[p]);
-    }
 }
 
 template <typename T, bool ODD, int FORM, int RT, int CT, int KW, int TURN>
@@ -226,12 +212,24 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
                         for (int j = 0; j < CT; ++j)
                             xb[s][j].template settle<false>(up_at(seg, j), all_up,
                                                             at < p.width ? p.r - col : 0);
+                        f32x4 before[RT][CT];
 #pragma unroll
                         for (int i = 0; i < RT; ++i) {
-                            const bool mine = tile_list[i * 16 + r] == seg && at < p.width;
-                            xa[s][i].template settle<false>(0, 8, mine ? 8 : 0);
+                            xa[s][i].keep(at < p.width);
+#pragma unroll
+                            for (int j = 0; j < CT; ++j)
+                                before[i][j] = acc[i][j];
                         }
                         products(xa[s], xb[s]);
+#pragma unroll
+                        for (int i = 0; i < RT; ++i) {
+                            const bool mine = tile_list[i * 16 + r] == seg;
+#pragma unroll
+                            for (int j = 0; j < CT; ++j)
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    acc[i][j][q] = mine ? acc[i][j][q] : before[i][j][q];
+                        }
                     }
                 }
             }

@@ -179,8 +179,8 @@ struct Reader {
 // Eight values of a line in registers.  ODD: 16-bit values whose place may not be a
 // multiple of four bytes, where loads of 16 bytes take twice as long: the aligned four
 // bytes that hold them are read (which end in the same four bytes as the values do)
-// and shifted together when they have arrived (`ready`).  301 rows by 1001 x 777, rank 7:
-// ODDFIG.
+// and shifted together when they have arrived (`ready`).  Adapters of rank 7 for 301
+// rows through 1001 x 777: 51 us before, 34 so.
 template <typename T, bool ODD = false>
 struct Eight {
     static_assert(!ODD || sizeof(T) == 2, "four-byte values are aligned");
@@ -398,6 +398,118 @@ __device__ __forceinline__ void find_lists(const ListJob &p, const PartTile &til
             segs[TM] = found;
     }
     lds_barrier();
+}
+
+// Operands of the matrix instructions from eight values: the values, or their parts.
+template <typename T, bool ODD>
+__device__ __forceinline__ void operands_of(const Eight<T, ODD> &x, s16x8 (&out)[Parts<T>::N])
+{
+    if constexpr (sizeof(T) == 2) {
+        out[0] = __builtin_bit_cast(s16x8, x.v);
+    } else {
+        u32x4 parts[3];
+        x.split(parts);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+            out[p] = __builtin_bit_cast(s16x8, parts[p]);
+    }
+}
+
+// The adapter kernels multiply a tile's rows with the up matrices of all its lists, with
+// zeros for the hidden rows of the other lists; an up matrix that holds an infinity or
+// NaN would so reach rows of other lists.  So a wave with a sum that is not finite, in
+// a tile of several lists, forms its sums again, each row's with the row's list alone.
+// `p0`, `n0`: the wave's first row and column; `lists`: its rows' lists.
+template <typename T, bool PAIR, int WM, int WN>
+__device__ __forceinline__ void keep_lists_apart(const ListJob &p, const PartTile &tile, int64_t p0,
+                                                 int n0, const int *lists, const int *segs,
+                                                 int count, f32x16 (&acc)[WM][WN])
+{
+    constexpr int NP = Parts<T>::N;
+    using E = typename Parts<T>::E;
+    using Values = Eight<T, sizeof(T) == 2>;
+    const int lane = lane_id(), r = lane & 31, half = lane >> 5;
+    bool mixed = count > 1;
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+        mixed = mixed || lists[i * 32 + r] != segs[0];
+    float zero = 0.f;
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                zero = __builtin_fmaf(acc[i][j][q], 0.f, zero);
+    if (count == 0 || !__any(mixed) || !__any(zero != 0.f))
+        return;
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                acc[i][j][q] = 0.f;
+    int64_t rows[WM], cols[WN];
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+        rows[i] = min(p0 + i * 32 + r, tile.p1 - 1);
+#pragma unroll
+    for (int j = 0; j < WN; ++j)
+        cols[j] = min(n0 + j * 32 + deal_row<PAIR>(r), p.n - 1);
+    const int64_t all_a = p.rows * p.kdim, all_b = (int64_t)p.n * p.kdim;
+    const int64_t all_hidden = p.rows * p.width, all_up = (int64_t)p.nlist * p.n * p.r;
+    auto operand = [&](const void *array, int64_t at, int64_t all, int left, s16x8 (&to)[NP]) {
+        Values x;
+        x.template read_near<true>(static_cast<const T *>(array), at, all);
+        x.ready();
+        x.template settle<true>(at, all, left);
+        operands_of(x, to);
+    };
+    // seg: the list whose rows take the products (-1: all rows do)
+    auto products = [&](const s16x8 (&oa)[NP], const s16x8 (&ob)[NP], int i, f32x16 &c, int seg) {
+        f32x16 d = c;
+#pragma unroll
+        for (int sum = NP - 1; sum >= 0; --sum)
+#pragma unroll
+            for (int q = 0; q <= sum; ++q)
+                d = PAIR ? mfma16<E>(ob[sum - q], oa[q], d) : mfma16<E>(oa[q], ob[sum - q], d);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const int row = i * 32 + (PAIR ? r : (q >> 2) * 8 + half * 4 + (q & 3));
+            c[q] = seg < 0 || lists[row] == seg ? d[q] : c[q];
+        }
+    };
+    for (int k0 = 0; k0 < p.kdim; k0 += 16) {
+        const int at = k0 + half * 8;
+#pragma unroll
+        for (int i = 0; i < WM; ++i) {
+            s16x8 oa[NP], ob[NP];
+            operand(p.a, rows[i] * p.kdim + at, all_a, p.kdim - at, oa);
+#pragma unroll
+            for (int j = 0; j < WN; ++j) {
+                operand(p.b, cols[j] * p.kdim + at, all_b, p.kdim - at, ob);
+                products(oa, ob, i, acc[i][j], -1);
+            }
+        }
+    }
+    for (int s = 0; s < count; ++s) {
+        const int seg = segs[s];
+        for (int k0 = 0; k0 < p.width; k0 += 16) {
+            const int at = k0 + half * 8, col = at < p.rp ? at : at - p.rp;
+#pragma unroll
+            for (int i = 0; i < WM; ++i) {
+                s16x8 oa[NP], ob[NP];
+                operand(p.hidden, rows[i] * p.width + at, all_hidden, p.width - at, oa);
+#pragma unroll
+                for (int j = 0; j < WN; ++j) {
+                    operand(p.up, ((int64_t)seg * p.n + cols[j]) * p.r + col, all_up,
+                            at < p.width ? p.r - col : 0, ob);
+                    products(oa, ob, i, acc[i][j], seg);
+                }
+            }
+        }
+    }
 }
 
 template <typename T, typename TO, int FORM, int KS, int WM, int WN, int MW, int NW, bool TINY>
@@ -762,6 +874,9 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
             step(std::false_type{}, x, c + 1, stage1, stage0);
         }
     }
+    if constexpr (FORM == kAdapter)
+        keep_lists_apart<T, PAIR>(p, tile, tile.p0 + wm * WM * 32, n0 + wn * WN * 32,
+                                  tile_list + wm * WM * 32, segs, segs[TM], acc);
 
     const int r = lane & 31, half = lane >> 5;
     const int64_t matrix = FORM == kGradient ? (int64_t)split * p.nlist + tile.e : 0;
@@ -876,7 +991,8 @@ struct TileGroups {
 };
 
 template <typename T, typename TO, int FORM, int KS, int STAGES, int WM, int WN, int MW, int NW>
-__global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, TileGroups groups)
+__global__ __launch_bounds__(64 * MW * NW, FORM == kAdapter && STAGES == 2 ? 2 : 1)
+void list_copy_kernel(ListJob p, TileGroups groups)
 {
     static_assert(sizeof(T) == 2, "float32 operands go through registers");
     using F = FormOf<FORM>;
@@ -1160,6 +1276,9 @@ __global__ __launch_bounds__(64 * MW * NW) void list_copy_kernel(ListJob p, Tile
         }
     }
     wait_vm<0>(); // no copy is under way to where results may go, or past the end
+    if constexpr (FORM == kAdapter)
+        keep_lists_apart<T, PAIR>(p, tile, tile.p0 + wm * WM * 32, n0 + wn * WN * 32,
+                                  tile_list + wm * WM * 32, segs, segs[TM], acc);
 
     const int r = lane & 31, half = lane >> 5;
     const int64_t matrix = FORM == kGradient ? (int64_t)split * p.nlist + tile.e : 0;
@@ -1320,7 +1439,9 @@ bool any_tiny(const ListJob &p)
     return a < 8 || b < 8 || (FORM == kAdapter && (int64_t)p.nlist * p.n * p.r < 8);
 }
 
-template <typename T, typename TO, int FORM, int KS, int WM, int WN, int MW, int NW>
+// ONLY_TINY: the caller has another kernel for all but tiny operands.
+template <typename T, typename TO, int FORM, int KS, int WM, int WN, int MW, int NW,
+          bool ONLY_TINY = false>
 hipError_t launch_tiles(ListJob p, hipStream_t stream)
 {
     constexpr int TM = 32 * WM * MW, TN = 32 * WN * NW, THREADS = 64 * MW * NW;
@@ -1337,9 +1458,10 @@ hipError_t launch_tiles(ListJob p, hipStream_t stream)
         mt = tile_slots(p.rows, p.nlist, TM);
     }
     const int64_t blocks = mt * p.nt, most = most_blocks(THREADS);
-    const bool tiny = any_tiny<FORM>(p);
-    const auto kernel = tiny ? list_tile_kernel<T, TO, FORM, KS, WM, WN, MW, NW, true>
-                             : list_tile_kernel<T, TO, FORM, KS, WM, WN, MW, NW, false>;
+    auto kernel = list_tile_kernel<T, TO, FORM, KS, WM, WN, MW, NW, true>;
+    if constexpr (!ONLY_TINY)
+        if (!any_tiny<FORM>(p))
+            kernel = list_tile_kernel<T, TO, FORM, KS, WM, WN, MW, NW, false>;
     for (int64_t b = 0; b < blocks; b += most) {
         p.block0 = b;
         hipLaunchKernelGGL(kernel,

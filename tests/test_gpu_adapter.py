@@ -25,7 +25,10 @@ PARTS = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -16, torch.float16: 2.0 ** -
 # t, n, d, lists, r
 SHAPES = [(1, 8, 8, 1, 1), (1, 256, 128, 4, 16), (5, 33, 17, 3, 7), (16, 64, 64, 2, 8),
           (32, 136, 200, 40, 16), (64, 128, 72, 1, 64), (129, 65, 49, 5, 33), (200, 264, 136, 300, 5),
-          (300, 130, 96, 3, 24), (700, 72, 64, 9, 40), (513, 257, 520, 2, 130)]
+          (300, 130, 96, 3, 24), (700, 72, 64, 9, 40), (513, 257, 520, 2, 130),
+          # every kind of tile: few and many of each size
+          (200, 1000, 64, 3, 8), (500, 4000, 40, 2, 8), (1000, 4000, 24, 2, 16),
+          (1300, 4200, 24, 3, 8), (2048, 4200, 32, 2, 8), (2100, 4201, 23, 2, 5)]
 
 
 def lists_of(rng, t, nlist, kind):
@@ -36,6 +39,27 @@ def lists_of(rng, t, nlist, kind):
     if kind == "none":
         return np.full(t, -1, np.int32)
     return rng.integers(-1, nlist + 1, t).astype(np.int32)
+
+
+def adapter64(x, w, down, up, lists, scales):
+    """The definition, a list at a time (the oracle's goes by rows)."""
+    out, mag = x @ w.T, np.abs(x) @ np.abs(w).T
+    for e in range(len(down)):
+        mine = np.flatnonzero(lists == e)
+        if len(mine):
+            s = 1.0 if scales is None else float(scales[e])
+            out[mine] += s * (x[mine] @ down[e].T) @ up[e].T
+            mag[mine] += abs(s) * (np.abs(x[mine]) @ np.abs(down[e]).T) @ np.abs(up[e]).T
+    return out, mag
+
+
+def test_definition_against_the_oracle():
+    rng = np.random.default_rng(1)
+    args = (rng.standard_normal((9, 5)), rng.standard_normal((4, 5)),
+            rng.standard_normal((3, 2, 5)), rng.standard_normal((3, 4, 2)),
+            np.array([0, 2, -1, 3, 1, 1, 2, 0, 9]), rng.random(3))
+    for got, want in zip(adapter64(*args), R.adapter(*args)):
+        assert np.allclose(got, want)
 
 
 def call(x, w, down, up, lists, scales, **kw):
@@ -55,7 +79,7 @@ def test_adapters_are_exact_on_integers(t, n, d, nlist, r, kind, dtype):
     lists = lists_of(rng, t, nlist, kind)
     for s in (scales, None):
         y = call(x, w, down, up, lists, s)
-        want, _ = R.adapter(np64(x), np64(w), np64(down), np64(up), lists,
+        want, _ = adapter64(np64(x), np64(w), np64(down), np64(up), lists,
                             None if s is None else np64(s))
         assert y.dtype == dtype and np.array_equal(np64(y), rounded(want, dtype))
 
@@ -74,3 +98,65 @@ def test_adapters_of_reals(t, n, d, nlist, r, dtype):
     error = sum_error(d + 2 * r, dtype) + sum_error(d, dtype) + 2.0 ** -24 + PARTS[dtype]
     sums = error * (1 + 2.0 ** -7) * mag
     assert (np.abs(got - want) <= sums + UNIT[dtype] * (np.abs(want) + sums) + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("t,n,d,nlist,r", [(20, 40, 64, 4, 8), (150, 257, 65, 3, 5), (300, 1000, 64, 3, 8),
+                                          (500, 4000, 16, 5, 8), (1000, 4000, 24, 4, 16),
+                                          (1300, 4200, 24, 9, 8), (2048, 4200, 32, 6, 8),
+                                          (2100, 4201, 23, 5, 5)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_bad_values_stay_where_they_are(t, n, d, nlist, r, dtype):
+    """What is wrong in one row, or in the matrices of one list, reaches no other row."""
+    rng = np.random.default_rng(t)
+    x, w = integers(rng, t, d, dtype=dtype), integers(rng, n, d, dtype=dtype)
+    down, up = integers(rng, nlist, r, d, dtype=dtype), integers(rng, nlist, n, r, dtype=dtype)
+    lists = rng.integers(-1, nlist, t).astype(np.int32)
+    lists[:2] = [0, -1]
+    clean = call(x, w, down, up, lists, None)
+    x[1], down[0, r - 1, d - 1], up[nlist - 1, 0] = float("inf"), float("nan"), float("nan")
+    got = call(x, w, down, up, lists, None)
+    hit = np.flatnonzero((lists == 0) | (lists == nlist - 1) | (np.arange(t) == 1))
+    rest = np.setdiff1d(np.arange(t), hit)
+    assert torch.equal(got[rest], clean[rest])
+    assert not got[0].isfinite().any() and not got[1].isfinite().any()
+
+
+def test_results_repeat_and_nothing_else_is_written():
+    rng = np.random.default_rng(4)
+    for dtype in TYPES:
+        for t, n, d, nlist, r in ((32, 130, 72, 6, 8), (200, 1000, 64, 3, 8), (600, 65, 33, 4, 7)):
+            x, w = reals(rng, t, d, dtype=dtype), reals(rng, n, d, dtype=dtype)
+            down, up = reals(rng, nlist, r, d, dtype=dtype), reals(rng, nlist, n, r, dtype=dtype)
+            lists = rng.integers(-1, nlist, t).astype(np.int32)
+            need = A.ivfpq_adapter_product_bytes(t, r)
+            results = []
+            for fill in (0x00, 0xFF):   # the workspace may hold anything, NaN too
+                ws = torch.full((need + 256,), fill, dtype=torch.uint8, device="cuda")
+                guard = torch.full((t * n + 64,), 3.0, dtype=dtype, device="cuda")
+                out = guard[32:-32].view(t, n)
+                results.append(call(x, w, down, up, lists, None, out=out, workspace=ws[:need]).clone())
+                assert (guard[:32] == 3).all() and (guard[-32:] == 3).all()
+                assert (ws[need:] == fill).all()
+            assert torch.equal(*results)
+
+
+def test_refusals_of_device_tensors():
+    x, w = torch.zeros((8, 16), device="cuda"), torch.zeros((4, 16), device="cuda")
+    down, up = torch.zeros((2, 3, 16), device="cuda"), torch.zeros((2, 4, 3), device="cuda")
+    o = torch.zeros(3, dtype=torch.int32, device="cuda")
+    order = torch.zeros(8, dtype=torch.int32, device="cuda")
+    small = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    for call_ in (lambda: A.ivfpq_adapter_product_ex(x, w.t(), down, up, o, order, order),
+                  lambda: A.ivfpq_adapter_product_ex(x, w, down.half(), up, o, order, order),
+                  lambda: A.ivfpq_adapter_product_ex(x, w, down, up[:, :3].contiguous(), o, order,
+                                                     order),
+                  lambda: A.ivfpq_adapter_product_ex(x, w, down, up, o[:2], order, order),
+                  lambda: A.ivfpq_adapter_product_ex(x, w, down, up, o, order[:7], order),
+                  lambda: A.ivfpq_adapter_product_ex(x, w, down, up, o, order, order[:7]),
+                  lambda: A.ivfpq_adapter_product_ex(x, w, down, up, o, order, order,
+                                                     scales=torch.ones(3, device="cuda"))):
+        with pytest.raises(ValueError):
+            call_()
+    with pytest.raises(A.IVFPQError):
+        A.ivfpq_adapter_product_ex(x, w, down, up, o, order, order, workspace=small)
+    assert A.ivfpq_adapter_product_ex(x[:0], w, down, up, o, order[:0], order[:0]).shape == (0, 4)
