@@ -1,4 +1,7 @@
-// Runs the arithmetic of csrc/list_plan.hpp on the CPU.  A line "walk TM ROWS NLIST
+// Runs the arithmetic of csrc/list_plan.hpp on the CPU.  A line "split P0 P1 SPLITS"
+// prints: parts that do not follow each other, rows not in them, parts but the last
+// that are no whole chunks.  "share ROWS NLIST N D" prints the gradient's tile size
+// and splits.  A line "walk TM ROWS NLIST
 // offsets..." prints: tile numbers, rows covered not exactly once, tiles that do not
 // start and end inside one part, and whether the fewer numbers of both ways were taken.
 #include "list_plan.hpp"
@@ -20,7 +23,31 @@ int main()
         std::string word;
         int tm, nlist;
         int64_t rows;
-        in >> word >> tm >> rows >> nlist;
+        in >> word;
+        if (word == "split") {
+            int64_t p0, p1;
+            int splits;
+            in >> p0 >> p1 >> splits;
+            int64_t at = p0, apart = 0, uneven = 0;
+            for (int s = 0; s < splits; ++s) {
+                int64_t a = p0, b = p1;
+                split_rows(a, b, s, splits);
+                apart += a != at || b < a;
+                uneven += b != p1 && (b - a) % 64 != 0;
+                at = b;
+            }
+            std::printf("split %lld %lld %lld\n", (long long)apart, (long long)(p1 - at),
+                        (long long)uneven);
+            continue;
+        }
+        if (word == "share") {
+            int n, d;
+            in >> rows >> nlist >> n >> d;
+            const GradientShare g = gradient_share(rows, nlist, n, d);
+            std::printf("share %d %d\n", g.size, g.splits);
+            continue;
+        }
+        in >> tm >> rows >> nlist;
         std::vector<int32_t> offsets(nlist + 1);
         for (int32_t &o : offsets)
             in >> o;

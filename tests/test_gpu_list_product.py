@@ -71,7 +71,9 @@ SHAPES = [(1, 1, 1, 1), (3, 1, 5, 7), (16, 2, 16, 32), (17, 3, 33, 31), (64, 1, 
           (65, 4, 129, 65), (127, 2, 128, 100), (128, 1, 256, 128), (200, 7, 72, 96),
           (300, 64, 40, 136), (31, 200, 24, 8), (1000, 3, 136, 72), (777, 16, 301, 200),
           (700, 2, 520, 264), (2500, 5, 96, 40), (40, 1, 1024, 512), (513, 2, 257, 1032),
-          (33, 9, 1040, 2050), (1500, 1, 16, 24)]
+          (33, 9, 1040, 2050), (1500, 1, 16, 24),
+          # enough tiles for the larger ones, in every way that operands are read
+          (2048, 1, 4200, 72), (2300, 2, 4224, 71), (3000, 3, 1200, 40), (3001, 3, 1201, 39)]
 
 
 @pytest.mark.parametrize("rows,nlist,n,d", SHAPES)
@@ -123,7 +125,12 @@ def test_product_of_reals(rows, nlist, n, d, transposed, dtype):
                                            (64, 1, 1, 64, 64), (333, 3, 5, 65, 129),
                                            (800, 2, 3, 136, 264), (100, 4, 150, 40, 24),
                                            (3000, 1, 2, 32, 48), (500, 2, 7, 257, 520),
-                                           (6000, 1, 1, 24, 40)])
+                                           (6000, 1, 1, 24, 40),
+                                           # larger tiles, workgroups that share a list, lists by
+                                           # length
+                                           (300, 1, 1, 1104, 2000), (1500, 3, 2, 1056, 1040),
+                                           (4500, 1, 2, 130, 264), (5000, 1, 3, 65, 33),
+                                           (2100, 2, 5, 1032, 2056)])
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("dtype,out", [(t, o) for t in TYPES for o in {t, torch.float32}])
 def test_gradient_is_exact_on_integers(t, k, nlist, n, d, gather, dtype, out):
@@ -154,3 +161,137 @@ def test_definitions_of_the_oracle():
     for e in range(3):
         part = slice(offsets[e], offsets[e + 1])
         assert np.allclose(grad[part].T @ x[order[part] // 2], want[e])
+
+
+def test_offsets_beyond_the_rows_and_entries_that_are_no_rows():
+    rng = np.random.default_rng(3)
+    x = integers(rng, 40, 64, dtype=torch.bfloat16)
+    w = integers(rng, 3, 72, 64, dtype=torch.bfloat16)
+    offsets = np.array([-5, 12, 30, 99], np.int32)
+    y = A.ivfpq_list_product_ex(x, w, torch.from_numpy(offsets).cuda())
+    want, _ = list_product64(np64(x), np64(w), np.clip(offsets, 0, 40), 40, np.arange(40), False)
+    assert np.array_equal(np64(y), rounded(want, torch.bfloat16))
+    # entries of order outside the rows stand for rows of zeros
+    order = np.arange(40, dtype=np.int32)
+    order[[3, 20, 39]] = [-1, 40, 2 ** 31 - 1]
+    for dtype in TYPES:
+        xt, wt = x.to(dtype), w.to(dtype)
+        o = torch.from_numpy(order).cuda()
+        f = torch.tensor([0, 12, 30, 40], dtype=torch.int32, device="cuda")
+        clean = np64(x).copy()
+        clean[[3, 20, 39]] = 0
+        got = A.ivfpq_list_product_ex(xt, wt, f, order=o)
+        want, _ = list_product64(clean, np64(w), [0, 12, 30, 40], 40, np.arange(40), False)
+        assert np.array_equal(np64(got), rounded(want, dtype))
+        grad = integers(rng, 40, 72, dtype=dtype)
+        got = A.ivfpq_list_product_grad_ex(grad, xt, f, order=o, dtype=torch.float32)
+        want = np.stack([np64(grad)[lo:hi].T @ clean[lo:hi] for lo, hi in ((0, 12), (12, 30),
+                                                                          (30, 40))])
+        assert np.array_equal(np64(got), want)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,nlist,n,d", [(130, 4, 72, 64), (20, 30, 33, 31), (600, 2, 264, 200)])
+def test_bad_values_stay_where_they_are(dtype, rows, nlist, n, d):
+    """An infinity or NaN in a row reaches that row's results alone, one in a matrix
+    that list's column; rows of no list are zero whatever is there."""
+    rng = np.random.default_rng(rows)
+    x, w = integers(rng, rows, d, dtype=dtype), integers(rng, nlist, n, d, dtype=dtype)
+    offsets = ragged(rng, rows, nlist, rows // 8, rows - rows // 9)
+    o = torch.from_numpy(offsets).cuda()
+    for transposed in (False, True):
+        m = w.transpose(1, 2).contiguous() if transposed else w
+        clean = A.ivfpq_list_product_ex(x, m, o, transposed=transposed)
+        xb, mb = x.clone(), m.clone()
+        row = rows // 2
+        e = int(np.searchsorted(offsets, row, side="right")) - 1
+        xb[row, d - 1] = float("nan")
+        xb[0] = float("inf")                       # before the first list
+        xb[rows - 1] = float("nan")                # past the last
+        (mb[e, 0, n - 1:] if transposed else mb[e, n - 1, :1]).fill_(float("inf"))
+        got = A.ivfpq_list_product_ex(xb, mb, o, transposed=transposed)
+        touched = torch.zeros_like(clean, dtype=torch.bool)
+        touched[row] = True
+        touched[offsets[e]:offsets[e + 1], n - 1] = True
+        assert torch.equal(got[~touched], clean[~touched])
+        assert got[row].isnan().all()
+        assert not got[offsets[e]:offsets[e + 1], n - 1].isfinite().any()
+
+
+def test_gradient_ignores_rows_of_other_lists():
+    rng = np.random.default_rng(8)
+    for dtype in TYPES:
+        for n, d in ((64, 72), (33, 31)):
+            grad, x = integers(rng, 500, n, dtype=dtype), integers(rng, 500, d, dtype=dtype)
+            o = torch.tensor([100, 170, 170, 333], dtype=torch.int32, device="cuda")
+            want = A.ivfpq_list_product_grad_ex(grad, x, o)
+            grad[:100], x[:100], grad[333:], x[333:] = (float("nan"), float("inf"), float("inf"),
+                                                        float("nan"))
+            assert torch.equal(A.ivfpq_list_product_grad_ex(grad, x, o), want)
+            assert (want[1] == 0).all()
+
+
+def test_results_repeat_and_nothing_else_is_written():
+    rng = np.random.default_rng(2)
+    for dtype in TYPES:
+        for rows, nlist, n, d in ((777, 9, 130, 136), (5000, 1, 65, 33), (2048, 1, 4200, 72)):
+            x, w = reals(rng, rows, d, dtype=dtype), reals(rng, nlist, n, d, dtype=dtype)
+            grad = reals(rng, rows, n, dtype=dtype)
+            o = torch.from_numpy(ragged(rng, rows, nlist)).cuda()
+            need = A.ivfpq_list_product_grad_bytes(rows, n, d, nlist)
+            y, g = [], []
+            for fill in (0.0, float("nan")):
+                guard = torch.full((rows * n + 64,), fill, dtype=dtype, device="cuda")
+                out = guard[32:-32].view(rows, n)
+                ws = torch.full((need + 256,), 0x7F, dtype=torch.uint8, device="cuda")
+                y.append(A.ivfpq_list_product_ex(x, w, o, out=out).clone())
+                g.append(A.ivfpq_list_product_grad_ex(grad, x, o, workspace=ws[:max(need, 16)]))
+                edge = torch.cat([guard[:32], guard[-32:]])
+                assert edge.isnan().all() if fill != fill else (edge == 0).all()
+                assert (ws[max(need, 16):] == 0x7F).all()
+            assert torch.equal(y[0], y[1]) and torch.equal(g[0], g[1])
+
+
+def test_rows_that_begin_at_any_element():
+    rng = np.random.default_rng(6)
+    for dtype in TYPES:
+        for shift in (1, 2, 3, 8):
+            for d in (64, 63):
+                base = integers(rng, 4 * 150 * 65 + 64, dtype=dtype)
+                x = base[shift:shift + 150 * d].view(150, d)
+                w = base[2 * shift + 150 * d:2 * shift + 150 * d + 3 * 40 * d].view(3, 40, d)
+                o = torch.tensor([0, 70, 71, 150], dtype=torch.int32, device="cuda")
+                want, _ = list_product64(np64(x), np64(w), o.tolist(), 150, np.arange(150), False)
+                assert np.array_equal(np64(A.ivfpq_list_product_ex(x, w, o)), rounded(want, dtype))
+                g = base[5 * shift:5 * shift + 150 * 40].view(150, 40)
+                got = A.ivfpq_list_product_grad_ex(g, x, o, dtype=torch.float32)
+                want = np.stack([np64(g)[lo:hi].T @ np64(x)[lo:hi]
+                                 for lo, hi in ((0, 70), (70, 71), (71, 150))])
+                assert np.array_equal(np64(got), want)
+
+
+def test_refusals_of_device_tensors():
+    x = torch.zeros((8, 16), device="cuda")
+    w = torch.zeros((2, 4, 16), device="cuda")
+    o = torch.zeros(3, dtype=torch.int32, device="cuda")
+    order = torch.zeros(8, dtype=torch.int32, device="cuda")
+    for call in (lambda: A.ivfpq_list_product_ex(x.t(), w, o),
+                 lambda: A.ivfpq_list_product_ex(x, w.transpose(1, 2), o, transposed=True),
+                 lambda: A.ivfpq_list_product_ex(x, w.to(torch.bfloat16), o),
+                 lambda: A.ivfpq_list_product_ex(x, w, o, transposed=True),
+                 lambda: A.ivfpq_list_product_ex(x, w, o[:2]),
+                 lambda: A.ivfpq_list_product_ex(x, w, o.long()),
+                 lambda: A.ivfpq_list_product_ex(x, w, o, order=order.view(4, 2)),
+                 lambda: A.ivfpq_list_product_ex(x, w, o, out=torch.zeros((8, 5), device="cuda")),
+                 lambda: A.ivfpq_list_product_grad_ex(x, x[:4], o),
+                 lambda: A.ivfpq_list_product_grad_ex(x, x, o, order=order[:7]),
+                 lambda: A.ivfpq_list_product_grad_ex(x, x, o[:1]),
+                 lambda: A.ivfpq_list_product_grad_ex(x, x, o, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: A.ivfpq_list_product_ex(x, w, o, order=order, k=0),
+                 lambda: A.ivfpq_list_product_grad_ex(x, x, o, dtype=torch.bfloat16)):
+        with pytest.raises(A.IVFPQError):
+            call()
+    assert A.ivfpq_list_product_ex(x[:0], w, o).shape == (0, 4)
+    assert (A.ivfpq_list_product_grad_ex(x[:0], x[:0], o) == 0).all()

@@ -47,3 +47,23 @@ def test_every_row_is_in_one_tile(driver):
                     cases.append(f"walk {tm} {rows} {nlist} " + " ".join(map(str, offsets)))
     for case, (slots, off, wrong, fewer) in zip(cases, driver(cases)):
         assert slots > 0 and off == 0 and wrong == 0 and fewer == 1, case
+
+
+def test_parts_of_a_list_cover_its_rows(driver):
+    cases = []
+    for splits in (1, 2, 4, 8, 64):
+        for p0 in (0, 5, 1000):
+            for n in (0, 1, 63, 64, 65, 128, 500, 4096, 4097, 100001):
+                cases.append(f"split {p0} {p0 + n} {splits}")
+    for case, (apart, left, uneven) in zip(cases, driver(cases)):
+        assert apart == 0 and left == 0 and uneven == 0, case
+
+
+def test_workgroups_share_a_list_only_where_tiles_are_few(driver):
+    cases = [(65536, 1, 2048, 2048), (65536, 8, 256, 256), (32768, 64, 2048, 2048), (2000, 16, 256, 128),
+             (100000, 2, 64, 64), (1 << 31, 1, 1, 1), (5000, 1, 1100, 2000)]
+    for (rows, nlist, n, d), (size, splits) in zip(
+            cases, driver([f"share {r} {l} {n} {d}" for r, l, n, d in cases])):
+        tiles = nlist * -(-n // size) * -(-d // size)
+        assert size in (128, 256) and 1 <= splits <= 64
+        assert splits == 1 or (splits * tiles <= 512 and rows // nlist >= splits * 512)
