@@ -18,24 +18,18 @@ namespace ivfpq {
 
 static int hidden_part(int r) { return (r + 7) / 8 * 8; }
 
-// Hidden rows are short and their contraction long, so they take the kernel of few rows,
-// of as many columns at once as they have.
+// Hidden rows are short and their contraction long, so they take the kernel of few rows: in
+// 16 x 16 blocks, whose eight waves share the contraction, up to a workgroup a CU; in
+// 32 x 32 from there on, which read the operands half as often.  bfloat16, d = 4096, the
+// whole call with 1024 columns: 1024 rows of one list, rank 64 (256 blocks): 36 us and
+// 44 in 32 x 32; 4096 rows of 16 lists, rank 64 (1056): 99 and 88.
 template <typename T>
 static hipError_t hidden_as(const ListJob &p, hipStream_t stream)
 {
     if (any_tiny<kHidden>(p))
         return launch_tiles<T, float, kHidden, 32, 2, 1, 2, 2, true>(p, stream);
-    const bool few = p.rows <= 16 * p.nlist;
-    if constexpr (sizeof(T) == 4) {
-        return few ? launch_direct<T, kHidden, 1, 1, 8, 2>(p, stream)
-                   : launch_direct<T, kHidden, 2, 2, 8, 1>(p, stream);
-    } else {
-        if (few)
-            return p.r <= 16 ? launch_direct<T, kHidden, 1, 1, 8, 2>(p, stream)
-                             : launch_direct<T, kHidden, 1, 4, 8, 1>(p, stream);
-        return p.r <= 16 ? launch_direct<T, kHidden, 4, 1, 8, 1>(p, stream)
-                         : launch_direct<T, kHidden, 2, 4, 8, 1>(p, stream);
-    }
+    return count_tiles<kHidden>(p, 16, 16) <= 256 ? launch_direct<T, kHidden, 1, 1, 8, 2>(p, stream)
+                                                  : launch_direct<T, kHidden, 2, 2, 8, 1>(p, stream);
 }
 
 template <typename T>
@@ -64,31 +58,40 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
     p.b = q.w;
     p.n = q.n;
     p.out = q.out;
-    // Few rows, or rows that the copies cannot read and too few tiles for all CUs.
     const bool copies = sizeof(T) == 2 && copies_fit<kAdapter>(p);
     const int64_t middle = count_tiles<kAdapter>(p, 128, 128);
-    if (!any_tiny<kAdapter>(p) && (p.rows <= 128 || (!copies && middle <= 64))) {
-        if (p.rows <= 16)
+    // Few rows: blocks whose waves share the contraction, the largest that still make a
+    // workgroup a CU.  16 rows of 4096 x 4096: 26 us in 16 x 16 blocks, 29 in 32 x 32, 44 in
+    // copied 32 x 128 tiles; 64 rows: 53, 33 and 44; 128: 90, 53 and 43; 32 rows of 11,008 x
+    // 4096: 73, 57 and 86.  Where the copies do not fit, up to two workgroups a CU: 256
+    // rows of 2048 x 2048 in float32 58 us, in 64 x 64 tiles 71; 512 rows: 99 and 74.
+    const int64_t blocks = count_tiles<kAdapter>(p, 32, 32);
+    if (!any_tiny<kAdapter>(p) && (p.rows <= 32 || blocks <= (copies ? 256 : 512))) {
+        if (p.rows <= 16 || count_tiles<kAdapter>(p, 16, 16) <= 256)
             return launch_direct<T, kAdapter, 1, 1, 8, 2>(p, stream);
-        if (p.rows <= 32)
+        if (count_tiles<kAdapter>(p, 32, 16) <= 256)
             return launch_direct<T, kAdapter, 2, 1, 8, 2>(p, stream);
         return launch_direct<T, kAdapter, 2, 2, 8, 1>(p, stream);
     }
     if constexpr (sizeof(T) == 2) {
         if (copies) {
-            if (middle <= 64)
-                return launch_copies<T, T, kAdapter, 64, 4, 1, 1, 1, 4>(p, stream);
-            if (middle <= 128)
-                return launch_copies<T, T, kAdapter, 64, 4, 1, 2, 2, 2>(p, stream);
-            if (middle <= 256)
-                return launch_copies<T, T, kAdapter, 64, 2, 1, 2, 2, 2>(p, stream);
-            if (3 * ((count_tiles<kAdapter>(p, 256, 256) + 255) / 256) <= (middle + 255) / 256)
-                return launch_copies<T, T, kAdapter, 64, 2, 4, 2, 2, 4>(p, stream);
-            return launch_copies<T, T, kAdapter, 64, 2, 2, 2, 2, 2>(p, stream);
+            switch (copy_tile(p.rows, p.nlist, p.n, p.kdim, false)) {
+            case 0: return launch_copies<T, T, kAdapter, 64, 4, 1, 1, 1, 4>(p, stream);
+            case 1: return launch_copies<T, T, kAdapter, 64, 4, 1, 2, 2, 2>(p, stream);
+            case 2: return launch_copies<T, T, kAdapter, 64, 2, 1, 2, 2, 2>(p, stream);
+            case 3: return launch_copies<T, T, kAdapter, 64, 4, 2, 2, 2, 2>(p, stream);
+            case 4: return launch_copies<T, T, kAdapter, 64, 2, 2, 2, 2, 2>(p, stream);
+            default: return launch_copies<T, T, kAdapter, 64, 2, 4, 2, 2, 4>(p, stream);
+            }
         }
     }
-    return middle <= 512 ? launch_tiles<T, T, kAdapter, 2 * KS, 1, 1, 2, 2>(p, stream)
-                         : launch_tiles<T, T, kAdapter, KS, 2, 2, 2, 2>(p, stream);
+    // Tiles of 64 x 64 or 128 x 128.  float32, 2048 x 2048: 1024 rows (128 of the larger) 92
+    // us and 131, 2048 rows (256) 152 and 139; bfloat16, 2001 x 2001: 4096 rows (512) 169
+    // and 177, 8192 307 and 320.
+    if constexpr (sizeof(T) == 4)
+        if (middle > 192)
+            return launch_tiles<T, T, kAdapter, KS, 2, 2, 2, 2>(p, stream);
+    return launch_tiles<T, T, kAdapter, 2 * KS, 1, 1, 2, 2>(p, stream);
 }
 
 size_t adapter_bytes(int64_t t, int r)

@@ -8,27 +8,31 @@ namespace ivfpq {
 template <typename T, int FORM>
 static hipError_t rows_as(const ListJob &p, hipStream_t stream)
 {
-    const int64_t middle = count_tiles<FORM>(p, 128, 128);
     if constexpr (sizeof(T) == 2) {
         if (copies_fit<FORM>(p)) {
-            const int64_t large = count_tiles<FORM>(p, 256, 256);
-            if (p.rows <= 16 * p.nlist)
-                return launch_copies<T, T, FORM, 64, 4, 1, 1, 1, 4>(p, stream);
-            if (p.rows > 256 * p.nlist && 3 * ((large + 255) / 256) <= (middle + 255) / 256)
-                return launch_copies<T, T, FORM, 64, 2, 4, 2, 2, 4>(p, stream);
-            if (p.rows <= 32 * p.nlist)
-                return launch_copies<T, T, FORM, 64, 2, 1, 2, 2, 2>(p, stream);
-            if (middle <= 192)
-                return launch_copies<T, T, FORM, 64, 4, 2, 2, 2, 2>(p, stream);
-            return launch_copies<T, T, FORM, 64, 2, 2, 2, 2, 2>(p, stream);
+            switch (copy_tile(p.rows, p.nlist, p.n, p.kdim, true)) {
+            case 0: return launch_copies<T, T, FORM, 64, 4, 1, 1, 1, 4>(p, stream);
+            case 1: return launch_copies<T, T, FORM, 64, 4, 1, 2, 2, 2>(p, stream);
+            case 2: return launch_copies<T, T, FORM, 64, 2, 1, 2, 2, 2>(p, stream);
+            case 3: return launch_copies<T, T, FORM, 64, 4, 2, 2, 2, 2>(p, stream);
+            case 4: return launch_copies<T, T, FORM, 64, 2, 2, 2, 2, 2>(p, stream);
+            default: return launch_copies<T, T, FORM, 64, 2, 4, 2, 2, 4>(p, stream);
+            }
         }
     }
     if constexpr (FORM == kRowsAlong) {
-        if (p.rows <= 4 * p.nlist && !any_tiny<FORM>(p))
+        // Few 16 x 32 tiles: their waves share the contraction.  float32, one list of 128
+        // rows, 1024 x 1024 (272 tiles): 15 us, in 64 x 64 tiles 22; 64 lists of 4 rows
+        // (1536): 80 and 67.
+        if (count_tiles<FORM>(p, 16, 32) <= 400 && !any_tiny<FORM>(p))
             return launch_direct<T, kRowsAlong, 1, 1, 4, 2>(p, stream);
     }
     constexpr int KS = sizeof(T) == 4 ? 16 : 32;
-    return p.rows <= 32 * p.nlist || middle <= 512
+    // Larger tiles where lists fill them and there are enough.  float32, 64 lists of
+    // 1024 x 1024, 64 rows each: 114 us in 64 x 64 tiles, 124 in 128 x 128; 512: 594 and
+    // 476.  8 lists of 1025 x 1025, bfloat16, 512 rows each (324 tiles): 58 and 58; 2048: 169
+    // and 148.
+    return p.rows <= 64 * p.nlist || count_tiles<FORM>(p, 128, 128) <= 512
                ? launch_tiles<T, T, FORM, 2 * KS, 1, 1, 2, 2>(p, stream)
                : launch_tiles<T, T, FORM, KS, 2, 2, 2, 2>(p, stream);
 }
@@ -69,7 +73,11 @@ static hipError_t gradient_as(const ListJob &p, int size, hipStream_t stream)
             return size == 256 ? launch_copies<T, TO, kGradient, 64, 2, 4, 2, 2, 4>(p, stream)
                                : launch_copies<T, TO, kGradient, 64, 2, 2, 2, 2, 2>(p, stream);
     }
-    return count_tiles<kGradient>(p, 128, 128) * p.splits > 512
+    // 64 x 64 tiles where larger ones leave CUs empty, float32 up to one tile a CU, 16-bit
+    // up to two: 256 rows a list, float32, 8 lists of 512 x 512 (128 tiles): 19 us in 64 x
+    // 64, 26 in 128 x 128; 16 lists (256): 34 and 30; bfloat16, 16 lists of 513 x 513
+    // (400): 25 and 25; 16 of 1025 x 1025 (1296): 64 and 59.
+    return count_tiles<kGradient>(p, 128, 128) * p.splits > (sizeof(T) == 4 ? 192 : 512)
                ? launch_tiles<T, TO, kGradient, KS, 2, 2, 2, 2>(p, stream)
                : launch_tiles<T, TO, kGradient, 32, 1, 1, 2, 2>(p, stream);
 }

@@ -55,14 +55,15 @@ int main()
         const int64_t slots = tile_slots(rows, nlist, tm);
         std::vector<int> seen(rows, 0);
         int64_t wrong = 0;
+        const int from = first_part(offsets.data());
         for (int64_t s = 0; s < slots; ++s) {
             int part = 0; // the last part that begins at or before the number
             for (int i = 0; i < nlist + 2; ++i)
-                if (part_slot(part_begin(offsets.data(), nlist, rows, i), i, tm, by_row) <= s)
+                if (part_slot(part_begin(offsets.data(), nlist, rows, i), i - from, tm, by_row) <= s)
                     part = i;
             const int64_t begin = part_begin(offsets.data(), nlist, rows, part);
             const int64_t end = part_begin(offsets.data(), nlist, rows, part + 1);
-            const int64_t p0 = slot_row(s, begin, end, part, tm, by_row);
+            const int64_t p0 = slot_row(s, begin, end, part - from, tm, by_row);
             const int64_t p1 = std::min(p0 + tm, end);
             if (p0 >= p1)
                 continue;
