@@ -53,8 +53,10 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
     tile.p0 = uniform(tile.p0);
     tile.p1 = uniform(tile.p1);
     const bool listed = FORM == kAdapter || (tile.e >= 0 && tile.e < p.nlist);
-    if (FORM == kHidden && !listed)
+    if (FORM == kHidden && !listed) {
+        no_list_rows(p, tile, n0 == 0, (int)threadIdx.x, 512);
         return;
+    }
 
     f32x4 acc[RT][CT];
 #pragma unroll

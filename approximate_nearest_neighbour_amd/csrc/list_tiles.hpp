@@ -355,6 +355,17 @@ __device__ __forceinline__ int64_t source_row(const ListJob &p, int64_t row)
     return q < p.arows ? q : -1;
 }
 
+// kHidden: the rows of a tile of no list have none.
+__device__ __forceinline__ void no_list_rows(const ListJob &p, const PartTile &tile, bool first,
+                                             int tid, int threads)
+{
+    for (int64_t row = tile.p0 + tid; first && row < tile.p1; row += threads) {
+        const int64_t t = source_row(p, row);
+        if (t >= 0)
+            p.row_list[t] = -1;
+    }
+}
+
 // The list of each row of a tile (-1: none), and these lists each once, ascending:
 // segs[0 .. segs[TM]).
 template <int TM, int THREADS>
@@ -367,7 +378,7 @@ __device__ __forceinline__ void find_lists(const ListJob &p, const PartTile &til
         int e = -1;
         if (row < tile.p1 && (uint32_t)p.pos[row] < (uint64_t)p.rows) {
             e = p.row_list[row];
-            e = e < p.nlist ? e : -1;
+            e = (uint32_t)e < (uint32_t)p.nlist ? e : -1;
         }
         tile_list[i] = e;
     }
@@ -557,8 +568,10 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
     const bool listed = FORM == kAdapter || (tile.e >= 0 && tile.e < p.nlist);
     const int64_t kdim = !listed ? 0 : FORM == kGradient ? max(tile.p1 - tile.p0, (int64_t)0)
                                                          : (int64_t)p.kdim;
-    if (FORM == kHidden && !listed)
+    if (FORM == kHidden && !listed) {
+        no_list_rows(p, tile, nt == 0, tid, THREADS);
         return;
+    }
 
     int64_t chunks = (kdim + KS - 1) / KS;
     const int64_t main_chunks = chunks;

@@ -579,7 +579,8 @@ size_t ivfpq_adapter_product_bytes(int64_t t, int r);
  * are those of one ivfpq_route_sort_ex of the rows' lists (k = 1), made once for
  * all products of the same rows; a row whose list is masked gets W x.  D_a x times
  * the scale is held in float32, for 16-bit types in two parts (binary16: below
- * 65504).  t = 0 is a no-op.  Its gradients come from ivfpq_list_product_ex and
+ * 65504); an infinity in D_a x or U_a gives infinities or NaN, in the rows of list a
+ * alone.  t = 0 is a no-op.  Its gradients come from ivfpq_list_product_ex and
  * ivfpq_list_product_grad_ex of the sorted rows.  Errors as above, with r in [1,
  * 2^12]. */
 ivfpq_status ivfpq_adapter_product_ex(const void *rows_dev, int type, int64_t t, int d,

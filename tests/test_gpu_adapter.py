@@ -160,3 +160,21 @@ def test_refusals_of_device_tensors():
     with pytest.raises(A.IVFPQError):
         A.ivfpq_adapter_product_ex(x, w, down, up, o, order, order, workspace=small)
     assert A.ivfpq_adapter_product_ex(x[:0], w, down, up, o, order[:0], order[:0]).shape == (0, 4)
+
+
+def test_rows_outside_the_lists_take_the_shared_product_alone():
+    """offsets narrower than the sort's: what lies outside belongs to no list, whatever
+    the workspace held."""
+    rng = np.random.default_rng(7)
+    for dtype in TYPES:
+        for t, n, d, r in ((40, 48, 64, 4), (300, 260, 72, 8), (33, 1, 3, 1)):
+            x, w = integers(rng, t, d, dtype=dtype), integers(rng, n, d, dtype=dtype)
+            down, up = integers(rng, 3, r, d, dtype=dtype), integers(rng, 3, n, r, dtype=dtype)
+            order = torch.arange(t, dtype=torch.int32, device="cuda")
+            ws = torch.zeros(A.ivfpq_adapter_product_bytes(t, r), dtype=torch.uint8, device="cuda")
+            offsets = torch.tensor([10, 15, 15, 30], dtype=torch.int32, device="cuda")
+            y = A.ivfpq_adapter_product_ex(x, w, down, up, offsets, order, order, workspace=ws)
+            lists = np.full(t, -1)
+            lists[10:15], lists[15:30] = 0, 2
+            want, _ = adapter64(np64(x), np64(w), np64(down), np64(up), lists, None)
+            assert np.array_equal(np64(y), np64(torch.from_numpy(want).to(dtype)))
