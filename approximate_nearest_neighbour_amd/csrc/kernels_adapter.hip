@@ -85,12 +85,17 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
             }
         }
     }
-    // Tiles of 64 x 64 or 128 x 128.  float32, 2048 x 2048: 1024 rows (128 of the larger) 92
-    // us and 131, 2048 rows (256) 152 and 139; bfloat16, 2001 x 2001: 4096 rows (512) 169
-    // and 177, 8192 307 and 320.
-    if constexpr (sizeof(T) == 4)
+    // In float32 tiles of 64 x 64 or 128 x 128: 2048 x 2048, 1024 rows (128 of the larger)
+    // 92 us and 131, 2048 rows (256) 152 and 139.  In 16 bits of 64 x 64, or of 64 x 128 by
+    // eight waves where those would take more than a turn of two a CU: 2001 x 2001, 2048 rows
+    // 93 us and 82, 4096 167 and 146 (128 x 128 tiles: 190).
+    if constexpr (sizeof(T) == 4) {
         if (middle > 192)
             return launch_tiles<T, T, kAdapter, KS, 2, 2, 2, 2>(p, stream);
+    } else {
+        if (count_tiles<kAdapter>(p, 64, 64) > 512)
+            return launch_tiles<T, T, kAdapter, 2 * KS, 1, 1, 2, 4>(p, stream);
+    }
     return launch_tiles<T, T, kAdapter, 2 * KS, 1, 1, 2, 2>(p, stream);
 }
 

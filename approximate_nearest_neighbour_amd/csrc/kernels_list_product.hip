@@ -32,9 +32,15 @@ static hipError_t rows_as(const ListJob &p, hipStream_t stream)
     // 1024 x 1024, 64 rows each: 114 us in 64 x 64 tiles, 124 in 128 x 128; 512: 594 and
     // 476.  8 lists of 1025 x 1025, bfloat16, 512 rows each (324 tiles): 58 and 58; 2048: 169
     // and 148.
-    return p.rows <= 64 * p.nlist || count_tiles<FORM>(p, 128, 128) <= 512
-               ? launch_tiles<T, T, FORM, 2 * KS, 1, 1, 2, 2>(p, stream)
-               : launch_tiles<T, T, FORM, KS, 2, 2, 2, 2>(p, stream);
+    if (p.rows > 64 * p.nlist && count_tiles<FORM>(p, 128, 128) > 512)
+        return launch_tiles<T, T, FORM, KS, 2, 2, 2, 2>(p, stream);
+    // 64 x 64 tiles, two a CU; in 16 bits 64 x 128 by eight waves where those would take a
+    // second turn.  Both ways through 16 lists of 1281 x 1281, 128 rows each: 119 us and
+    // 99; 8 lists of 1025 x 1025, 64 rows each (204 tiles): 37 and 39.
+    if constexpr (sizeof(T) == 2)
+        if (count_tiles<FORM>(p, 64, 64) > 512)
+            return launch_tiles<T, T, FORM, 2 * KS, 1, 1, 2, 4>(p, stream);
+    return launch_tiles<T, T, FORM, 2 * KS, 1, 1, 2, 2>(p, stream);
 }
 
 template <typename T>
