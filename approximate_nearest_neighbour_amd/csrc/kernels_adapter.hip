@@ -19,17 +19,23 @@ namespace ivfpq {
 static int hidden_part(int r) { return (r + 7) / 8 * 8; }
 
 // Hidden rows are short and their contraction long, so they take the kernel of few rows: in
-// 16 x 16 blocks, whose eight waves share the contraction, up to a workgroup a CU; in
-// 32 x 32 from there on, which read the operands half as often.  bfloat16, d = 4096, the
-// whole call with 1024 columns: 1024 rows of one list, rank 64 (256 blocks): 36 us and
-// 44 in 32 x 32; 4096 rows of 16 lists, rank 64 (1056): 99 and 88.
+// 16 x 16 blocks, whose eight waves share the contraction, up to a workgroup a CU; from
+// there on in 32 x 32, which read the operands half as often; from four such blocks a
+// CU on, if the copies fit, in copied tiles of 64 x 64.  bfloat16, d = 4096, the whole
+// call with 1024 columns, rank 64: 1024 rows of one list (256 blocks) 34 us, 43 and 40;
+// 2048 of 16 lists (544) 64, 50 and 55; 8192 of 16 lists (2080) 161, 123 and 97.
 template <typename T>
 static hipError_t hidden_as(const ListJob &p, hipStream_t stream)
 {
     if (any_tiny<kHidden>(p))
         return launch_tiles<T, float, kHidden, 32, 2, 1, 2, 2, true>(p, stream);
-    return count_tiles<kHidden>(p, 16, 16) <= 256 ? launch_direct<T, kHidden, 1, 1, 8, 2>(p, stream)
-                                                  : launch_direct<T, kHidden, 2, 2, 8, 1>(p, stream);
+    const int64_t blocks = count_tiles<kHidden>(p, 16, 16);
+    if (blocks <= 256)
+        return launch_direct<T, kHidden, 1, 1, 8, 2>(p, stream);
+    if constexpr (sizeof(T) == 2)
+        if (blocks > 1024 && copies_fit<kHidden>(p))
+            return launch_copies<T, float, kHidden, 64, 4, 1, 1, 2, 2>(p, stream);
+    return launch_direct<T, kHidden, 2, 2, 8, 1>(p, stream);
 }
 
 template <typename T>

@@ -426,6 +426,42 @@ __device__ __forceinline__ void operands_of(const Eight<T, ODD> &x, s16x8 (&out)
     }
 }
 
+// A wave's hidden rows (not dealt: a lane has one column of sixteen rows), and the rows'
+// lists.  `p0`, `n0`: the wave's first row and column.
+template <typename T, int WM, int WN>
+__device__ __forceinline__ void store_hidden(const ListJob &p, const PartTile &tile, int64_t p0,
+                                             int n0, bool first, int threads,
+                                             const f32x16 (&acc)[WM][WN])
+{
+    const int r = lane_id() & 31, half = lane_id() >> 5;
+    const float scale = p.scales ? p.scales[tile.e] : 1.f;
+    for (int64_t row = tile.p0 + threadIdx.x; first && row < tile.p1; row += threads) {
+        const int64_t t = source_row(p, row);
+        if (t >= 0)
+            p.row_list[t] = tile.e;
+    }
+#pragma unroll
+    for (int j = 0; j < WN; ++j) {
+        const int col = n0 + j * 32 + r;
+        if (col >= p.rp)
+            continue;
+#pragma unroll
+        for (int i = 0; i < WM; ++i)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const int64_t row = p0 + i * 32 + (q >> 2) * 8 + half * 4 + (q & 3);
+                const int64_t t = row < tile.p1 ? source_row(p, row) : -1;
+                if (t < 0)
+                    continue;
+                const float h = col < p.r ? acc[i][j][q] * scale : 0.f;
+                T *to = static_cast<T *>(p.hidden) + t * p.width + col;
+                to[0] = (T)h;
+                if constexpr (Parts<T>::N == 1)
+                    to[p.rp] = (T)(h - (float)to[0]);
+            }
+    }
+}
+
 // The adapter kernels multiply a tile's rows with the up matrices of all its lists, with
 // zeros for the hidden rows of the other lists; an up matrix that holds an infinity or
 // NaN would so reach rows of other lists.  So a wave with a sum that is not finite, in
@@ -896,36 +932,8 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
     const int64_t row_base = FORM == kGradient ? matrix * p.m + m0 : tile.p0;
     const int64_t row_end = FORM == kGradient ? (matrix + 1) * p.m : tile.p1;
     if constexpr (FORM == kHidden) {
-        // a lane has one column of sixteen rows (PAIR is false: TO is float)
         static_assert(!PAIR, "hidden rows");
-        const float scale = p.scales ? p.scales[tile.e] : 1.f;
-        if (nt == 0)
-            for (int64_t row = tile.p0 + tid; row < tile.p1; row += THREADS) {
-                const int64_t t = source_row(p, row);
-                if (t >= 0)
-                    p.row_list[t] = tile.e;
-            }
-#pragma unroll
-        for (int j = 0; j < WN; ++j) {
-            const int col = n0 + (wn * WN + j) * 32 + r;
-            if (col >= p.rp)
-                continue;
-#pragma unroll
-            for (int i = 0; i < WM; ++i)
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const int64_t row =
-                        row_base + (wm * WM + i) * 32 + (q >> 2) * 8 + half * 4 + (q & 3);
-                    const int64_t t = row < row_end ? source_row(p, row) : -1;
-                    if (t < 0)
-                        continue;
-                    const float h = acc[i][j][q] * scale; // zero past column r
-                    T *to = static_cast<T *>(p.hidden) + t * p.width + col;
-                    to[0] = (T)h;
-                    if constexpr (NP == 1)
-                        to[p.rp] = (T)(h - (float)to[0]);
-                }
-        }
+        store_hidden<T>(p, tile, tile.p0 + wm * WM * 32, n0 + wn * WN * 32, nt == 0, THREADS, acc);
         return;
     }
     TO *out = static_cast<TO *>(p.out);
@@ -1051,6 +1059,10 @@ void list_copy_kernel(ListJob p, TileGroups groups)
     tile.p1 = uniform(tile.p1);
     tile.e = __builtin_amdgcn_readfirstlane(tile.e);
     const bool listed = FORM == kAdapter || (tile.e >= 0 && tile.e < p.nlist);
+    if (FORM == kHidden && !listed) {
+        no_list_rows(p, tile, nt == 0, tid, THREADS);
+        return;
+    }
     const int64_t kdim = !listed ? 0 : FORM == kGradient ? max(tile.p1 - tile.p0, (int64_t)0)
                                                          : (int64_t)p.kdim;
     int chunks = (int)((kdim + KS - 1) / KS); // a list has fewer than 2^31 rows
@@ -1353,6 +1365,11 @@ void list_copy_kernel(ListJob p, TileGroups groups)
         keep_lists_apart<T, PAIR>(p, tile, tile.p0 + wm * WM * 32, n0 + wn * WN * 32,
                                   tile_list + wm * WM * 32, segs, segs[TM], acc);
 
+    if constexpr (FORM == kHidden) {
+        static_assert(!PAIR, "hidden rows");
+        store_hidden<T>(p, tile, tile.p0 + wm * WM * 32, n0 + wn * WN * 32, nt == 0, THREADS, acc);
+        return;
+    }
     const int r = lane & 31, half = lane >> 5;
     const int64_t matrix = FORM == kGradient ? (int64_t)split * p.nlist + tile.e : 0;
     const int64_t row_base = FORM == kGradient ? matrix * p.m + m0 : tile.p0;

@@ -28,7 +28,7 @@ SHAPES = [(1, 8, 8, 1, 1), (1, 256, 128, 4, 16), (5, 33, 17, 3, 7), (16, 64, 64,
           (300, 130, 96, 3, 24), (700, 72, 64, 9, 40), (513, 257, 520, 2, 130),
           # every kind of tile: few and many of each size
           (200, 1000, 64, 3, 8), (500, 4000, 40, 2, 8), (1000, 4000, 24, 2, 16),
-          (1300, 4200, 24, 3, 8), (2048, 4200, 32, 2, 8), (2100, 4201, 23, 2, 5)]
+          (1300, 4200, 24, 3, 8), (2048, 4200, 32, 2, 8), (2100, 4201, 23, 2, 5), (4200, 72, 64, 3, 64), (4300, 40, 72, 5, 61)]
 
 
 def lists_of(rng, t, nlist, kind):
@@ -103,7 +103,7 @@ def test_adapters_of_reals(t, n, d, nlist, r, dtype):
 @pytest.mark.parametrize("t,n,d,nlist,r", [(20, 40, 64, 4, 8), (150, 257, 65, 3, 5), (300, 1000, 64, 3, 8),
                                           (500, 4000, 16, 5, 8), (1000, 4000, 24, 4, 16),
                                           (1300, 4200, 24, 9, 8), (2048, 4200, 32, 6, 8),
-                                          (2100, 4201, 23, 5, 5)])
+                                          (2100, 4201, 23, 5, 5), (4200, 72, 136, 5, 64)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_bad_values_stay_where_they_are(t, n, d, nlist, r, dtype):
     """What is wrong in one row, or in the matrices of one list, reaches no other row."""
