@@ -8,6 +8,10 @@
 // its row: whole lines of memory for 16-bit rows.  Two turns of TURN units are under
 // way, one of them while the other is multiplied.  Rows may begin at any address.
 //
+// 32 rows of 4096 x 4096 with their adapters: 20 us for the shared product (34 MB, which
+// partly stay in the caches), 10 for the hidden rows of rank 16: there a chain of search,
+// row numbers, loads and join.
+//
 // An adapter's hidden rows are multiplied with the up matrices after the shared ones:
 // the lists of the tile's rows are dealt to the KW waves.  A lane's results are of one
 // row, and keep what they were where the list is not the row's.
