@@ -95,3 +95,43 @@ def test_rows(d):
     assert np.array_equal(np64(y[at]), np64(torch.from_numpy(exact).to(BF)))
     y[at] = 0
     assert not y.any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("n,d", [(3, 1 << 20), (1 << 20, 3), (8, (1 << 20) - 1)])
+def test_the_widest_rows(n, d, dtype):
+    rng = np.random.default_rng(n)
+    x, w = integers(rng, 5, d, dtype=dtype, top=1), integers(rng, 2, n, d, dtype=dtype, top=1)
+    offsets, order = cuda(0, 2, 5), cuda(4, 0, 2, 2, 1)
+    y = A.ivfpq_list_product_ex(x, w, offsets, order=order)
+    rows = np64(x)[order.tolist()]
+    want = np.concatenate([rows[:2] @ np64(w[0]).T, rows[2:] @ np64(w[1]).T])
+    assert np.array_equal(np64(y), np64(torch.from_numpy(want).to(dtype)))
+    wt = w.transpose(1, 2).contiguous()
+    assert torch.equal(A.ivfpq_list_product_ex(x, wt, offsets, order=order, transposed=True), y)
+    g = integers(rng, 5, n, dtype=dtype, top=1)
+    got = A.ivfpq_list_product_grad_ex(g, x, offsets, order=order, dtype=torch.float32)
+    for e, (lo, hi) in enumerate(((0, 2), (2, 5))):
+        assert np.array_equal(np64(got[e]), np64(g)[lo:hi].T @ rows[lo:hi])
+    offsets, order, pos = A.ivfpq_route_sort_ex(cuda(1, -1, 0, 1, 1).view(-1, 1), 2)
+    grad = A.ivfpq_table_grad_ex(x, offsets, order, dtype=torch.float32)
+    assert np.array_equal(np64(grad), np.stack([np64(x)[2], np64(x)[[0, 3, 4]].sum(0)]))
+    assert torch.equal(A.ivfpq_table_lookup_ex(x, cuda(4, 9)), torch.stack([x[4], x[4] * 0]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("t", [3, 100, 300])
+def test_the_highest_rank(t, dtype):
+    n, d, r, nlist = 600, 64, 1 << 12, 3
+    rng = np.random.default_rng(t)
+    x, w = integers(rng, t, d, dtype=dtype, top=1), integers(rng, n, d, dtype=dtype, top=1)
+    down = integers(rng, nlist, r, d, dtype=dtype, top=1)
+    up = integers(rng, nlist, n, r, dtype=dtype, top=1)
+    lists = rng.integers(-1, nlist, t)
+    y = A.ivfpq_adapter_product_ex(x, w, down, up, *A.ivfpq_route_sort_ex(
+        torch.from_numpy(lists[:, None].astype(np.int32)).cuda(), nlist))
+    want = np64(x) @ np64(w).T
+    for e in range(nlist):
+        mine = lists == e
+        want[mine] += np64(x)[mine] @ np64(down[e]).T @ np64(up[e]).T
+    assert np.array_equal(np64(y), np64(torch.from_numpy(want).to(dtype)))
