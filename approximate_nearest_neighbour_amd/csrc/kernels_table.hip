@@ -371,7 +371,7 @@ __global__ __launch_bounds__(256) void table_grad_wave_kernel(TableGrad g, int64
     while (at < count) {
         // the slots of the next 64 positions, of which eight at a time are taken
         const int base = p, last = begin_of(count);
-        const int mine = base + lane < last ? g.order[base + lane] : -1;
+        const int mine = position_before(base, lane, last) ? g.order[base + lane] : -1;
         const int row = mine >= 0 ? (int)g.k.div((uint32_t)mine) : -1;
         while (at < count && p - base < 64 && p >= base) {
             // p is before the end of its list (and that past `last` only if the offsets do

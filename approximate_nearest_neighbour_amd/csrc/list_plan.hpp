@@ -70,6 +70,13 @@ __host__ __device__ inline void split_rows(int64_t &p0, int64_t &p1, int s, int 
     p1 = p0 + per < end ? p0 + per : end;
 }
 
+// Whether position base + lane is before `last`, for positions that fit 32 bits and 64
+// lanes: their sum may not fit (base from 2^31 - 63 on), their distance does.
+__host__ __device__ inline bool position_before(int base, int lane, int last)
+{
+    return lane < last - base;
+}
+
 // A kind of tile that 16-bit operands are copied for: tm x tn results, `per_cu`
 // workgroups a CU; a chunk of 64 takes `alone` us where no CU has more workgroups than it
 // holds, those of 256 tiles `full` us where all have many, and matrices come from

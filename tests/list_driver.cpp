@@ -1,7 +1,8 @@
 // Runs the arithmetic of csrc/list_plan.hpp on the CPU.  A line "split P0 P1 SPLITS"
 // prints: parts that do not follow each other, rows not in them, parts but the last
 // that are no whole chunks.  "share ROWS NLIST N D" prints the gradient's tile size
-// and splits.  A line "walk TM ROWS NLIST
+// and splits.  "batch BASE LAST" prints how many of 64 lanes have a position from BASE on
+// before LAST, and how many of those have none.  A line "walk TM ROWS NLIST
 // offsets..." prints: tile numbers, rows covered not exactly once, tiles that do not
 // start and end inside one part, and whether the fewer numbers of both ways were taken.
 #include "list_plan.hpp"
@@ -45,6 +46,17 @@ int main()
             in >> rows >> nlist >> n >> d;
             const GradientShare g = gradient_share(rows, nlist, n, d);
             std::printf("share %d %d\n", g.size, g.splits);
+            continue;
+        }
+        if (word == "batch") {
+            int base, last, count = 0, wrong = 0;
+            in >> base >> last;
+            for (int lane = 0; lane < 64; ++lane)
+                if (position_before(base, lane, last)) {
+                    ++count;
+                    wrong += (int64_t)base + lane >= last;
+                }
+            std::printf("batch %d %d\n", count, wrong);
             continue;
         }
         in >> tm >> rows >> nlist;

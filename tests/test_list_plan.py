@@ -67,3 +67,13 @@ def test_workgroups_share_a_list_only_where_tiles_are_few(driver):
         tiles = nlist * -(-n // size) * -(-d // size)
         assert size in (128, 256) and 1 <= splits <= 64
         assert splits == 1 or (splits * tiles <= 512 and rows // nlist >= splits * 512)
+
+
+def test_positions_of_a_batch_end_where_the_lists_do(driver):
+    """Also where a position and a lane's number have no sum in 32 bits."""
+    top = 2 ** 31 - 1
+    cases = [(base, last) for last in (0, 1, 63, 64, 65, 1000, top - 64, top - 1, top)
+             for base in (0, last - 65, last - 64, last - 63, last - 1, last, last + 1, top - 1)
+             if 0 <= base <= top]
+    for (base, last), (count, wrong) in zip(cases, driver([f"batch {b} {e}" for b, e in cases])):
+        assert count == min(max(last - base, 0), 64) and wrong == 0, (base, last)
