@@ -54,9 +54,11 @@ __global__ __launch_bounds__(256) void table_lookup_kernel(const T *__restrict__
         const int64_t row = i0 + i * step;
         if (row >= n)
             break;
+        // zero whatever the factor is where there is no row
+        const float factor = (uint64_t)id[i] < (uint64_t)rows ? scale : 0.f;
 #pragma unroll
         for (int e = 0; e < N; ++e)
-            v[i].v[e] *= scale;
+            v[i].v[e] *= factor;
         v[i].store(out + row * d + c, d - c);
     }
 }
@@ -319,7 +321,7 @@ __global__ __launch_bounds__(256) void table_grad_kernel(TableGrad g, int64_t gr
         s.add_rows(static_cast<const T *>(g.grad), g.nvec, g.k, g.d, at, g.order, lo, hi);
     else
         add_spans(s, g, lo, hi, at);
-    s.store(static_cast<TO *>(g.out) + l * g.d, g.d, at, g.scale);
+    s.store(static_cast<TO *>(g.out) + l * g.d, g.d, at, lo < hi ? g.scale : 0.f);
 }
 
 // The same for longer rows: a wave has 512 columns of up to kTableRows lists in a row.
@@ -351,8 +353,8 @@ __global__ __launch_bounds__(256) void table_grad_wave_kernel(TableGrad g, int64
     s.clear();
     int at = 0; // list that is being summed, its next position and its end
     int p = 0, end = 0;
-    auto put = [&](int list) {
-        s.template store<NT>(static_cast<TO *>(g.out) + (l0 + list) * g.d, g.d, cols, g.scale);
+    auto put = [&](int list, float scale) { // an empty list's with 0, whatever the factor is
+        s.template store<NT>(static_cast<TO *>(g.out) + (l0 + list) * g.d, g.d, cols, scale);
         s.clear();
     };
     // On to the first list from `at` on that has positions to sum; empty ones are stored,
@@ -364,7 +366,7 @@ __global__ __launch_bounds__(256) void table_grad_wave_kernel(TableGrad g, int64
             if (end > p && end - p <= g.span)
                 return;
             if (end <= p)
-                put(at);
+                put(at, 0.f);
         }
     };
     advance();
@@ -390,7 +392,7 @@ __global__ __launch_bounds__(256) void table_grad_wave_kernel(TableGrad g, int64
                     s.add(b, i);
                     ++p;
                     if (p == end) {
-                        put(at++);
+                        put(at++, g.scale);
                         advance();
                     }
                 }
@@ -401,7 +403,7 @@ __global__ __launch_bounds__(256) void table_grad_wave_kernel(TableGrad g, int64
         const int lo = begin_of(at), hi = begin_of(at + 1);
         if (hi - lo > g.span) {
             add_spans(s, g, lo, hi, cols);
-            put(at);
+            put(at, g.scale);
         }
     }
 }

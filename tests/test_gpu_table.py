@@ -160,3 +160,24 @@ def test_sums_of_the_lists_vectors():
     got = A.ivfpq_table_grad_ex(x, offsets, order, k=2)
     want, _ = R.table_gradient(np64(x), lists, 12, 1.0)
     assert np.array_equal(np64(got), want)
+
+
+@pytest.mark.parametrize("scale", [float("inf"), float("nan"), -1.0])
+@pytest.mark.parametrize("d", [5, 40, 520])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_that_are_not_there_are_zero_whatever_the_factor(dtype, d, scale):
+    table = torch.ones((9, d), dtype=dtype, device="cuda")
+    ids = torch.tensor([-1, 9, 3, 2 ** 31 - 1, 0, -7], dtype=torch.int32, device="cuda")
+    out = A.ivfpq_table_lookup_ex(table, ids, scale=scale)
+    want = torch.zeros((6, d), dtype=dtype)
+    want[[2, 4]] = scale
+    assert torch.equal(out.cpu().nan_to_num(7.0), want.nan_to_num(7.0))
+    # lists 0, 3 and 8 have one row each, 5 a long one, the others none
+    ids = torch.full((400,), 5, dtype=torch.int32)
+    ids[:4] = torch.tensor([0, 3, 8, -1])
+    offsets, order, _ = A.ivfpq_route_sort_ex(ids.view(-1, 1).cuda(), 9)
+    got = A.ivfpq_table_grad_ex(torch.ones((400, d), dtype=dtype, device="cuda"), offsets, order,
+                                scale=scale)
+    want = torch.zeros((9, d), dtype=dtype)
+    want[[0, 3, 8]], want[5] = scale, 396 * scale
+    assert torch.equal(got.cpu().nan_to_num(7.0), want.nan_to_num(7.0))
