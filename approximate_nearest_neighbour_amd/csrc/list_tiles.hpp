@@ -465,9 +465,15 @@ __device__ __forceinline__ void store_hidden(const ListJob &p, const PartTile &t
 // The adapter kernels multiply a tile's rows with the up matrices of all its lists, with
 // zeros for the hidden rows of the other lists; an up matrix that holds an infinity or
 // NaN would so reach rows of other lists.  So a wave with a sum that is not finite, in
-// a tile of several lists, forms its sums again, each row's with the row's list alone.
+// a tile of several lists, looks for such a value in the up matrices' rows of its
+// columns, and if there is one forms its sums again, each row's with the row's list
+// alone: in the same steps, so that rows without such a value keep their sums to the
+// last bit.  What is not finite in a row of x, or in its hidden row, stays in that row
+// anyway.  8192 rows of 16 lists, 4096 x 4096, rank 64, bfloat16: 264 us, with a NaN in
+// every row of x 258 (6.0 ms if those waves formed their sums again), with one in an up
+// matrix 730.
 // `p0`, `n0`: the wave's first row and column; `lists`: its rows' lists.
-template <typename T, bool PAIR, int WM, int WN>
+template <typename T, bool PAIR, bool TINY, int WM, int WN>
 __device__ __forceinline__ void keep_lists_apart(const ListJob &p, const PartTile &tile, int64_t p0,
                                                  int n0, const int *lists, const int *segs,
                                                  int count, f32x16 (&acc)[WM][WN])
@@ -490,13 +496,6 @@ __device__ __forceinline__ void keep_lists_apart(const ListJob &p, const PartTil
                 zero = __builtin_fmaf(acc[i][j][q], 0.f, zero);
     if (count == 0 || !__any(mixed) || !__any(zero != 0.f))
         return;
-#pragma unroll
-    for (int i = 0; i < WM; ++i)
-#pragma unroll
-        for (int j = 0; j < WN; ++j)
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-                acc[i][j][q] = 0.f;
     int64_t rows[WM], cols[WN];
 #pragma unroll
     for (int i = 0; i < WM; ++i)
@@ -508,11 +507,32 @@ __device__ __forceinline__ void keep_lists_apart(const ListJob &p, const PartTil
     const int64_t all_hidden = p.rows * p.width, all_up = (int64_t)p.nlist * p.n * p.r;
     auto operand = [&](const void *array, int64_t at, int64_t all, int left, s16x8 (&to)[NP]) {
         Values x;
-        x.template read_near<true>(static_cast<const T *>(array), at, all);
+        x.template read_near<TINY>(static_cast<const T *>(array), at, all);
         x.ready();
-        x.template settle<true>(at, all, left);
+        x.template settle<TINY>(at, all, left);
         operands_of(x, to);
     };
+    bool bad = false; // a part that is not finite: its exponent's bits are all ones
+    for (int s = 0; s < count; ++s)
+        for (int k0 = half * 8; k0 < p.r; k0 += 16)
+#pragma unroll
+            for (int j = 0; j < WN; ++j) {
+                s16x8 o[NP];
+                operand(p.up, ((int64_t)segs[s] * p.n + cols[j]) * p.r + k0, all_up, p.r - k0, o);
+                constexpr int ONES = std::is_same<E, __bf16>::value ? 0x7F80 : 0x7C00;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    bad = bad || (o[0][q] & ONES) == ONES;
+            }
+    if (!__any(bad))
+        return;
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+                acc[i][j][q] = 0.f;
     // seg: the list whose rows take the products (-1: all rows do)
     auto products = [&](const s16x8 (&oa)[NP], const s16x8 (&ob)[NP], int i, f32x16 &c, int seg) {
         f32x16 d = c;
@@ -929,8 +949,8 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
         }
     }
     if constexpr (FORM == kAdapter)
-        keep_lists_apart<T, PAIR>(p, tile, tile.p0 + wm * WM * 32, n0 + wn * WN * 32,
-                                  tile_list + wm * WM * 32, segs, segs[TM], acc);
+        keep_lists_apart<T, PAIR, TINY>(p, tile, tile.p0 + wm * WM * 32, n0 + wn * WN * 32,
+                                        tile_list + wm * WM * 32, segs, segs[TM], acc);
 
     const int r = lane & 31, half = lane >> 5;
     const int64_t matrix = FORM == kGradient ? (int64_t)split * p.nlist + tile.e : 0;
@@ -1372,8 +1392,8 @@ void list_copy_kernel(ListJob p, TileGroups groups)
     }
     wait_vm<0>(); // no copy is under way to where results may go, or past the end
     if constexpr (FORM == kAdapter)
-        keep_lists_apart<T, PAIR>(p, tile, tile.p0 + wm * WM * 32, n0 + wn * WN * 32,
-                                  tile_list + wm * WM * 32, segs, segs[TM], acc);
+        keep_lists_apart<T, PAIR, false>(p, tile, tile.p0 + wm * WM * 32, n0 + wn * WN * 32,
+                                         tile_list + wm * WM * 32, segs, segs[TM], acc);
 
     if constexpr (FORM == kHidden) {
         static_assert(!PAIR, "hidden rows");

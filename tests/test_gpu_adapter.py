@@ -178,3 +178,62 @@ def test_rows_outside_the_lists_take_the_shared_product_alone():
             lists[10:15], lists[15:30] = 0, 2
             want, _ = adapter64(np64(x), np64(w), np64(down), np64(up), lists, None)
             assert np.array_equal(np64(y), np64(torch.from_numpy(want).to(dtype)))
+
+
+# a shape for every kernel that forms the results: blocks of few rows (16 x 16, 32 x 16,
+# 32 x 32), copied tiles of every size, tiles through registers of every size
+TILES = [(20, 40, 64, 4, 8), (33, 65, 77, 6, 7), (64, 1500, 64, 3, 16), (129, 1500, 64, 3, 16),
+         (150, 257, 65, 3, 5), (300, 4000, 64, 3, 8), (500, 4000, 40, 5, 8), (1000, 4000, 24, 4, 16),
+         (1300, 4200, 24, 9, 8), (2048, 4200, 32, 6, 8), (600, 1001, 25, 4, 5),
+         (2100, 4201, 23, 5, 5), (4200, 72, 136, 5, 64)]
+
+
+@pytest.mark.parametrize("t,n,d,nlist,r", TILES)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_bad_values_change_no_other_rounding(t, n, d, nlist, r, dtype):
+    """Real values: what a row or a list's matrices hold leaves every other row's sums as
+    they are, to the last bit."""
+    rng = np.random.default_rng(t + 1)
+    x, w = reals(rng, t, d, dtype=dtype), reals(rng, n, d, dtype=dtype)
+    down, up = reals(rng, nlist, r, d, dtype=dtype), reals(rng, nlist, n, r, dtype=dtype)
+    lists = rng.integers(-1, nlist, t).astype(np.int32)
+    lists[:4] = [0, -1, 1, 1]
+    clean = call(x, w, down, up, lists, None)
+    x[[1, 3, t - 1]] = torch.tensor([[float("inf")], [float("nan")], [float("-inf")]],
+                                    device="cuda").to(dtype)
+    up[0, n // 2], down[nlist - 1, 0, 0] = float("inf"), float("nan")
+    got = call(x, w, down, up, lists, None)
+    hit = (lists == 0) | (lists == nlist - 1)
+    hit[[1, 3, t - 1]] = True
+    rest = np.flatnonzero(~hit)
+    assert len(rest) and torch.equal(got[rest], clean[rest])
+    assert not got[0, n // 2].isfinite() and not got[[1, 3, t - 1]].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_that_are_not_finite_cost_no_second_product(dtype):
+    """A NaN in every row of x (a value that overflowed) takes the time of a clean batch;
+    where each such tile formed its sums again it took more than ten times that."""
+    t, n, d, nlist, r = 4096, 2048, 2048, 8, 16
+    rng = np.random.default_rng(5)
+    x, w = reals(rng, t, d, dtype=dtype), reals(rng, n, d, dtype=dtype)
+    down, up = reals(rng, nlist, r, d, dtype=dtype), reals(rng, nlist, n, r, dtype=dtype)
+    lists = torch.from_numpy(rng.integers(-1, nlist, (t, 1)).astype(np.int32)).cuda()
+    plan = A.ivfpq_route_sort_ex(lists, nlist)
+    bad = x.clone()
+    bad[:, 7] = float("nan")
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+
+    def least(rows):
+        times = []
+        for _ in range(6):
+            ends[0].record()
+            for _ in range(3):
+                A.ivfpq_adapter_product_ex(rows, w, down, up, *plan)
+            ends[1].record()
+            ends[1].synchronize()
+            times.append(ends[0].elapsed_time(ends[1]))
+        return min(times)
+
+    clean_ms, bad_ms = least(x), least(bad)
+    assert bad_ms < 4 * clean_ms
