@@ -295,3 +295,114 @@ def test_refusals_of_device_tensors():
             call()
     assert A.ivfpq_list_product_ex(x[:0], w, o).shape == (0, 4)
     assert (A.ivfpq_list_product_grad_ex(x[:0], x[:0], o) == 0).all()
+
+
+def three_parts(rng, *shape, kind, terms):
+    """float32 values that one bfloat16 does not hold, and of which about 12 in `terms` are not
+    zero: "wide" ones have 18 bits (three parts), "narrow" ones 1, "two" 9 bits (two
+    parts).  Products of wide and narrow, or two and two, are integers below 2^18, so
+    60 of them add to less than 2^24."""
+    v = {"wide": rng.integers(1 << 16, 1 << 17, shape) * 2 + 1, "narrow": np.ones(shape, int),
+         "two": rng.integers(128, 256, shape) * 2 + 1}[kind]
+    v = v * rng.choice([-1, 1], shape)
+    if kind != "wide":
+        v = v * (rng.random(shape) < min(1.0, 12 / terms))
+    return torch.from_numpy(v.astype(np.float32)).cuda()
+
+
+PAIRS = [("wide", "narrow"), ("narrow", "wide"), ("two", "two")]
+
+
+@pytest.mark.parametrize("rows,nlist,n,d", [s for s in SHAPES if s[0] > 1])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("kinds", PAIRS)
+def test_float32_products_use_all_parts(rows, nlist, n, d, transposed, kinds):
+    rng = np.random.default_rng(rows + n + d)
+    x = three_parts(rng, rows, d, kind=kinds[0], terms=d)
+    w = three_parts(rng, nlist, *((d, n) if transposed else (n, d)), kind=kinds[1], terms=d)
+    offsets = ragged(rng, rows, nlist, rows // 9, rows - rows // 7)
+    y = A.ivfpq_list_product_ex(x, w, torch.from_numpy(offsets).cuda(), transposed=transposed)
+    want, mag = list_product64(np64(x), np64(w), offsets, rows, np.arange(rows), transposed)
+    assert mag.max() < 2 ** 24 and np.array_equal(np64(y), want)
+
+
+GRADIENT_TILES = [(333, 3, 5, 65, 129), (800, 2, 3, 136, 264), (300, 1, 1, 1104, 2000),
+                  (1500, 3, 2, 1056, 1040), (4500, 1, 2, 130, 264), (5000, 1, 3, 65, 33),
+                  (2100, 2, 5, 1032, 2056)]
+
+
+@pytest.mark.parametrize("t,k,nlist,n,d", GRADIENT_TILES)
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("kinds", PAIRS)
+def test_float32_gradients_use_all_parts(t, k, nlist, n, d, gather, kinds):
+    rng = np.random.default_rng(t + n)
+    lists = rng.integers(-1, nlist, (t, k)).astype(np.int32)
+    offsets, order, _ = A.ivfpq_route_sort_ex(torch.from_numpy(lists).cuda(), nlist)
+    terms = max(np.diff(offsets.tolist()))
+    grad = three_parts(rng, t * k, n, kind=kinds[0], terms=terms)
+    x = three_parts(rng, t if gather else t * k, d, kind=kinds[1], terms=terms)
+    got = A.ivfpq_list_product_grad_ex(grad, x, offsets, order=order if gather else None, k=k)
+    source = np.maximum(order.cpu().numpy(), 0) // k if gather else np.arange(t * k)
+    g64, x64, bounds = np64(grad), np64(x), offsets.tolist()
+    for e, (lo, hi) in enumerate(zip(bounds, bounds[1:])):
+        assert (np.abs(g64[lo:hi]).T @ np.abs(x64[source[lo:hi]])).max() < 2 ** 24
+        assert np.array_equal(np64(got[e]), g64[lo:hi].T @ x64[source[lo:hi]])
+
+
+# enough tiles for the larger copies and for the larger tiles through registers
+@pytest.mark.parametrize("rows,nlist,n,d", [(2048, 1, 4200, 72), (3000, 3, 1200, 264),
+                                            (3001, 3, 1201, 39), (700, 2, 520, 264)])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_products_of_reals_in_larger_tiles(rows, nlist, n, d, transposed, dtype):
+    rng = np.random.default_rng(n + d)
+    x = reals(rng, rows, d, dtype=dtype)
+    w = reals(rng, nlist, *((d, n) if transposed else (n, d)), dtype=dtype)
+    offsets = ragged(rng, rows, nlist)
+    y = A.ivfpq_list_product_ex(x, w, torch.from_numpy(offsets).cuda(), transposed=transposed)
+    want, mag = list_product64(np64(x), np64(w), offsets, rows, np.arange(rows), transposed)
+    sums = sum_error(d, dtype) * mag
+    assert (np.abs(np64(y) - want) <= sums + UNIT[dtype] * (np.abs(want) + sums) + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("t,k,nlist,n,d", GRADIENT_TILES)
+@pytest.mark.parametrize("dtype,out", [(t, o) for t in TYPES for o in {t, torch.float32}])
+def test_gradients_of_reals(t, k, nlist, n, d, dtype, out):
+    rng = np.random.default_rng(t + d)
+    lists = rng.integers(-1, nlist, (t, k)).astype(np.int32)
+    offsets, order, _ = A.ivfpq_route_sort_ex(torch.from_numpy(lists).cuda(), nlist)
+    grad, x = reals(rng, t * k, n, dtype=dtype), reals(rng, t, d, dtype=dtype)
+    got = A.ivfpq_list_product_grad_ex(grad, x, offsets, order=order, k=k, dtype=out)
+    g64, x64, bounds = np64(grad), np64(x)[np.maximum(order.cpu().numpy(), 0) // k], offsets.tolist()
+    for e, (lo, hi) in enumerate(zip(bounds, bounds[1:])):
+        want = g64[lo:hi].T @ x64[lo:hi]
+        # joining the parts of a list adds at most 64 sums
+        sums = sum_error(hi - lo + 64, dtype) * (np.abs(g64[lo:hi]).T @ np.abs(x64[lo:hi]))
+        assert (np.abs(np64(got[e]) - want) <=
+                sums + UNIT[out] * (np.abs(want) + sums) + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("rows,n,d", [(40, 33, 64), (200, 1030, 64), (2048, 2200, 72)])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_small_float32_factors(rows, n, d, transposed):
+    """Factors from 2^-110 on keep their 24 bits, smaller ones are rounded to multiples of
+    2^-133: one factor of a result is such a number, the other 2^100 or 0."""
+    rng = np.random.default_rng(d)
+    for e in (-133, -140, -149):
+        whole = rng.integers(1 << 23, 1 << 24, (rows, d)).astype(np.float64)
+        if e < -133:
+            whole = np.round(whole / 2 ** 8)      # the least have less than 24 bits
+        x = torch.from_numpy(np.ldexp(whole, e)).float().cuda()
+        assert np.array_equal(np64(x), np.ldexp(whole, e)) or e == -149
+        w = torch.zeros((1, n, d), device="cuda")
+        w[0, torch.arange(n), torch.from_numpy(rng.integers(0, d, n))] = 2.0 ** 100
+        o = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+        want = np64(x) @ np64(w[0]).T
+        m = w.transpose(1, 2).contiguous() if transposed else w
+        y = A.ivfpq_list_product_ex(x, m, o, transposed=transposed)
+        error = 0.0 if e == -133 else 2.0 ** (100 - 134)
+        assert (np.abs(np64(y) - want) <= error).all()
+        g = torch.zeros((rows, 5), device="cuda")
+        g[rows // 2] = 2.0 ** 100
+        got = A.ivfpq_list_product_grad_ex(g, x, o)
+        assert (np.abs(np64(got[0]) - 2.0 ** 100 * np64(x)[rows // 2]) <= error).all()
