@@ -2,21 +2,27 @@
 //
 // y[t] = W x[t] + s[a] U[a] (D[a] x[t]), a the list (adapter) of row t, in two
 // launches: the hidden rows h[t] = s[a] D[a] x[t], a product per list of the sorted
-// rows, then the shared product with the contraction continued over the hidden rows:
-// after the chunks of x and W come, for each list among a tile's rows, chunks of
-// that list's hidden rows (the other rows zero) and its up matrix.  So the adapters
-// add to sums that are still in registers.
+// rows, then the shared product, whose tiles begin (those of few rows end) with the
+// adapters' products, so that both add to sums in registers.
 //
-// Hidden rows of 16-bit types are kept as two parts, h = high + low, side by side,
-// and multiplied with the same up matrix twice: rounded once more to 16 bits they
-// would add an error as large as the result's own rounding.  float32 hidden
-// rows are float32.
+// Hidden rows are float32: those of 16-bit types in three bfloat16 parts, which hold all 24
+// bits of a float32 value of 2^-110 or more, each multiplied with the same up matrix.  Two
+// parts lose 8 bits, which show where W x and the adapter cancel; binary16 parts lose
+// what leaves binary16's range, below 2^-14 bit by bit and above 65504 all.  Binary16 up
+// matrices are split in two bfloat16 parts on their way into the matrix instructions.
+// 8192 rows through 4096 x 4096, rank 64: 275 us in bfloat16, 294 in binary16 (with two
+// parts of the rows' type 273 and 284).
 #include "list_direct.hpp"
 #include "list_tiles.hpp"
 
 namespace ivfpq {
 
-static int hidden_part(int r) { return (r + 7) / 8 * 8; }
+// Values of a hidden row, and of all hidden rows: whole steps and blocks (HiddenPlace).
+static int hidden_width(int r) { return (r + 15) / 16 * 16; }
+static size_t hidden_values(int64_t t, int r)
+{
+    return (size_t)((t + 31) / 32 * 32) * (size_t)hidden_width(r);
+}
 
 // Hidden rows are short and their contraction long, so they take the kernel of few rows: in
 // 16 x 16 blocks, whose eight waves share the contraction, up to a workgroup a CU; from
@@ -53,10 +59,11 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
     p.scales = q.scales;
     p.up = q.up;
     p.r = q.r;
-    p.rp = hidden_part(q.r);
-    p.width = sizeof(T) == 4 ? p.rp : 2 * p.rp;
+    p.rp = hidden_width(q.r);
     p.hidden = q.ws;
-    p.row_list = reinterpret_cast<int32_t *>(static_cast<T *>(q.ws) + q.t * p.width);
+    p.row_list = reinterpret_cast<int32_t *>(
+        static_cast<typename HiddenPlace<T>::E *>(q.ws) +
+        hidden_values(q.t, q.r) * HiddenPlace<T>::PARTS);
     p.b = q.down;
     p.n = q.r;
     if (hipError_t e = hidden_as<T>(p, stream))
@@ -67,10 +74,10 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
     const bool copies = sizeof(T) == 2 && copies_fit<kAdapter>(p);
     const int64_t middle = count_tiles<kAdapter>(p, 128, 128);
     // Few rows: blocks whose waves share the contraction, the largest that still make a
-    // workgroup a CU.  16 rows of 4096 x 4096: 26 us in 16 x 16 blocks, 29 in 32 x 32, 44 in
-    // copied 32 x 128 tiles; 64 rows: 53, 33 and 44; 128: 90, 53 and 43; 32 rows of 11,008 x
-    // 4096: 73, 57 and 86.  Where the copies do not fit, up to two workgroups a CU: 256
-    // rows of 2048 x 2048 in float32 58 us, in 64 x 64 tiles 71; 512 rows: 99 and 74.
+    // workgroup a CU.  16 rows of 4096 x 4096: 24 us in 16 x 16 blocks, 29 in 32 x 32, 35 in
+    // copied 32 x 128 tiles; 64 rows: 53, 34 and 37; 128: 87, 51 and 35; 32 rows of 11,008 x
+    // 4096: 72, 56 and 69.  Where the copies do not fit, up to two workgroups a CU: 128
+    // rows of 2048 x 2048 in float32 38 us, in 64 x 64 tiles 52; 256 rows: 56 and 52.
     const int64_t blocks = count_tiles<kAdapter>(p, 32, 32);
     if (!any_tiny<kAdapter>(p) && (p.rows <= 32 || blocks <= (copies ? 256 : 512))) {
         if (p.rows <= 16 || count_tiles<kAdapter>(p, 16, 16) <= 256)
@@ -92,9 +99,9 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
         }
     }
     // In float32 tiles of 64 x 64 or 128 x 128: 2048 x 2048, 1024 rows (128 of the larger)
-    // 92 us and 131, 2048 rows (256) 152 and 139.  In 16 bits of 64 x 64, or of 64 x 128 by
-    // eight waves where those would take more than a turn of two a CU: 2001 x 2001, 2048 rows
-    // 93 us and 82, 4096 167 and 146 (128 x 128 tiles: 190).
+    // 79 us and 102, 2048 rows (256) 136 and 122.  In 16 bits of 64 x 64, or of 64 x 128 by
+    // eight waves where those would take more than a turn of two a CU: 2001 x 2001, 512 rows
+    // (256 of the smaller) 36 us and 39, 2048 rows 75 and 60, 4096 137 and 109.
     if constexpr (sizeof(T) == 4) {
         if (middle > 192)
             return launch_tiles<T, T, kAdapter, KS, 2, 2, 2, 2>(p, stream);
@@ -107,8 +114,8 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
 
 size_t adapter_bytes(int64_t t, int r)
 {
-    // hidden rows, 32 bits a value in either form, and the rows' lists
-    return (size_t)t * ((size_t)hidden_part(r) * 4 + 4);
+    // hidden rows, 32 bits a value or three times 16, and the rows' lists
+    return hidden_values(t, r) * 6 + (size_t)t * 4;
 }
 
 hipError_t launch_adapter(const AdapterProduct &p, int type, hipStream_t stream)

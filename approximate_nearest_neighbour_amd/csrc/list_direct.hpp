@@ -33,6 +33,51 @@ __device__ __forceinline__ f32x4 mfma16_small(s16x8 a, s16x8 b, f32x4 c)
                                                       __builtin_bit_cast(V, b), c, 0, 0, 0);
 }
 
+// The list of each row of a tile (-1: none), and these lists each once, ascending:
+// segs[0 .. segs[TM]).
+template <int TM, int THREADS>
+__device__ __forceinline__ void find_lists(const ListJob &p, const PartTile &tile, int *tile_list,
+                                           int *segs)
+{
+    const int tid = (int)threadIdx.x, lane = lane_id();
+    for (int i = tid; i < TM; i += THREADS) {
+        const int64_t row = tile.p0 + i;
+        int e = -1;
+        if (row < tile.p1 && (uint32_t)p.pos[row] < (uint64_t)p.rows) {
+            e = p.row_list[row];
+            e = (uint32_t)e < (uint32_t)p.nlist ? e : -1;
+        }
+        tile_list[i] = e;
+    }
+    lds_barrier();
+    if (tid < 64) {
+        int last = -1, found = 0;
+        for (;;) { // at most TM times
+            uint32_t next = 0xFFFFFFFFu;
+#pragma unroll
+            for (int i = 0; i < (TM + 63) / 64; ++i) {
+                const int e = i * 64 + lane < TM ? tile_list[i * 64 + lane] : -1;
+                next = e > last ? min(next, (uint32_t)e) : next;
+            }
+            next = min(next, xor_lane<1>(next));
+            next = min(next, xor_lane<2>(next));
+            next = min(next, xor_lane<4>(next));
+            next = min(next, xor_lane<8>(next));
+            next = min(next, xor_lane<16>(next));
+            next = min(next, xor_lane<32>(next));
+            if (next == 0xFFFFFFFFu)
+                break;
+            last = (int)next;
+            if (lane == 0)
+                segs[found] = last;
+            ++found;
+        }
+        if (lane == 0)
+            segs[TM] = found;
+    }
+    lds_barrier();
+}
+
 template <typename T, bool ODD, int FORM, int RT, int CT, int KW, int TURN>
 __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
 {
@@ -184,16 +229,25 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
             }
         }
         if constexpr (FORM == kAdapter) {
-            const T *hidden = static_cast<const T *>(p.hidden), *up = static_cast<const T *>(p.up);
+            using Place = HiddenPlace<T>;
+            const typename Place::E *hidden = static_cast<const typename Place::E *>(p.hidden);
+            const T *up = static_cast<const T *>(p.up);
             const int64_t all_up = (int64_t)p.nlist * p.n * p.r;
             const int count = segs[TM];
             constexpr int AHEAD = RT + CT <= 3 ? 4 : 2; // lists under way
-            for (int at0 = 0; at0 < p.width; at0 += 32) { // 32 values a matrix instruction
-                const int at = at0 + g * 8, col = at < p.rp ? at : at - p.rp;
+            for (int at0 = 0; at0 < p.rp; at0 += 32) {  // 32 values a matrix instruction
+                const int at = at0 + g * 8;
+                Eight<typename Place::E> h[RT][Place::PARTS];
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int q = 0; q < Place::PARTS; ++q)
+                        h[i][q].read(hidden + q * 512 +
+                                     Place::piece(tile.p0 + i * 16 + r, min(at, p.rp - 8), p.rp));
                 for (int s0 = first; s0 < count; s0 += AHEAD * KW) {
-                    Values xb[AHEAD][CT], xa[AHEAD][RT];
+                    Values xb[AHEAD][CT];
                     auto up_at = [&](int seg, int j) {
-                        return ((int64_t)seg * p.n + min(n0 + j * 16 + r, p.n - 1)) * p.r + col;
+                        return ((int64_t)seg * p.n + min(n0 + j * 16 + r, p.n - 1)) * p.r + at;
                     };
 #pragma unroll
                     for (int s = 0; s < AHEAD; ++s) {
@@ -201,40 +255,47 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
 #pragma unroll
                         for (int j = 0; j < CT; ++j)
                             xb[s][j].template read_near<false>(up, up_at(seg, j), all_up);
+                    }
+                    s16x8 oh[RT][kHiddenParts];
 #pragma unroll
-                        for (int i = 0; i < RT; ++i) {
-                            const int64_t row = min(tile.p0 + i * 16 + r, tile.p1 - 1);
-                            xa[s][i].read(hidden + row * p.width + min(at, p.width - 8));
-                        }
+                    for (int i = 0; i < RT; ++i) {
+#pragma unroll
+                        for (int q = 0; q < Place::PARTS; ++q)
+                            h[i][q].keep(at < p.rp);
+                        if constexpr (Place::PARTS == 1)
+                            operands_of(h[i][0], oh[i]);
+                        else
+#pragma unroll
+                            for (int q = 0; q < kHiddenParts; ++q)
+                                oh[i][q] = __builtin_bit_cast(s16x8, h[i][q].v);
                     }
 #pragma unroll
                     for (int s = 0; s < AHEAD; ++s) {
                         if (s0 + s * KW >= count)
                             break;
                         const int seg = segs[s0 + s * KW];
-                        all_ready(xa[s]);
                         all_ready(xb[s]);
 #pragma unroll
-                        for (int j = 0; j < CT; ++j)
+                        for (int j = 0; j < CT; ++j) {
                             xb[s][j].template settle<false>(up_at(seg, j), all_up,
-                                                            at < p.width ? p.r - col : 0);
-                        f32x4 before[RT][CT];
+                                                            at < p.rp ? p.r - at : 0);
+                            s16x8 ou[UpParts<T>::N];
+                            UpParts<T>::of(xb[s][j], ou);
 #pragma unroll
-                        for (int i = 0; i < RT; ++i) {
-                            xa[s][i].keep(at < p.width);
+                            for (int i = 0; i < RT; ++i) {
+                                f32x4 d = acc[i][j];
+                                // parts whose numbers add to 2, then 1, then 0
 #pragma unroll
-                            for (int j = 0; j < CT; ++j)
-                                before[i][j] = acc[i][j];
-                        }
-                        products(xa[s], xb[s]);
+                                for (int sum = kHiddenParts - 1; sum >= 0; --sum)
 #pragma unroll
-                        for (int i = 0; i < RT; ++i) {
-                            const bool mine = tile_list[i * 16 + r] == seg;
-#pragma unroll
-                            for (int j = 0; j < CT; ++j)
+                                    for (int q = 0; q <= sum; ++q)
+                                        if (sum - q < UpParts<T>::N)
+                                            d = mfma16_small<__bf16>(ou[sum - q], oh[i][q], d);
+                                const bool mine = tile_list[i * 16 + r] == seg;
 #pragma unroll
                                 for (int q = 0; q < 4; ++q)
-                                    acc[i][j][q] = mine ? acc[i][j][q] : before[i][j][q];
+                                    acc[i][j][q] = mine ? d[q] : acc[i][j][q];
+                            }
                         }
                     }
                 }
@@ -281,16 +342,11 @@ __global__ __launch_bounds__(512) void list_direct_kernel(ListJob p)
             if (listed && !there[i])
                 v = f32x4{0.f, 0.f, 0.f, 0.f};
             if constexpr (FORM == kHidden) {
-                T *to = static_cast<T *>(p.hidden) + t * p.width + n;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (n + q >= p.rp)
-                        continue;
-                    const float h = n + q < p.r ? v[q] * scale : 0.f;
-                    to[q] = (T)h;
-                    if constexpr (NP == 1)
-                        to[p.rp + q] = (T)(h - (float)to[q]);
-                }
+                for (int q = 0; q < 4; ++q)
+                    if (n + q < p.rp)
+                        HiddenPlace<T>::put(p.hidden, t, n + q, p.rp,
+                                            n + q < p.r ? v[q] * scale : 0.f);
             } else {
                 typedef T V __attribute__((ext_vector_type(4), aligned(sizeof(T))));
                 T *out = static_cast<T *>(p.out) + row * p.n + n;

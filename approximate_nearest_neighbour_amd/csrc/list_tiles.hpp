@@ -335,14 +335,14 @@ struct ListJob {
     const int32_t *by_size = nullptr; // kGradient: the lists, the longest first (nullptr: as they are)
     int splits = 1; // kGradient: workgroups that share a list's rows, a result each
     int64_t block0 = 0; // the launch's first workgroup
-    // adapters: hidden rows [t][width] (16-bit: high parts, then low parts, rp each),
-    // the list of each row, up matrices [nlist][n][r], scales [nlist] or nullptr
+    // adapters: hidden rows (HiddenPlace; rp values each, r and zeros), the list of each row,
+    // up matrices [nlist][n][r], scales [nlist] or nullptr
     void *hidden = nullptr;
     int32_t *row_list = nullptr;
     const int32_t *pos = nullptr;
     const void *up = nullptr;
     const float *scales = nullptr;
-    int r = 0, rp = 0, width = 0;
+    int r = 0, rp = 0;
 };
 
 // Row of the gathered operand that sorted row p takes; -1 where there is none.
@@ -355,6 +355,32 @@ __device__ __forceinline__ int64_t source_row(const ListJob &p, int64_t row)
     return q < p.arows ? q : -1;
 }
 
+// Hidden rows in the workspace, as the matrix instructions' operands: blocks of 32 rows, in a
+// block steps of 16 values, in a step two times 32 pieces of eight values, the rows' first
+// and then their second ones.  16-bit types have three bfloat16 parts of each value, which
+// hold float32's 24 bits (see above), a step's parts one after the other.
+template <typename T>
+struct HiddenPlace {
+    using E = typename std::conditional<sizeof(T) == 4, float, __bf16>::type;
+    static constexpr int PARTS = sizeof(T) == 4 ? 1 : 3;
+    // values before row t's piece of eight from value `at` on (first part; 512 values a part)
+    __device__ __forceinline__ static int64_t piece(int64_t t, int at, int rp)
+    {
+        return (t >> 5) * (rp * 32 * PARTS) + (at >> 4) * (512 * PARTS) + (at & 8) * 32 +
+               (t & 31) * 8;
+    }
+    __device__ __forceinline__ static void put(void *hidden, int64_t t, int at, int rp, float h)
+    {
+        E *to = static_cast<E *>(hidden) + piece(t, at, rp) + (at & 7);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+            to[q * 512] = (E)h;
+            h -= (float)to[q * 512];
+        }
+    }
+};
+constexpr int kHiddenParts = 3; // as operands
+
 // kHidden: the rows of a tile of no list have none.
 __device__ __forceinline__ void no_list_rows(const ListJob &p, const PartTile &tile, bool first,
                                              int tid, int threads)
@@ -364,51 +390,6 @@ __device__ __forceinline__ void no_list_rows(const ListJob &p, const PartTile &t
         if (t >= 0)
             p.row_list[t] = -1;
     }
-}
-
-// The list of each row of a tile (-1: none), and these lists each once, ascending:
-// segs[0 .. segs[TM]).
-template <int TM, int THREADS>
-__device__ __forceinline__ void find_lists(const ListJob &p, const PartTile &tile, int *tile_list,
-                                           int *segs)
-{
-    const int tid = (int)threadIdx.x, lane = lane_id();
-    for (int i = tid; i < TM; i += THREADS) {
-        const int64_t row = tile.p0 + i;
-        int e = -1;
-        if (row < tile.p1 && (uint32_t)p.pos[row] < (uint64_t)p.rows) {
-            e = p.row_list[row];
-            e = (uint32_t)e < (uint32_t)p.nlist ? e : -1;
-        }
-        tile_list[i] = e;
-    }
-    lds_barrier();
-    if (tid < 64) {
-        int last = -1, found = 0;
-        for (;;) { // at most TM times
-            uint32_t next = 0xFFFFFFFFu;
-#pragma unroll
-            for (int i = 0; i < (TM + 63) / 64; ++i) {
-                const int e = i * 64 + lane < TM ? tile_list[i * 64 + lane] : -1;
-                next = e > last ? min(next, (uint32_t)e) : next;
-            }
-            next = min(next, xor_lane<1>(next));
-            next = min(next, xor_lane<2>(next));
-            next = min(next, xor_lane<4>(next));
-            next = min(next, xor_lane<8>(next));
-            next = min(next, xor_lane<16>(next));
-            next = min(next, xor_lane<32>(next));
-            if (next == 0xFFFFFFFFu)
-                break;
-            last = (int)next;
-            if (lane == 0)
-                segs[found] = last;
-            ++found;
-        }
-        if (lane == 0)
-            segs[TM] = found;
-    }
-    lds_barrier();
 }
 
 // Operands of the matrix instructions from eight values: the values, or their parts.
@@ -425,6 +406,30 @@ __device__ __forceinline__ void operands_of(const Eight<T, ODD> &x, s16x8 (&out)
             out[p] = __builtin_bit_cast(s16x8, parts[p]);
     }
 }
+
+// What an up matrix's values become where they meet hidden rows, whose parts are bfloat16:
+// bfloat16 ones stay, the 11 bits of binary16 ones are two bfloat16 parts, whose range
+// holds theirs, float32 ones are three.
+template <typename T>
+struct UpParts {
+    static constexpr int N = sizeof(T) == 4 ? 3 : std::is_same<T, _Float16>::value ? 2 : 1;
+    template <bool ODD>
+    __device__ __forceinline__ static void of(const Eight<T, ODD> &x, s16x8 (&out)[N])
+    {
+        if constexpr (N == 2) {
+            typedef _Float16 H8 __attribute__((ext_vector_type(8)));
+            typedef float F8 __attribute__((ext_vector_type(8)));
+            typedef __bf16 B8 __attribute__((ext_vector_type(8)));
+            const F8 v = __builtin_convertvector(__builtin_bit_cast(H8, x.v), F8);
+            const B8 high = __builtin_convertvector(v, B8);
+            out[0] = __builtin_bit_cast(s16x8, high);
+            out[1] = __builtin_bit_cast(
+                s16x8, __builtin_convertvector(v - __builtin_convertvector(high, F8), B8));
+        } else {
+            operands_of(x, out);
+        }
+    }
+};
 
 // A wave's hidden rows (not dealt: a lane has one column of sixteen rows), and the rows'
 // lists.  `p0`, `n0`: the wave's first row and column.
@@ -453,128 +458,234 @@ __device__ __forceinline__ void store_hidden(const ListJob &p, const PartTile &t
                 const int64_t t = row < tile.p1 ? source_row(p, row) : -1;
                 if (t < 0)
                     continue;
-                const float h = col < p.r ? acc[i][j][q] * scale : 0.f;
-                T *to = static_cast<T *>(p.hidden) + t * p.width + col;
-                to[0] = (T)h;
-                if constexpr (Parts<T>::N == 1)
-                    to[p.rp] = (T)(h - (float)to[0]);
+                HiddenPlace<T>::put(p.hidden, t, col, p.rp,
+                                    col < p.r ? acc[i][j][q] * scale : 0.f);
             }
     }
 }
 
-// The adapter kernels multiply a tile's rows with the up matrices of all its lists, with
-// zeros for the hidden rows of the other lists; an up matrix that holds an infinity or
-// NaN would so reach rows of other lists.  So a wave with a sum that is not finite, in
-// a tile of several lists, looks for such a value in the up matrices' rows of its
-// columns, and if there is one forms its sums again, each row's with the row's list
-// alone: in the same steps, so that rows without such a value keep their sums to the
-// last bit.  What is not finite in a row of x, or in its hidden row, stays in that row
-// anyway.  8192 rows of 16 lists, 4096 x 4096, rank 64, bfloat16: 264 us, with a NaN in
-// every row of x 258 (6.0 ms if those waves formed their sums again), with one in an up
-// matrix 730.
-// `p0`, `n0`: the wave's first row and column; `lists`: its rows' lists.
-template <typename T, bool PAIR, bool TINY, int WM, int WN>
-__device__ __forceinline__ void keep_lists_apart(const ListJob &p, const PartTile &tile, int64_t p0,
-                                                 int n0, const int *lists, const int *segs,
-                                                 int count, f32x16 (&acc)[WM][WN])
+// The list of an adapter's row, as two loads that may be under way for long.
+struct RowList {
+    int32_t pos, e;
+    __device__ __forceinline__ void load(const ListJob &p, int64_t row, int64_t end)
+    {
+        pos = row < end ? p.pos[row] : -1;
+        e = row < end ? p.row_list[row] : -1;
+    }
+    // -1: none (a masked row's entry is whatever the workspace held)
+    __device__ __forceinline__ int list(const ListJob &p) const
+    {
+        return (uint32_t)pos < (uint64_t)p.rows && (uint32_t)e < (uint32_t)p.nlist ? e : -1;
+    }
+};
+
+// Offset of a load that reads nothing: past any range (ranges are below 2^31 bytes).
+constexpr uint32_t kNowhere = 0x80000000u;
+
+// A memory range of less than 2^31 bytes from byte `from` on.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t range_of(const void *base, int64_t from,
+                                                           int64_t bytes)
 {
-    constexpr int NP = Parts<T>::N;
-    using E = typename Parts<T>::E;
-    using Values = Eight<T, sizeof(T) == 2>;
+    from = uniform(from);
+    const int64_t left = min(max(bytes - from, (int64_t)0), (int64_t)0x7FFFFFFF);
+    const uint8_t *p = static_cast<const uint8_t *>(base) + from;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)uniform(left),
+                                             0x00027000);
+}
+
+// A wave's first sums: each row's hidden row times the up matrix of the row's own list, while
+// the first chunks of x and W are under way.  A block of 32 rows takes its lists one after
+// the other, all its hidden rows times that list's up matrix, of which the list's
+// rows keep the sums.  So nothing of one row, or of one list's matrices, reaches a row of
+// another list, neither an infinity or NaN nor a rounding.  Blocks that have the same list
+// alone share the up matrix's operands.  Hidden rows go from memory to registers, as
+// their place is the operands'; rows of an up matrix would take 64 short pieces a load
+// that way, and go through a part of LDS of the wave's own where the copies can read them.
+// bfloat16, 8192 rows of 16 requests, 4096 x 4096, rank 64: 256 us, without any list 247
+// (binary16, whose up matrices take two parts: 270 for one list of all rows, bfloat16 253).
+// Every list among 32 rows costs its products anew: 4096 rows dealt one by one to 8 lists of
+// rank 16 146 us, to 64 lists of rank 64 397, about 120 where a list's rows are together.
+// `p0`, `n0`: the wave's first row and column; `rows`: of row i 32 + (lane & 31); `slab`:
+// SLAB bytes of LDS (0: none).
+template <typename T, int SLAB, bool PAIR, bool TINY, int WM, int WN>
+__device__ __forceinline__ void adapter_sums(const ListJob &p, int64_t p0, int n0,
+                                             const RowList (&rows)[WM], uint8_t *slab,
+                                             f32x16 (&acc)[WM][WN])
+{
+    constexpr bool COPY = SLAB > 0;
+    static_assert(!COPY || (sizeof(T) == 2 && SLAB >= WN * 32 * 64), "16-bit rows, 32 values");
+    // values of an up matrix's rows brought together, hidden values loaded together
+    constexpr int UPS = !COPY ? 16 : SLAB >= WN * 32 * 128 ? 64 : 32, STEPS = COPY ? 2 : 1;
+    constexpr int GROUPS = UPS / 16 / STEPS, AHEAD = WM * WN < 8 ? GROUPS : 1; // registers
+    using Up = Eight<T, !COPY && sizeof(T) == 2>;
+    using Place = HiddenPlace<T>;
     const int lane = lane_id(), r = lane & 31, half = lane >> 5;
-    bool mixed = count > 1;
-#pragma unroll
-    for (int i = 0; i < WM; ++i)
-        mixed = mixed || lists[i * 32 + r] != segs[0];
-    float zero = 0.f;
-#pragma unroll
-    for (int i = 0; i < WM; ++i)
-#pragma unroll
-        for (int j = 0; j < WN; ++j)
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-                zero = __builtin_fmaf(acc[i][j][q], 0.f, zero);
-    if (count == 0 || !__any(mixed) || !__any(zero != 0.f))
-        return;
-    int64_t rows[WM], cols[WN];
-#pragma unroll
-    for (int i = 0; i < WM; ++i)
-        rows[i] = min(p0 + i * 32 + r, tile.p1 - 1);
-#pragma unroll
-    for (int j = 0; j < WN; ++j)
-        cols[j] = min(n0 + j * 32 + deal_row<PAIR>(r), p.n - 1);
-    const int64_t all_a = p.rows * p.kdim, all_b = (int64_t)p.n * p.kdim;
-    const int64_t all_hidden = p.rows * p.width, all_up = (int64_t)p.nlist * p.n * p.r;
-    auto operand = [&](const void *array, int64_t at, int64_t all, int left, s16x8 (&to)[NP]) {
-        Values x;
-        x.template read_near<TINY>(static_cast<const T *>(array), at, all);
-        x.ready();
-        x.template settle<TINY>(at, all, left);
-        operands_of(x, to);
+    const int64_t all_up = (int64_t)p.nlist * p.n * p.r;
+    using Lines = ivfpq::Place<true, WN * 32, COPY ? UPS : 64>;
+    Reader<true, WN * 32, COPY ? UPS : 64, WN, PAIR> reader;
+    if constexpr (COPY)
+        reader.init(0);
+    Up u[WN]; // not COPY
+    auto up_at = [&](int seg, int j, int at) { // columns past the last repeat it; not stored
+        return ((int64_t)seg * p.n + min(n0 + j * 32 + deal_row<PAIR>(r), p.n - 1)) * p.r + at;
     };
-    bool bad = false; // a part that is not finite: its exponent's bits are all ones
-    for (int s = 0; s < count; ++s)
-        for (int k0 = half * 8; k0 < p.r; k0 += 16)
+    // values u0 on of list seg's matrix
+    auto load_up = [&](int seg, int u0) {
+        if constexpr (COPY) {
+            const __amdgpu_buffer_rsrc_t range =
+                range_of(p.up, ((int64_t)seg * p.n + n0) * p.r * 2, all_up * 2);
+            wait_lds(); // the slab is read
+#pragma unroll
+            for (int c = 0; c < Lines::PLANE / 1024; ++c) {
+                const int line = (c * 64 + lane) / Lines::BLOCKS;
+                const int at = u0 + ((lane % Lines::BLOCKS) ^ Lines::swizzle(line)) * 8;
+                copy16_to_lds(range, at < p.r ? (uint32_t)(line * p.r + at) * 2 : kNowhere, 0,
+                              slab + c * 1024);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < WN; ++j)
+                u[j].template read_near<TINY>(static_cast<const T *>(p.up),
+                                              up_at(seg, j, u0 + half * 8), all_up);
+        }
+    };
+    auto settle_up = [&](int seg, int u0) { // once after load_up
+        if constexpr (COPY) {
+            wait_vm<0>();
+        } else {
 #pragma unroll
             for (int j = 0; j < WN; ++j) {
-                s16x8 o[NP];
-                operand(p.up, ((int64_t)segs[s] * p.n + cols[j]) * p.r + k0, all_up, p.r - k0, o);
-                constexpr int ONES = std::is_same<E, __bf16>::value ? 0x7F80 : 0x7C00;
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    bad = bad || (o[0][q] & ONES) == ONES;
+                u[j].ready();
+                u[j].template settle<TINY>(up_at(seg, j, u0 + half * 8), all_up,
+                                           p.r - u0 - half * 8);
             }
-    if (!__any(bad))
-        return;
+        }
+    };
+    // block i's hidden rows; past the last block, whose results are dropped, that one's
+    struct Hiddens {
+        Eight<typename Place::E> h[STEPS][Place::PARTS];
+    };
+    auto load_hidden = [&](Hiddens &to, int i, int k0) {
+        const typename Place::E *from = static_cast<const typename Place::E *>(p.hidden) +
+                                        Place::piece(min(p0 + i * 32, (p.rows - 1) & ~(int64_t)31),
+                                                     0, p.rp) + lane * 8;
 #pragma unroll
-    for (int i = 0; i < WM; ++i)
+        for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+            for (int q = 0; q < Place::PARTS; ++q)
+                to.h[k][q].read(from +
+                                (min(k0 + k * 16, p.rp - 16) / 16 * Place::PARTS + q) * 512);
+    };
+    // group g of the values from u0 on
+    auto products = [&](const Hiddens &h, int u0, int g, f32x16 (&d)[WN]) {
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+            const int step = g * STEPS + k;
+            if (u0 + step * 16 >= p.rp)
+                break;
+            s16x8 oh[kHiddenParts];
+            if constexpr (Place::PARTS == 1)
+                operands_of(h.h[k][0], oh);
+            else
+#pragma unroll
+                for (int q = 0; q < kHiddenParts; ++q)
+                    oh[q] = __builtin_bit_cast(s16x8, h.h[k][q].v);
+#pragma unroll
+            for (int j = 0; j < WN; ++j) {
+                s16x8 ou[UpParts<T>::N];
+                if constexpr (COPY) {
+                    Up x;
+                    x.v = __builtin_bit_cast(u32x4, reader.read(slab, j, step));
+                    UpParts<T>::of(x, ou);
+                } else {
+                    UpParts<T>::of(u[j], ou);
+                }
+                // parts whose numbers add to 2, then 1, then 0
+#pragma unroll
+                for (int sum = kHiddenParts - 1; sum >= 0; --sum)
+#pragma unroll
+                    for (int q = 0; q <= sum; ++q)
+                        if (sum - q < UpParts<T>::N)
+                            d[j] = PAIR ? mfma16<__bf16>(ou[sum - q], oh[q], d[j])
+                                        : mfma16<__bf16>(oh[q], ou[sum - q], d[j]);
+            }
+        }
+    };
+    // the sums' row of result q
+    auto row_of = [&](int q) { return PAIR ? r : (q >> 2) * 8 + half * 4 + (q & 3); };
+
+    int list[WM];
+    uint32_t left[WM]; // a block's rows whose list is to come
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+        list[i] = rows[i].list(p);
+        left[i] = (uint32_t)__ballot(list[i] >= 0);
 #pragma unroll
         for (int j = 0; j < WN; ++j)
 #pragma unroll
             for (int q = 0; q < 16; ++q)
                 acc[i][j][q] = 0.f;
-    // seg: the list whose rows take the products (-1: all rows do)
-    auto products = [&](const s16x8 (&oa)[NP], const s16x8 (&ob)[NP], int i, f32x16 &c, int seg) {
-        f32x16 d = c;
-#pragma unroll
-        for (int sum = NP - 1; sum >= 0; --sum)
-#pragma unroll
-            for (int q = 0; q <= sum; ++q)
-                d = PAIR ? mfma16<E>(ob[sum - q], oa[q], d) : mfma16<E>(oa[q], ob[sum - q], d);
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-            const int row = i * 32 + (PAIR ? r : (q >> 2) * 8 + half * 4 + (q & 3));
-            c[q] = seg < 0 || lists[row] == seg ? d[q] : c[q];
-        }
-    };
-    for (int k0 = 0; k0 < p.kdim; k0 += 16) {
-        const int at = k0 + half * 8;
-#pragma unroll
-        for (int i = 0; i < WM; ++i) {
-            s16x8 oa[NP], ob[NP];
-            operand(p.a, rows[i] * p.kdim + at, all_a, p.kdim - at, oa);
-#pragma unroll
-            for (int j = 0; j < WN; ++j) {
-                operand(p.b, cols[j] * p.kdim + at, all_b, p.kdim - at, ob);
-                products(oa, ob, i, acc[i][j], -1);
-            }
-        }
     }
-    for (int s = 0; s < count; ++s) {
-        const int seg = segs[s];
-        for (int k0 = 0; k0 < p.width; k0 += 16) {
-            const int at = k0 + half * 8, col = at < p.rp ? at : at - p.rp;
+    if constexpr (WM > 1) {
+        const int seg = left[0] ? __builtin_amdgcn_readlane(list[0], __builtin_ctz(left[0])) : -1;
+        bool same = seg >= 0;
 #pragma unroll
-            for (int i = 0; i < WM; ++i) {
-                s16x8 oa[NP], ob[NP];
-                operand(p.hidden, rows[i] * p.width + at, all_hidden, p.width - at, oa);
+        for (int i = 0; i < WM; ++i)
+            same = same && left[i] == (uint32_t)__ballot(list[i] == seg);
+        if (same) {
+            for (int u0 = 0; u0 < p.rp; u0 += UPS) {
+                Hiddens h[2];
+                load_up(seg, u0);
+                load_hidden(h[0], 0, u0);
+                settle_up(seg, u0);
 #pragma unroll
-                for (int j = 0; j < WN; ++j) {
-                    operand(p.up, ((int64_t)seg * p.n + cols[j]) * p.r + col, all_up,
-                            at < p.width ? p.r - col : 0, ob);
-                    products(oa, ob, i, acc[i][j], seg);
+                for (int c = 0; c < GROUPS * WM; ++c) {
+                    if (c + 1 < GROUPS * WM)
+                        load_hidden(h[(c + 1) & 1], (c + 1) % WM, u0 + (c + 1) / WM * STEPS * 16);
+                    products(h[c & 1], u0, c / WM, acc[c % WM]);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < WM; ++i)
+#pragma unroll
+                for (int j = 0; j < WN; ++j)
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        acc[i][j][q] = left[i] >> row_of(q) & 1 ? acc[i][j][q] : 0.f;
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+        while (left[i]) {
+            const int seg = __builtin_amdgcn_readlane(list[i], __builtin_ctz(left[i]));
+            const uint32_t mine = (uint32_t)__ballot(list[i] == seg);
+            left[i] &= ~mine;
+            f32x16 d[WN];
+#pragma unroll
+            for (int j = 0; j < WN; ++j)
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    d[j][q] = 0.f;
+            for (int u0 = 0; u0 < p.rp; u0 += UPS) {
+                Hiddens h[AHEAD];
+                load_up(seg, u0);
+#pragma unroll
+                for (int g = 0; g < AHEAD; ++g)
+                    load_hidden(h[g], i, u0 + g * STEPS * 16);
+                settle_up(seg, u0);
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) {
+                    if (g >= AHEAD)
+                        load_hidden(h[g % AHEAD], i, u0 + g * STEPS * 16);
+                    products(h[g % AHEAD], u0, g, d);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < WN; ++j)
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    acc[i][j][q] = mine >> row_of(q) & 1 ? d[j][q] : acc[i][j][q];
         }
     }
 }
@@ -596,8 +707,6 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
     using PB = Place<F::B_ALONG, TN, KS>;
     constexpr int STAGE = NP * (PA::PLANE + PB::PLANE);
     __shared__ __align__(16) uint8_t stage0[STAGE], stage1[STAGE];
-    __shared__ int segs[FORM == kAdapter ? TM + 1 : 1]; // lists of the tile's rows, their number
-    __shared__ int tile_list[FORM == kAdapter ? TM : 1];
 
     const int tid = (int)threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -634,22 +743,25 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
         return;
     }
 
-    int64_t chunks = (kdim + KS - 1) / KS;
-    const int64_t main_chunks = chunks;
-    const int per_seg = FORM == kAdapter ? (p.width + KS - 1) / KS : 1;
-    if constexpr (FORM == kAdapter) {
-        find_lists<TM, THREADS>(p, tile, tile_list, segs);
-        chunks += (int64_t)segs[TM] * per_seg;
-    }
+    const int64_t chunks = (kdim + KS - 1) / KS;
 
     f32x16 acc[WM][WN];
+    if constexpr (FORM == kAdapter) {
+        RowList lists[WM];
 #pragma unroll
-    for (int i = 0; i < WM; ++i)
+        for (int i = 0; i < WM; ++i)
+            lists[i].load(p, tile.p0 + (wm * WM + i) * 32 + (lane & 31), tile.p1);
+        adapter_sums<T, 0, PAIR, TINY>(p, tile.p0 + wm * WM * 32, n0 + wn * WN * 32, lists, nullptr,
+                                       acc);
+    } else {
 #pragma unroll
-        for (int j = 0; j < WN; ++j)
+        for (int i = 0; i < WM; ++i)
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-                acc[i][j][q] = 0.f;
+            for (int j = 0; j < WN; ++j)
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    acc[i][j][q] = 0.f;
+    }
 
     // pieces of eight values, a thread's own of both operands
     constexpr int QA = PA::LINES * PA::BLOCKS / THREADS, QB = PB::LINES * PB::BLOCKS / THREADS;
@@ -687,12 +799,6 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
         Eight<T, ODD> a[QA], b[QB];
         int64_t at[FORM == kGradient ? QB : 1]; // kGradient: where b's pieces come from
         int count[FORM == kGradient ? QB : 1];
-    };
-    // of an adapter's chunk: its list and where it begins
-    auto extra_of = [&](int64_t c, int &seg, int &k0) {
-        const int x = (int)(c - main_chunks);
-        seg = segs[x / per_seg];
-        k0 = x % per_seg * KS;
     };
     // Where a piece of a chunk begins in its array, and how many of its values there are:
     // the first chunk's place, and the same step for all pieces.
@@ -738,37 +844,10 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
         else
             return {first_b[j] + c * step_b, line < left ? p.n - n0 - value : 0};
     };
-    auto extra_a = [&](int seg, int k0, int j) -> Part {
-        const int piece = j * THREADS + tid, row = piece / PA::BLOCKS;
-        const int at = k0 + piece % PA::BLOCKS * 8;
-        const bool mine = tile_list[row] == seg;
-        return {(tile.p0 + (mine ? row : 0)) * p.width + at, mine ? p.width - at : 0};
-    };
-    auto extra_b = [&](int seg, int k0, int j) -> Part {
-        const int piece = j * THREADS + tid, row = n0 + piece / PB::BLOCKS;
-        const int at = k0 + piece % PB::BLOCKS * 8;
-        const int col = at < p.rp ? at : at - p.rp; // the low parts meet the same values
-        return {((int64_t)seg * p.n + min(row, p.n - 1)) * p.r + col,
-                row < p.n && at < p.width ? p.r - col : 0};
-    };
     const int64_t all_a = F::A_ALONG ? p.arows * p.kdim : p.rows * p.m;
     const int64_t all_b = FORM == kGradient ? p.arows * p.n
                                             : (FORM == kAdapter ? 1 : (int64_t)p.nlist) * p.n * p.kdim;
-    const int64_t all_hidden = p.rows * p.width, all_up = (int64_t)p.nlist * p.n * p.r;
     auto load = [&](Chunk &to, int64_t c) {
-        if (FORM == kAdapter && c >= main_chunks) {
-            int seg, k0;
-            extra_of(c, seg, k0);
-#pragma unroll
-            for (int j = 0; j < QA; ++j)
-                to.a[j].template read_near<TINY>(static_cast<const T *>(p.hidden),
-                                                 extra_a(seg, k0, j).at, all_hidden);
-#pragma unroll
-            for (int j = 0; j < QB; ++j)
-                to.b[j].template read_near<TINY>(static_cast<const T *>(p.up),
-                                                 extra_b(seg, k0, j).at, all_up);
-            return;
-        }
 #pragma unroll
         for (int j = 0; j < QA; ++j)
             to.a[j].template read_near<TINY>(a, part_a(c, j).at, all_a);
@@ -784,7 +863,7 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
                 to.count[j] = there ? p.n - n0 - piece % PB::BLOCKS * 8 : 0;
                 to.b[j].template read_near<TINY>(b, to.at[j], all_b);
             }
-            load_slots(min(c + 1, main_chunks - 1));
+            load_slots(min(c + 1, chunks - 1));
         } else {
 #pragma unroll
             for (int j = 0; j < QB; ++j)
@@ -799,37 +878,22 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
 #pragma unroll
         for (int j = 0; j < QB; ++j)
             from.b[j].ready();
-        if (FORM == kAdapter && c >= main_chunks && !none) {
-            int seg, k0;
-            extra_of(c, seg, k0);
+        if (last || edge_a || TINY) {
 #pragma unroll
             for (int j = 0; j < QA; ++j) {
-                const Part q = extra_a(seg, k0, j);
-                from.a[j].template settle<TINY>(q.at, all_hidden, q.count);
+                const Part q = part_a(c, j);
+                from.a[j].template settle<TINY>(q.at, all_a, q.count);
             }
+        }
+        if (last || edge_b || TINY) {
 #pragma unroll
             for (int j = 0; j < QB; ++j) {
-                const Part q = extra_b(seg, k0, j);
-                from.b[j].template settle<TINY>(q.at, all_up, q.count);
-            }
-        } else {
-            if (last || edge_a || TINY) {
-#pragma unroll
-                for (int j = 0; j < QA; ++j) {
-                    const Part q = part_a(c, j);
-                    from.a[j].template settle<TINY>(q.at, all_a, q.count);
-                }
-            }
-            if (last || edge_b || TINY) {
-#pragma unroll
-                for (int j = 0; j < QB; ++j) {
-                    Part q;
-                    if constexpr (FORM == kGradient)
-                        q = {from.at[j], none ? 0 : from.count[j]};
-                    else
-                        q = part_b(c, j);
-                    from.b[j].template settle<TINY>(q.at, all_b, q.count);
-                }
+                Part q;
+                if constexpr (FORM == kGradient)
+                    q = {from.at[j], none ? 0 : from.count[j]};
+                else
+                    q = part_b(c, j);
+                from.b[j].template settle<TINY>(q.at, all_b, q.count);
             }
         }
 #pragma unroll
@@ -855,7 +919,7 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
     // stretch without a branch, in which the compiler lays them side by side.
     auto plain = [&](int64_t c) {
         const int64_t k1 = (c + 1) * KS;
-        bool fits = !TINY && c < main_chunks && k1 <= kdim;
+        bool fits = !TINY && k1 <= kdim;
         if constexpr (!F::A_ALONG)
             fits = fits && (tile.p0 + k1 - 1) * p.m + m0 + TM <= all_a;
         if constexpr (FORM == kGradient)
@@ -948,9 +1012,6 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
             step(std::false_type{}, x, c + 1, stage1, stage0);
         }
     }
-    if constexpr (FORM == kAdapter)
-        keep_lists_apart<T, PAIR, TINY>(p, tile, tile.p0 + wm * WM * 32, n0 + wn * WN * 32,
-                                        tile_list + wm * WM * 32, segs, segs[TM], acc);
 
     const int r = lane & 31, half = lane >> 5;
     const int64_t matrix = FORM == kGradient ? (int64_t)split * p.nlist + tile.e : 0;
@@ -1003,20 +1064,6 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
 // tiles of 16-bit operands copied from memory into LDS without registers
 // ---------------------------------------------------------------------------
 
-// Offset of a copy that reads nothing: past any range (ranges are below 2^31 bytes).
-constexpr uint32_t kNowhere = 0x80000000u;
-
-// A memory range of less than 2^31 bytes from byte `from` on.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t range_of(const void *base, int64_t from,
-                                                           int64_t bytes)
-{
-    from = uniform(from);
-    const int64_t left = min(max(bytes - from, (int64_t)0), (int64_t)0x7FFFFFFF);
-    const uint8_t *p = static_cast<const uint8_t *>(base) + from;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (int)uniform(left),
-                                             0x00027000);
-}
-
 // Which tile a workgroup forms: groups of `high` by `wide` tiles go to the XCDs in turn
 // (every eighth workgroup runs on the same one), m first inside a group, so that the
 // tiles that an XCD's 32 CUs form together share operands in its cache, and numbers
@@ -1056,8 +1103,6 @@ void list_copy_kernel(ListJob p, TileGroups groups)
     // another
     __shared__ __align__(16) uint8_t stage0[STAGE], stage1[STAGE];
     __shared__ __align__(16) uint8_t stage2[STAGES > 2 ? STAGE : 16], stage3[STAGES > 3 ? STAGE : 16];
-    __shared__ int segs[FORM == kAdapter ? TM + 1 : 1];
-    __shared__ int tile_list[FORM == kAdapter ? TM : 1];
 
     const int tid = (int)threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1095,9 +1140,13 @@ void list_copy_kernel(ListJob p, TileGroups groups)
     }
     const int64_t kdim = !listed ? 0 : FORM == kGradient ? max(tile.p1 - tile.p0, (int64_t)0)
                                                          : (int64_t)p.kdim;
-    int chunks = (int)((kdim + KS - 1) / KS); // a list has fewer than 2^31 rows
-    const int main_chunks = chunks;
-    const int per_seg = FORM == kAdapter ? (p.width + KS - 1) / KS : 1;
+    const int chunks = (int)((kdim + KS - 1) / KS); // a list has fewer than 2^31 rows
+    RowList lists[WM]; // under way before the first copies
+    if constexpr (FORM == kAdapter) {
+#pragma unroll
+        for (int i = 0; i < WM; ++i)
+            lists[i].load(p, tile.p0 + (wm * WM + i) * 32 + (lane & 31), tile.p1);
+    }
 
     // copies: instruction j of a wave brings 1 KB of consecutive LDS lines, a lane 16 bytes
     constexpr int CA = PA::PLANE / 1024 / WAVES, CB = PB::PLANE / 1024 / WAVES;
@@ -1161,74 +1210,6 @@ void list_copy_kernel(ListJob p, TileGroups groups)
         }
     };
 
-    // kAdapter: where a chunk's copies read, set up once a chunk (`prepare`) and for most
-    // chunks only a step along the rows, so that no copy has a branch of its own (256
-    // rows of 4096 x 4096: 33 us with one, 20 without).
-    struct Range {
-        const uint8_t *base;
-        int bytes;
-        __device__ __forceinline__ __amdgpu_buffer_rsrc_t range() const
-        {
-            return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, bytes,
-                                                     0x00027000);
-        }
-    };
-    auto part_of = [&](const void *base, int64_t first, int64_t bytes) {
-        first = uniform(first);
-        return Range{static_cast<const uint8_t *>(base) + first,
-                     (int)uniform(min(max(bytes - first, (int64_t)0), (int64_t)0x7FFFFFFF))};
-    };
-    struct {
-        Range a, b;
-        int along;
-    } from{};
-    uint32_t va[FORM == kAdapter ? CA : 1], vb[FORM == kAdapter ? CB : 1];
-    if constexpr (FORM == kAdapter) {
-        from.a = part_of(p.a, tile.p0 * lda * 2, abytes);
-        from.b = part_of(p.b, (int64_t)n0 * ldb * 2, bbytes);
-#pragma unroll
-        for (int j = 0; j < CA; ++j)
-            va[j] = offa[j];
-#pragma unroll
-        for (int j = 0; j < CB; ++j)
-            vb[j] = offb[j];
-    }
-    const int whole_chunks = (int)(kdim / KS);
-    auto prepare = [&](int c) {
-        if constexpr (FORM == kAdapter) {
-            from.along = c < main_chunks ? c * KS * 2 : 0;
-            if (c < whole_chunks)
-                return;
-            const int left = c < main_chunks ? (int)(kdim - (int64_t)c * KS) : 0;
-            if (c < main_chunks || c >= chunks) { // the rows' end; nothing
-#pragma unroll
-                for (int j = 0; j < CA; ++j)
-                    va[j] = block_a(j) * 8 < left ? offa[j] : kNowhere;
-#pragma unroll
-                for (int j = 0; j < CB; ++j)
-                    vb[j] = block_b(j) * 8 < left ? offb[j] : kNowhere;
-                return;
-            }
-            const int x = c - main_chunks, nth = x / per_seg;
-            const int seg = __builtin_amdgcn_readfirstlane(segs[nth]);
-            const int k0 = (x - nth * per_seg) * KS;
-            from.a = part_of(p.hidden, tile.p0 * p.width * 2, p.rows * p.width * 2);
-            from.b = part_of(p.up, ((int64_t)seg * p.n + n0) * p.r * 2,
-                             (int64_t)p.nlist * p.n * p.r * 2);
-#pragma unroll
-            for (int j = 0; j < CA; ++j) {
-                const int at = k0 + block_a(j) * 8;
-                const bool mine = tile_list[line_a(j)] == seg && at < p.width;
-                va[j] = mine ? (line_a(j) * p.width + at) * 2 : kNowhere;
-            }
-#pragma unroll
-            for (int j = 0; j < CB; ++j) { // the low parts meet the same values
-                const int at = k0 + block_b(j) * 8, col = at < p.rp ? at : at - p.rp;
-                vb[j] = at < p.width ? (line_b(j) * p.r + col) * 2 : kNowhere;
-            }
-        }
-    };
-
     // Copy q of chunk c (A's copies, then B's) into the chunk's LDS place.  Past the last
     // chunk nothing is read, and the place cleared: so the number of copies under way
     // is known.
@@ -1236,11 +1217,6 @@ void list_copy_kernel(ListJob p, TileGroups groups)
         const bool of_a = q < CA;
         const int j = of_a ? q : q - CA;
         to += of_a ? (wave * CA + j) * 1024 : PA::PLANE + (wave * CB + j) * 1024;
-        if constexpr (FORM == kAdapter) {
-            copy16_to_lds(of_a ? from.a.range() : from.b.range(), of_a ? va[j] : vb[j], from.along,
-                          to);
-            return;
-        }
         const int64_t k0 = (int64_t)c * KS;
         const int left = (int)min(kdim - k0, (int64_t)KS); // values in the chunk
         // The range check of a copy subtracts the scalar offset from the range's bytes, so
@@ -1279,19 +1255,10 @@ void list_copy_kernel(ListJob p, TileGroups groups)
     constexpr std::integral_constant<int, 2> i2{};
     constexpr std::integral_constant<int, 3> i3{};
 
-    // the rows' lists are looked up while the first chunks are under way, if those are whole
-    const bool lists_first = FORM == kAdapter && whole_chunks < STAGES - 1;
-    auto add_lists = [&] {
-        find_lists<TM, THREADS>(p, tile, tile_list, segs);
-        chunks += segs[TM] * per_seg;
-    };
-    if (lists_first)
-        add_lists();
     load_slots(0);
     place_slots(0);
     load_slots(1);
     auto fetch_all = [&](int c, uint8_t *to) {
-        prepare(c);
 #pragma unroll
         for (int q = 0; q < CA + CB; ++q)
             fetch(c, to, q);
@@ -1301,17 +1268,24 @@ void list_copy_kernel(ListJob p, TileGroups groups)
         fetch_all(1, place(i1));
     if constexpr (STAGES > 3)
         fetch_all(2, place(i2));
-    if (FORM == kAdapter && !lists_first)
-        add_lists();
 
     f32x16 acc[WM][WN];
+    if constexpr (FORM == kAdapter) {
+        // LDS: the last stage, whose first copies come after the next barrier
+        constexpr int SLAB = STAGE / WAVES / 1024 * 1024;
+        adapter_sums<T, SLAB, PAIR, false>(p, tile.p0 + wm * WM * 32, n0 + wn * WN * 32, lists,
+                                           place(std::integral_constant<int, STAGES - 1>{}) +
+                                               wave * SLAB,
+                                           acc);
+    } else {
 #pragma unroll
-    for (int i = 0; i < WM; ++i)
+        for (int i = 0; i < WM; ++i)
 #pragma unroll
-        for (int j = 0; j < WN; ++j)
+            for (int j = 0; j < WN; ++j)
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-                acc[i][j][q] = 0.f;
+                for (int q = 0; q < 16; ++q)
+                    acc[i][j][q] = 0.f;
+    }
     Reader<F::A_ALONG, TM, KS, WM, false> reada;
     Reader<F::B_ALONG, TN, KS, WN, PAIR> readb;
     reada.init(wm * WM * 32);
@@ -1348,7 +1322,6 @@ void list_copy_kernel(ListJob p, TileGroups groups)
         const uint8_t *now = place(i);
         uint8_t *ahead = place(std::integral_constant<int, I + STAGES - 1>{});
         place_slots(c + 1);
-        prepare(c + STAGES - 1);
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
             if (s == PARTS)
@@ -1391,9 +1364,6 @@ void list_copy_kernel(ListJob p, TileGroups groups)
         }
     }
     wait_vm<0>(); // no copy is under way to where results may go, or past the end
-    if constexpr (FORM == kAdapter)
-        keep_lists_apart<T, PAIR, false>(p, tile, tile.p0 + wm * WM * 32, n0 + wn * WN * 32,
-                                         tile_list + wm * WM * 32, segs, segs[TM], acc);
 
     if constexpr (FORM == kHidden) {
         static_assert(!PAIR, "hidden rows");

@@ -48,6 +48,14 @@ __device__ __forceinline__ void wait_vm()
     __asm__ volatile("" ::: "memory");
 }
 
+// Until this wave's LDS operations are done, as before a copy to where it read.
+__device__ __forceinline__ void wait_lds()
+{
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __asm__ volatile("" ::: "memory");
+}
+
 // Row of a second operand's 32 that operand row r of a 32 x 32 sum holds, when
 // that operand goes first into the matrix instruction.  A lane's results i = 4 a
 // + c are operand rows 8 a + 4 half + c; PAIR makes them rows 16 (a / 2) + 8 half

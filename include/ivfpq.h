@@ -578,9 +578,9 @@ size_t ivfpq_adapter_product_bytes(int64_t t, int r);
  * scales_dev [nlist] float32 (NULL: 1).  offsets_dev, order_dev [t] and pos_dev [t]
  * are those of one ivfpq_route_sort_ex of the rows' lists (k = 1), made once for
  * all products of the same rows; a row whose list is masked gets W x.  D_a x times
- * the scale is held in float32, for 16-bit types in two parts (binary16: below
- * 65504); an infinity in D_a x or U_a gives infinities or NaN, in the rows of list a
- * alone.  t = 0 is a no-op.  Its gradients come from ivfpq_list_product_ex and
+ * the scale is a float32 value, in 16-bit types too, and is multiplied as a factor of
+ * float32 products is, with their limits; an infinity in D_a x or U_a gives infinities
+ * or NaN, in the rows of list a alone.  t = 0 is a no-op.  Its gradients come from ivfpq_list_product_ex and
  * ivfpq_list_product_grad_ex of the sorted rows.  Errors as above, with r in [1,
  * 2^12]. */
 ivfpq_status ivfpq_adapter_product_ex(const void *rows_dev, int type, int64_t t, int d,

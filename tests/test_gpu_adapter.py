@@ -210,6 +210,45 @@ def test_bad_values_change_no_other_rounding(t, n, d, nlist, r, dtype):
     assert not got[0, n // 2].isfinite() and not got[[1, 3, t - 1]].isfinite().any()
 
 
+# the power of two of the hidden rows; up matrices have the one that makes it 2^-10, or 2^-20
+POWERS = {torch.float32: (-90, -24, 0, 14, 90), torch.bfloat16: (-90, -24, 0, 14, 90),
+          torch.float16: (-34, -24, 0, 14)}
+
+
+@pytest.mark.parametrize("t,n,d,nlist,r", TILES)
+@pytest.mark.parametrize("dtype,power", [(t, p) for t in TYPES for p in POWERS[t]])
+def test_hidden_rows_are_held_to_the_last_bit(t, n, d, nlist, r, dtype, power):
+    """Hidden values of 21 bits at any power of two, which the shared product cancels for the
+    rows of list 0: columns of x hold the bits, rows of down their signs, a row of up one
+    entry.  Every term is a multiple of `unit` and all of a result's are below 2^24 units
+    together, so that a float32 sum of them is exact in any order."""
+    rng = np.random.default_rng(t + r)
+    bits, unit = 22, 2.0 ** (-20 if power == -34 else -10)
+    x = torch.zeros((t, d))
+    x[:, :bits] = torch.from_numpy(rng.integers(0, 2, (t, bits)) * 2.0 ** (np.arange(bits) % 11))
+    x[:, bits:] = torch.from_numpy(rng.integers(-3, 4, (t, d - bits)).astype(np.float32))
+    down = torch.zeros((nlist, r, d))
+    down[:, :, :bits] = torch.from_numpy(rng.choice([-1.0, 1.0], (nlist, r, bits)) *
+                                         2.0 ** (np.arange(bits) // 11 * 10))
+    up = torch.zeros((nlist, n, r))
+    at = torch.from_numpy(rng.integers(0, r, (nlist, n, 1)))
+    up.scatter_(2, at, torch.from_numpy(rng.choice([-1.0, 1.0], (nlist, n, 1))).float())
+    w = -unit * (up[0] @ down[0])
+    w[:, 0] += unit
+    up *= unit * 2.0 ** -power
+    scales = torch.full((nlist,), 2.0 ** power, device="cuda")
+    lists = rng.integers(-1, nlist, t).astype(np.int32)
+    lists[::3] = 0
+    args = [a.to(dtype).cuda() for a in (x, w, down, up)]
+    for a, b in zip(args, (x, w, down, up)):
+        assert torch.equal(a.cpu().float(), b)
+    y = call(*args, lists, scales)
+    want, mag = adapter64(*(np64(a) for a in args), lists, np64(scales))
+    assert mag.max() < 2 ** 24 * unit
+    assert np.array_equal(want[::3], unit * np64(x)[::3, :1] * np.ones((1, n)))
+    assert np.array_equal(np64(y), rounded(want, dtype))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_rows_that_are_not_finite_cost_no_second_product(dtype):
     """A NaN in every row of x (a value that overflowed) takes the time of a clean batch;
