@@ -92,7 +92,9 @@ class Adapted(torch.autograd.Function):
         listed = torch.bucketize(torch.arange(len(x), dtype=torch.int32, device=x.device),
                                  offsets[:-1], right=True) - 1
         factor = scales[listed.clamp(0, nlist - 1)]       # of the sorted rows; others are zero
-        rows = A.ivfpq_route_gather_ex(grad, order, 1) * factor[:, None]
+        # as the rows' weights, so that the product is float32 and rounded once to their type
+        weights = factor[pos.clamp(min=0).view(-1).long()]
+        rows = A.ivfpq_route_gather_ex(grad, order, 1, weights=weights[:, None])
         hidden = A.ivfpq_list_product_ex(x, down, offsets, order=order)
         grad_hidden = A.ivfpq_list_product_ex(rows, up, offsets, transposed=True)
         grad_rows = A.ivfpq_list_product_ex(grad_hidden, down, offsets, transposed=True)

@@ -267,3 +267,30 @@ def test_threads_with_streams_of_their_own():
     for th in threads:
         th.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gradients_of_adapters_in_every_type(dtype):
+    """Small integers and powers of two, sums that 8 bits hold, so that every type's
+    gradients are exact, rounded once."""
+    rng = np.random.default_rng(21)
+    t, n, d, nlist, r = 90, 20, 12, 4, 2
+    small = lambda *s: torch.from_numpy(  # noqa: E731
+        rng.integers(-1, 2, s).astype(np.float32)).to(dtype).cuda()
+    x, down, up = (p.requires_grad_() for p in (small(t, d), small(nlist, r, d), small(nlist, n, r)))
+    w, dy = small(n, d), small(t, n)
+    scales = torch.tensor([1, 0.5, 2, -1], device="cuda")
+    lists = torch.from_numpy(rng.integers(-1, nlist, t).astype(np.int32)).cuda()
+    y = E.Adapted.apply(x, w, down, up, scales,
+                        *A.ivfpq_route_sort_ex(lists.view(-1, 1), nlist))
+    y.backward(dy)
+    ref = [p.detach().double().cpu().requires_grad_() for p in (x, down, up)]
+    e = lists.long().cpu()
+    per = torch.stack([s * (ref[0] @ a.t()) @ b.t()
+                       for a, b, s in zip(ref[1], ref[2], scales.double().cpu())], 1)
+    want = ref[0] @ w.double().cpu().t() + torch.where(
+        (e >= 0)[:, None], per[torch.arange(t), e.clamp(min=0)], 0.0)
+    want.backward(dy.double().cpu())
+    assert torch.equal(y.detach().cpu(), want.detach().to(dtype))
+    for got, p in zip((x, down, up), ref):
+        assert got.grad.dtype == dtype and torch.equal(got.grad.cpu(), p.grad.to(dtype))
