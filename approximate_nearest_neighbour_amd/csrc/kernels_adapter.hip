@@ -76,10 +76,11 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
     // Few rows: blocks whose waves share the contraction, the largest that still make a
     // workgroup a CU.  16 rows of 4096 x 4096: 24 us in 16 x 16 blocks, 29 in 32 x 32, 35 in
     // copied 32 x 128 tiles; 64 rows: 53, 34 and 37; 128: 87, 51 and 35; 32 rows of 11,008 x
-    // 4096: 72, 56 and 69.  Where the copies do not fit, up to two workgroups a CU: 128
-    // rows of 2048 x 2048 in float32 38 us, in 64 x 64 tiles 52; 256 rows: 56 and 52.
+    // 4096: 72, 56 and 69.  Where the copies do not fit: 128 rows of 2048 x 2048 in float32
+    // (256 blocks of 32 x 32) 38 us, in 64 x 64 tiles 52; 192 rows 55 and 52; binary16, rank
+    // 7, 256 rows of 1001 x 777 (256 blocks) 21.6 and 24.0, 301 rows 29.4 and 24.3.
     const int64_t blocks = count_tiles<kAdapter>(p, 32, 32);
-    if (!any_tiny<kAdapter>(p) && (p.rows <= 32 || blocks <= (copies ? 256 : 512))) {
+    if (!any_tiny<kAdapter>(p) && (p.rows <= 32 || blocks <= 256)) {
         if (p.rows <= 16 || count_tiles<kAdapter>(p, 16, 16) <= 256)
             return launch_direct<T, kAdapter, 1, 1, 8, 2>(p, stream);
         if (count_tiles<kAdapter>(p, 32, 16) <= 256)
