@@ -179,8 +179,10 @@ struct Reader {
 // Eight values of a line in registers.  ODD: 16-bit values whose place may not be a
 // multiple of four bytes, where loads of 16 bytes take twice as long: the aligned four
 // bytes that hold them are read (which end in the same four bytes as the values do)
-// and shifted together when they have arrived (`ready`).  Adapters of rank 7 for 301
-// rows through 1001 x 777: 51 us before, 34 so.
+// and shifted together when they have arrived (`ready`).  The blocks of few rows take
+// it, which wait for their loads (128 rows of 2001 x 2001 with adapters of rank 16: 48 us
+// without, 31 so); the tiles through registers do not, as theirs are two chunks ahead (16,384
+// rows of 16 lists of 1501 x 1001: 130 us, so 153).
 template <typename T, bool ODD = false>
 struct Eight {
     static_assert(!ODD || sizeof(T) == 2, "four-byte values are aligned");
@@ -517,7 +519,7 @@ __device__ __forceinline__ void adapter_sums(const ListJob &p, int64_t p0, int n
     // values of an up matrix's rows brought together, hidden values loaded together
     constexpr int UPS = !COPY ? 16 : SLAB >= WN * 32 * 128 ? 64 : 32, STEPS = COPY ? 2 : 1;
     constexpr int GROUPS = UPS / 16 / STEPS, AHEAD = WM * WN < 8 ? GROUPS : 1; // registers
-    using Up = Eight<T, !COPY && sizeof(T) == 2>;
+    using Up = Eight<T>;
     using Place = HiddenPlace<T>;
     const int lane = lane_id(), r = lane & 31, half = lane >> 5;
     const int64_t all_up = (int64_t)p.nlist * p.n * p.r;
@@ -554,11 +556,9 @@ __device__ __forceinline__ void adapter_sums(const ListJob &p, int64_t p0, int n
             wait_vm<0>();
         } else {
 #pragma unroll
-            for (int j = 0; j < WN; ++j) {
-                u[j].ready();
+            for (int j = 0; j < WN; ++j)
                 u[j].template settle<TINY>(up_at(seg, j, u0 + half * 8), all_up,
                                            p.r - u0 - half * 8);
-            }
         }
     };
     // block i's hidden rows; past the last block, whose results are dropped, that one's
@@ -794,9 +794,8 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
     const bool edge_b = FORM == kGradient || n0 + TN > p.n;
 
     // A chunk on its way: read at once, settled (ends, missing lines) when it goes to LDS.
-    constexpr bool ODD = sizeof(T) == 2; // aligned 16-bit operands take the copies below
     struct Chunk {
-        Eight<T, ODD> a[QA], b[QB];
+        Eight<T> a[QA], b[QB];
         int64_t at[FORM == kGradient ? QB : 1]; // kGradient: where b's pieces come from
         int count[FORM == kGradient ? QB : 1];
     };
@@ -872,12 +871,6 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
     };
     auto store = [&](Chunk &from, int64_t c, uint8_t *to) {
         const bool none = c >= chunks, last = (c + 1) * KS > kdim;
-#pragma unroll
-        for (int j = 0; j < QA; ++j)
-            from.a[j].ready();
-#pragma unroll
-        for (int j = 0; j < QB; ++j)
-            from.b[j].ready();
         if (last || edge_a || TINY) {
 #pragma unroll
             for (int j = 0; j < QA; ++j) {
@@ -932,7 +925,6 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
 #pragma unroll
         for (int j = 0; j < QA; ++j) {
             const int piece = j * THREADS + tid;
-            from.a[j].ready();
             if constexpr (F::PER_LIST_ROWS)
                 from.a[j].keep(arow[j] >= 0);
             from.a[j].store(to + PA::at(piece / PA::BLOCKS, piece % PA::BLOCKS), PA::PLANE);
@@ -940,7 +932,6 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
 #pragma unroll
         for (int j = 0; j < QB; ++j) {
             const int piece = j * THREADS + tid;
-            from.b[j].ready();
             if constexpr (FORM == kGradient)
                 from.b[j].keep(from.count[j] > 0);
             from.b[j].store(to + NP * PA::PLANE + PB::at(piece / PB::BLOCKS, piece % PB::BLOCKS),
