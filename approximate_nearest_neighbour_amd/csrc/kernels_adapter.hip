@@ -77,8 +77,8 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
     // workgroup a CU.  16 rows of 4096 x 4096: 24 us in 16 x 16 blocks, 29 in 32 x 32, 35 in
     // copied 32 x 128 tiles; 64 rows: 53, 34 and 37; 128: 87, 51 and 35; 32 rows of 11,008 x
     // 4096: 72, 56 and 69.  Where the copies do not fit: 128 rows of 2048 x 2048 in float32
-    // (256 blocks of 32 x 32) 38 us, in 64 x 64 tiles 52; 192 rows 55 and 52; binary16, rank
-    // 7, 256 rows of 1001 x 777 (256 blocks) 21.6 and 24.0, 301 rows 29.4 and 24.3.
+    // (256 blocks of 32 x 32) 39 us, in 64 x 64 tiles 53; 192 rows 57 and 53; binary16, rank
+    // 7, 256 rows of 1001 x 777 (256 blocks) 21.8 and 21.3, 301 rows 29.4 and 21.4.
     const int64_t blocks = count_tiles<kAdapter>(p, 32, 32);
     if (!any_tiny<kAdapter>(p) && (p.rows <= 32 || blocks <= 256)) {
         if (p.rows <= 16 || count_tiles<kAdapter>(p, 16, 16) <= 256)
@@ -100,9 +100,9 @@ static hipError_t adapter_as(const AdapterProduct &q, hipStream_t stream)
         }
     }
     // In float32 tiles of 64 x 64 or 128 x 128: 2048 x 2048, 1024 rows (128 of the larger)
-    // 79 us and 102, 2048 rows (256) 136 and 122.  In 16 bits of 64 x 64, or of 64 x 128 by
+    // 77 us and 98, 2048 rows (256) 131 and 114.  In 16 bits of 64 x 64, or of 64 x 128 by
     // eight waves where those would take more than a turn of two a CU: 2001 x 2001, 512 rows
-    // (256 of the smaller) 36 us and 39, 2048 rows 75 and 60, 4096 137 and 109.
+    // (256 of the smaller) 30 us and 35, 2048 rows 65 and 55, 4096 116 and 96.
     if constexpr (sizeof(T) == 4) {
         if (middle > 192)
             return launch_tiles<T, T, kAdapter, KS, 2, 2, 2, 2>(p, stream);

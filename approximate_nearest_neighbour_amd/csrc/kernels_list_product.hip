@@ -22,21 +22,24 @@ static hipError_t rows_as(const ListJob &p, hipStream_t stream)
     }
     if constexpr (FORM == kRowsAlong) {
         // Few 16 x 32 tiles: their waves share the contraction.  float32, one list of 128
-        // rows, 1024 x 1024 (272 tiles): 15 us, in 64 x 64 tiles 22; 64 lists of 4 rows
-        // (1536): 80 and 67.
-        if (count_tiles<FORM>(p, 16, 32) <= 400 && !any_tiny<FORM>(p))
+        // rows, 1024 x 1024 (256 tiles): 14 us, in 64 x 64 tiles 21; 8 lists of 2 rows, 2049
+        // x 2049 (325): 41 and 57; 64 lists of 4 rows, 1024 x 1024 (1536): 80 and 57.
+        // bfloat16, one list of 1025 x 1025, 64 rows (132): 10 and 12; 128 rows (264): 17
+        // and 12.
+        if (count_tiles<FORM>(p, 16, 32) <= (sizeof(T) == 4 ? 400 : 256) && !any_tiny<FORM>(p))
             return launch_direct<T, kRowsAlong, 1, 1, 4, 2>(p, stream);
     }
     constexpr int KS = sizeof(T) == 4 ? 16 : 32;
     // Larger tiles where lists fill them and there are enough.  float32, 64 lists of
-    // 1024 x 1024, 64 rows each: 114 us in 64 x 64 tiles, 124 in 128 x 128; 512: 594 and
-    // 476.  8 lists of 1025 x 1025, bfloat16, 512 rows each (324 tiles): 58 and 58; 2048: 169
-    // and 148.
+    // 1024 x 1024, 64 rows each: 109 us in 64 x 64 tiles, 117 in 128 x 128; 512: 482 and
+    // 381.  8 lists of 1025 x 1025, bfloat16, 512 rows each (324 tiles): 49 and 46; 2048: 139
+    // and 117.
     if (p.rows > 64 * p.nlist && count_tiles<FORM>(p, 128, 128) > 512)
         return launch_tiles<T, T, FORM, KS, 2, 2, 2, 2>(p, stream);
     // 64 x 64 tiles, two a CU; in 16 bits 64 x 128 by eight waves where those would take a
-    // second turn.  Both ways through 16 lists of 1281 x 1281, 128 rows each: 119 us and
-    // 99; 8 lists of 1025 x 1025, 64 rows each (204 tiles): 37 and 39.
+    // second turn (of which two fit a CU as well).  Both ways through 16 lists of 1281 x 1281,
+    // 128 rows each: 98 us and 81; 8 lists of 1025 x 1025, 64 rows each (204 tiles): 26 and
+    // 31.
     if constexpr (sizeof(T) == 2)
         if (count_tiles<FORM>(p, 64, 64) > 512)
             return launch_tiles<T, T, FORM, 2 * KS, 1, 1, 2, 4>(p, stream);
@@ -80,9 +83,9 @@ static hipError_t gradient_as(const ListJob &p, int size, hipStream_t stream)
                                : launch_copies<T, TO, kGradient, 64, 2, 2, 2, 2, 2>(p, stream);
     }
     // 64 x 64 tiles where larger ones leave CUs empty, float32 up to one tile a CU, 16-bit
-    // up to two: 256 rows a list, float32, 8 lists of 512 x 512 (128 tiles): 19 us in 64 x
-    // 64, 26 in 128 x 128; 16 lists (256): 34 and 30; bfloat16, 16 lists of 513 x 513
-    // (400): 25 and 25; 16 of 1025 x 1025 (1296): 64 and 59.
+    // up to two: 256 rows a list, float32, 8 lists of 512 x 512 (128 tiles): 16 us in 64 x
+    // 64, 22 in 128 x 128; 16 lists (256): 26 and 24; bfloat16, 16 lists of 513 x 513
+    // (400): 22 and 21; 16 of 1025 x 1025 (1296): 51 and 48.
     return count_tiles<kGradient>(p, 128, 128) * p.splits > (sizeof(T) == 4 ? 192 : 512)
                ? launch_tiles<T, TO, kGradient, KS, 2, 2, 2, 2>(p, stream)
                : launch_tiles<T, TO, kGradient, 32, 1, 1, 2, 2>(p, stream);

@@ -23,7 +23,8 @@
 // own: 512 x 512 results of 2048 random products are off by 7.0e-7 of their norm, the
 // library's float32 product by 8.1e-7.  Six bfloat16 instructions take 6 / 16 of the
 // time of the float32 one.  What rounds to an infinity in bfloat16 (magnitudes from
-// 255.5 2^120 on) becomes a NaN this way.
+// 255.5 2^120 on) becomes a NaN this way; below 2^-110 the third part is one of
+// bfloat16's numbers below the normal ones, which are multiples of 2^-133.
 #pragma once
 
 #include "list_plan.hpp"
@@ -694,7 +695,7 @@ __device__ __forceinline__ void adapter_sums(const ListJob &p, int64_t p0, int n
 // that the copies cannot read.  Bound by the matrix instructions, six a product, and the
 // split beside them in float32 (the gradient of 65,536 rows, 2048 x 2048: 3.5 ms, 158 TF,
 // the library's float32 product 153), by the loads' latency where tiles are few (1554 odd
-// rows of 16 lists of 1000 x 1501: 34 us, 1.1 a chunk).
+// rows of 16 lists of 1000 x 1501: 27 us, 16 chunks of two workgroups a CU).
 template <typename T, typename TO, int FORM, int KS, int WM, int WN, int MW, int NW, bool TINY>
 __global__ __launch_bounds__(64 * MW * NW, 2) void list_tile_kernel(ListJob p)
 {
