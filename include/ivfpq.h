@@ -529,9 +529,9 @@ ivfpq_status ivfpq_route_combine_grad_ex(const void *grad_dev, const void *rows_
  * overlaps no input.  Two calls that may run at the same time need a workspace
  * each.  Sums are float32, rounded once to the output's type.  float32 products
  * are formed from three bfloat16 parts of each factor, every one within 2^-23 of
- * itself; a factor whose magnitude is 255.5 2^120 or more, an infinity among them,
- * gives NaN there, in 16-bit types an infinity gives what float32 sums of its
- * products give. */
+ * itself; a factor below 2^-110 is first rounded to a multiple of 2^-133; one whose
+ * magnitude is 255.5 2^120 or more, an infinity among them, gives NaN there, in 16-bit
+ * types an infinity gives what float32 sums of its products give. */
 
 /* Rows sorted by list, each times its list's own matrix: matrices_dev holds nlist
  * matrices [n][d] (transposed 0) or [d][n] (not 0), offsets_dev [nlist + 1]
@@ -539,7 +539,8 @@ ivfpq_status ivfpq_route_combine_grad_ex(const void *grad_dev, const void *rows_
  * rows] count as the nearer end).  Output row p of list e is matrix e (transposed:
  * its transpose) times row order[p] / k of rows_dev [arows][d], or row p when
  * order_dev is NULL (then arows >= rows).  Rows of no list are zero; an entry of
- * order outside the rows stands for a row of zeros.  out_dev [rows][n] of `type`.
+ * order outside the rows stands for a row of zeros (which an infinity or NaN in the
+ * list's matrix may turn into NaN).  out_dev [rows][n] of `type`.
  * rows = 0 is a no-op.  The gradient of the sorted rows is the same call on the
  * outputs' gradient with the other `transposed`, n and d exchanged (then
  * ivfpq_route_combine_ex takes it to the vectors).  Errors: IVFPQ_E_INVALID_ARG (a
