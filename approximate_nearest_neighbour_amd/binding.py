@@ -821,8 +821,8 @@ def ivfpq_adapter_product_ex(x: torch.Tensor, w: torch.Tensor, down: torch.Tenso
 
 def ivfpq_table_lookup_ex(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out=None,
                           stream=None) -> torch.Tensor:
-    """scale * table[ids]: table [rows, d], ids int32 of any shape; zero where an id is
-    outside the table.  Returns [*ids.shape, d]."""
+    """scale * table[ids]: table [rows, d], ids int32 of any shape (of a search: ids.int());
+    zero where an id is outside the table.  Returns [*ids.shape, d]."""
     kind, (rows, d) = _rows(table)
     shape = _slots(ids, "ids")
     out = _out(out, (*shape, d), table.dtype, table.device, stream)
