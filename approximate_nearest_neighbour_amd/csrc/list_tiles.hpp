@@ -377,8 +377,9 @@ struct HiddenPlace {
         E *to = static_cast<E *>(hidden) + piece(t, at, rp) + (at & 7);
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) {
-            to[q * 512] = (E)h;
-            h -= (float)to[q * 512];
+            const E part = (E)h;
+            to[q * 512] = part;
+            h -= (float)part;
         }
     }
 };

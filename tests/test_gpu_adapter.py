@@ -276,3 +276,27 @@ def test_rows_that_are_not_finite_cost_no_second_product(dtype):
 
     clean_ms, bad_ms = least(x), least(bad)
     assert bad_ms < 4 * clean_ms
+
+
+# a size for each copied tile, 32 x 128 to 256 x 256, and for the tiles through registers
+BY_TILE = [((500, 521, 24), (24, 72, 136)), ((1700, 520, 24), (24, 72, 136)),
+           ((1300, 3001, 24), (24, 72, 136)), ((1800, 1032, 24), (24, 72, 136)),
+           ((800, 5000, 24), (24, 72, 136)), ((2700, 3000, 24), (24, 72, 136)),
+           ((600, 1001, 25), (3, 33, 70)), ((2100, 2001, 23), (3, 33, 70))]
+
+
+@pytest.mark.parametrize("t,n,d,r", [(*size, r) for size, ranks in BY_TILE for r in ranks])
+@pytest.mark.parametrize("kind", ["runs", "mixed"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_ranks_in_every_tile(t, n, d, r, kind, dtype):
+    """Ranks that end inside a step, a group of steps, or after several; one list in all
+    of a tile's rows, or more than 32 in it."""
+    rng = np.random.default_rng(t + r)
+    nlist = 3 if kind == "runs" else 40
+    x, w = integers(rng, t, d, dtype=dtype), integers(rng, n, d, dtype=dtype)
+    down = integers(rng, nlist, r, d, dtype=dtype, top=2)
+    up = integers(rng, nlist, n, r, dtype=dtype, top=2)
+    lists = lists_of(rng, t, nlist, kind)
+    want, mag = adapter64(np64(x), np64(w), np64(down), np64(up), lists, None)
+    assert mag.max() < 2 ** 24
+    assert np.array_equal(np64(call(x, w, down, up, lists, None)), rounded(want, dtype))

@@ -135,3 +135,24 @@ def test_the_highest_rank(t, dtype):
         mine = lists == e
         want[mine] += np64(x)[mine] @ np64(down[e]).T @ np64(up[e]).T
     assert np.array_equal(np64(y), np64(torch.from_numpy(want).to(dtype)))
+
+
+@pytest.mark.parametrize("t,d,r", [(20, 64, 64), (600, 64, 64), (600, 63, 63)])
+def test_up_matrices(t, d, r):
+    nlist, n = 1 << 16, 600                            # 2.5e9 elements
+    rng = np.random.default_rng(r)
+    up = torch.zeros((nlist, n, r), dtype=BF, device="cuda")
+    down = torch.zeros((nlist, r, d), dtype=BF, device="cuda")
+    used = [0, 1, nlist // 2, nlist - 2, nlist - 1]
+    up[used], down[used] = (integers(rng, 5, n, r, dtype=BF, top=1),
+                            integers(rng, 5, r, d, dtype=BF, top=1))
+    x, w = integers(rng, t, d, dtype=BF), integers(rng, n, d, dtype=BF)
+    pick = rng.integers(-1, 5, t)
+    lists = np.where(pick < 0, -1, np.array(used)[pick]).astype(np.int32)
+    y = A.ivfpq_adapter_product_ex(x, w, down, up, *A.ivfpq_route_sort_ex(
+        torch.from_numpy(lists[:, None]).cuda(), nlist))
+    want = np64(x) @ np64(w).T
+    for i, e in enumerate(used):
+        mine = pick == i
+        want[mine] += np64(x)[mine] @ np64(down[e]).T @ np64(up[e]).T
+    assert np.array_equal(np64(y), np64(torch.from_numpy(want).to(BF)))
